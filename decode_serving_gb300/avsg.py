@@ -79,6 +79,55 @@ class avsg_info(ctypes.Structure):
     ]
 
 
+AVSG_BF16 = 0
+AVSG_F16 = 1
+
+
+class avsg_pages(ctypes.Structure):
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("num_layers", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("d_k", ctypes.c_void_p),
+        ("d_v", ctypes.c_void_p),
+        ("d_tables", ctypes.c_void_p),
+        ("d_len", ctypes.c_void_p),
+        ("d_free", ctypes.c_void_p),
+        ("d_free_count", ctypes.c_void_p),
+        ("d_error", ctypes.c_void_p),
+    ]
+
+
+class avsg_rotary(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("rot_offset", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("q_f32", ctypes.c_int32),
+        ("tokens_per_request", ctypes.c_int32),
+        ("layer", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("magnitude", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+        ("d_q", ctypes.c_void_p),
+        ("d_k", ctypes.c_void_p),
+        ("d_v", ctypes.c_void_p),
+        ("d_freq", ctypes.c_void_p),
+        ("d_pos", ctypes.c_void_p),
+        ("d_slot", ctypes.c_void_p),
+        ("d_q_out", ctypes.c_void_p),
+    ]
+
+
 AVSG_NUM_KERNELS = 8
 
 
@@ -113,6 +162,10 @@ SIGNATURES = {
     "avsg_cuda_error": [_P],
     "avsg_attention_noalloc": [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P,
                                _P, _P, ctypes.c_float, _P],
+    "avsg_page_plan": [ctypes.POINTER(avsg_pages), _P, _P, _I32, _P, _P, _P, _P, _P],
+    "avsg_rotary_frequencies": [_I32] + [ctypes.c_double] * 5 + [_P],
+    "avsg_rotary_write": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_rotary), _P],
+    "avsg_tree_keep": [ctypes.POINTER(avsg_pages), _P, _P, _P, _P, _P, _P],
     "avsg_read_rows": [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, _I32, _P, _P],
 }
 
@@ -254,6 +307,34 @@ def avsg_read_rows(src, num_rows, row_bytes, d_idx, n, d_sink, ctas=0, stream=0)
     """Reads n rows at the given indices and discards them (a measurement aid)."""
     _check(load_library().avsg_read_rows(src, int(num_rows), int(row_bytes), d_idx, int(n),
                                          int(ctas), d_sink, stream or None), "avsg_read_rows")
+
+
+def avsg_page_plan(pages: avsg_pages, d_new, d_mask, capacity, d_first, d_slot, d_pos,
+                   d_free_count_out, stream=0) -> None:
+    _check(load_library().avsg_page_plan(pages, d_new, d_mask or None, capacity, d_first,
+                                         d_slot or None, d_pos or None, d_free_count_out,
+                                         stream or None), "avsg_page_plan")
+
+
+def avsg_rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_turns=32.0,
+                            original=0.0) -> np.ndarray:
+    """Turns per position of each pair as 64-bit binary fractions (host only)."""
+    out = np.zeros(max(int(rot_dim) // 2, 1), np.uint64)
+    _check(load_library().avsg_rotary_frequencies(int(rot_dim), float(base), float(factor),
+                                                  float(low_turns), float(high_turns),
+                                                  float(original), out.ctypes.data),
+           "avsg_rotary_frequencies")
+    return out
+
+
+def avsg_rotary_write(pages: avsg_pages, args: "avsg_rotary", stream=0) -> None:
+    _check(load_library().avsg_rotary_write(pages, args, stream or None), "avsg_rotary_write")
+
+
+def avsg_tree_keep(pages: avsg_pages, d_first, d_path, d_keep, d_len_out, d_free_count_out,
+                   stream=0) -> None:
+    _check(load_library().avsg_tree_keep(pages, d_first, d_path or None, d_keep, d_len_out,
+                                         d_free_count_out, stream or None), "avsg_tree_keep")
 
 
 def avsg_strerror(code: int) -> str:

@@ -1,0 +1,157 @@
+"""A paged device cache for decoding with drafted tokens: marshalling around
+avsg_page_plan, avsg_rotary_write, avsg_tree_attention and avsg_tree_keep
+(include/avsg.h has the layouts and the rules).
+
+All tensors are the caller's, contiguous and on one CUDA device; shapes, types
+and devices are checked here (``ValueError``), the rest by the library
+(``AvsgError``).  Nothing synchronises except ``error`` and ``clear_error``.
+"""
+from __future__ import annotations
+
+import numpy as np
+import torch
+
+from . import avsg as C
+
+_TYPES = {torch.bfloat16: C.AVSG_BF16, torch.float16: C.AVSG_F16}
+
+
+def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_turns=32.0,
+                       original=0) -> torch.Tensor:
+    """The frequency table of ``PagedCache.rotary`` (a host tensor: 64-bit words as int64)."""
+    t = C.avsg_rotary_frequencies(rot_dim, base, factor, low_turns, high_turns, original)
+    return torch.from_numpy(t[:int(rot_dim) // 2].view(np.int64))
+
+
+class PagedCache:
+    """Pages, block tables, lengths and free pages of a batch of requests.
+
+    k, v [layers][num_pages][kv_heads][page_tokens][head_dim] bf16 or fp16;
+    tables [requests][max_pages], lens [requests], free [num_pages] and
+    free_count [1] int32.  New tokens are ragged rows: request r owns rows
+    first[r] .. first[r + 1] of every per-token tensor.
+    """
+
+    def __init__(self, k, v, tables, lens, free, free_count):
+        if k.dim() != 5 or v.shape != k.shape or k.dtype not in _TYPES or v.dtype != k.dtype:
+            raise ValueError("k and v: [layers][num_pages][kv_heads][page_tokens][head_dim], "
+                             "both bfloat16 or both float16")
+        if k.device.type != "cuda":
+            raise ValueError("the cache lives on a CUDA device")
+        layers, pages, heads, page, dim = k.shape
+        self.device, self.dtype = k.device, k.dtype
+        self.requests, self.kv_heads, self.head_dim = len(lens), heads, dim
+        self.k, self.v, self.tables, self.lens = k, v, tables, lens
+        self.free, self.free_count = free, free_count
+        self._check("k", k, k.dtype, None)
+        self._check("v", v, k.dtype, None)
+        self._check("tables", tables, torch.int32, (len(lens), tables.shape[-1]))
+        self._check("lens", lens, torch.int32, (len(lens),))
+        self._check("free", free, torch.int32, (pages,))
+        self._check("free_count", free_count, torch.int32, (1,))
+        self._error = torch.zeros(4, dtype=torch.int32, device=k.device)
+        self._pages = C.avsg_pages(len(lens), layers, pages, heads, page, dim, tables.shape[1],
+                                   _TYPES[k.dtype], k.data_ptr(), v.data_ptr(), tables.data_ptr(),
+                                   lens.data_ptr(), free.data_ptr(), free_count.data_ptr(),
+                                   self._error.data_ptr())
+
+    @classmethod
+    def allocate(cls, requests, max_pages, num_pages, kv_heads, page_tokens, head_dim, layers=1,
+                 dtype=torch.bfloat16, device="cuda") -> "PagedCache":
+        """An empty cache: no tokens, every page free (taken from 0 upward)."""
+        shape = (layers, num_pages, kv_heads, page_tokens, head_dim)
+        ints = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros(shape, dtype=dtype, device=device),
+                   torch.zeros(shape, dtype=dtype, device=device),
+                   torch.zeros(requests, max_pages, **ints), torch.zeros(requests, **ints),
+                   torch.arange(num_pages - 1, -1, -1, **ints), torch.full((1,), num_pages, **ints))
+
+    def _check(self, name, t, dtype, shape):
+        if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or (
+                shape is not None and t.shape != shape):
+            raise ValueError(f"{name}: a contiguous {dtype} tensor on {self.device}"
+                             + (f" of shape {list(shape)}" if shape is not None else "")
+                             + f" is wanted, not {t.dtype} {list(t.shape)} on {t.device}")
+
+    def _rows(self, name, t, heads):
+        """Token rows of heads * head_dim values with any stride between tokens; the stride."""
+        if t.dtype != self.dtype or t.device != self.device or t.dim() not in (2, 3):
+            raise ValueError(f"{name}: {self.dtype} rows on {self.device} are wanted")
+        width = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
+        inner = t.stride(-1) == 1 and (t.dim() == 2 or t.shape[1] == 1 or t.stride(1) == t.shape[2])
+        if width != heads * self.head_dim or not (inner or t.numel() == 0):
+            raise ValueError(f"{name}: rows of {heads} x {self.head_dim} consecutive values are wanted")
+        return t.stride(0) if t.shape[0] > 1 else width
+
+    def plan(self, new, first, slots, positions, mask=None, free_count_out=None, stream=0):
+        """Tables, slots and positions of the step's new tokens.  new [requests],
+        first [requests + 1], slots and positions [capacity] int32; mask
+        [tokens] int64 words of ancestor bits; free_count_out defaults to the
+        cache's own count."""
+        r = self.requests
+        out = self.free_count if free_count_out is None else free_count_out
+        self._check("new", new, torch.int32, (r,))
+        self._check("first", first, torch.int32, (r + 1,))
+        self._check("slots", slots, torch.int32, (slots.numel(),))
+        self._check("positions", positions, torch.int32, slots.shape)
+        self._check("free_count_out", out, torch.int32, (1,))
+        if mask is not None:
+            self._check("mask", mask, torch.int64, (mask.numel(),))
+        C.avsg_page_plan(self._pages, new.data_ptr(), 0 if mask is None else mask.data_ptr(),
+                         slots.numel(), first.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                         out.data_ptr(), stream)
+
+    def rotary(self, q, k, v, positions, slots, freq, q_out, layer=0, rot_offset=0,
+               interleaved=False, magnitude=1.0, tokens_per_request=1, stream=0):
+        """Rotates q into q_out and k into the pages, stores v beside it.
+
+        q [T][q_heads * head_dim] (or [T][q_heads][head_dim]), k and v like it
+        with kv_heads, any stride between tokens; slots [T] or None (slot t for
+        token t); freq from ``rotary_frequencies``, on the device; q_out
+        contiguous, the cache's type or float32."""
+        tokens = q.shape[0]
+        heads = q.shape[1] // self.head_dim if q.dim() == 2 else q.shape[1]
+        qs, ks, vs = self._rows("q", q, heads), self._rows("k", k, self.kv_heads), \
+            self._rows("v", v, self.kv_heads)
+        if k.shape[0] != tokens or v.shape[0] != tokens:
+            raise ValueError("q, k and v have one row per token")
+        f32 = q_out.dtype == torch.float32
+        self._check("q_out", q_out, torch.float32 if f32 else self.dtype, None)
+        if q_out.numel() != tokens * heads * self.head_dim:
+            raise ValueError("q_out: as many values as q has")
+        self._check("positions", positions, torch.int32, (tokens,))
+        self._check("freq", freq, torch.int64, (freq.numel(),))
+        if slots is not None:
+            self._check("slots", slots, torch.int32, (tokens,))
+        C.avsg_rotary_write(self._pages, C.avsg_rotary(
+            tokens, heads, 2 * freq.numel(), rot_offset, int(interleaved), int(f32),
+            tokens_per_request, layer, qs, ks, vs, magnitude, 0, q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
+            0 if slots is None else slots.data_ptr(), q_out.data_ptr()), stream)
+
+    def keep(self, first, path, keep, lens_out=None, free_count_out=None, stream=0):
+        """Keeps the accepted drafts of every layer and frees the pages past the
+        new lengths.  keep [requests] int32: kept tokens, or -1: the request
+        ends; path [tokens] int32 or None: the first keep[r] ones."""
+        r = self.requests
+        lens = self.lens if lens_out is None else lens_out
+        count = self.free_count if free_count_out is None else free_count_out
+        self._check("first", first, torch.int32, (r + 1,))
+        self._check("keep", keep, torch.int32, (r,))
+        self._check("lens_out", lens, torch.int32, (r,))
+        self._check("free_count_out", count, torch.int32, (1,))
+        if path is not None:
+            self._check("path", path, torch.int32, (path.numel(),))
+        C.avsg_tree_keep(self._pages, first.data_ptr(), 0 if path is None else path.data_ptr(),
+                         keep.data_ptr(), lens.data_ptr(), count.data_ptr(), stream)
+
+    def error(self):
+        """(code, request, position) of the first latched device error, code 0
+        for none; waits for the device."""
+        return tuple(self._error.tolist()[:3])
+
+    def clear_error(self):
+        """Waits for the device and drops a latched error."""
+        torch.cuda.synchronize(self.device)
+        self._error.zero_()
+        torch.cuda.synchronize(self.device)

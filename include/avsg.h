@@ -331,6 +331,142 @@ int avsg_host_free(void* p);
 int avsg_read_rows(const void* src, int64_t num_rows, int64_t row_bytes, const int32_t* d_idx,
                    int64_t n, int32_t ctas, uint32_t* d_sink, void* stream);
 
+/*
+ * Paged device cache.  For K and V that stay on the device -- a draft model's
+ * layers, layers that are not offloaded -- and for drafted tokens that are not
+ * part of the host store yet: block tables and slot maps built on the GPU from
+ * request lengths, rotary positions written straight into the pages, attention
+ * for draft trees (or chains, or prompt chunks) over the pages, and the keep
+ * of the accepted drafts.  A step is
+ *   avsg_page_plan     once: tables, slots and positions of the new tokens
+ *   avsg_rotary_write  per layer: q rotated, k rotated and stored, v stored
+ *   avsg_tree_attention per layer
+ *   avsg_tree_keep     once, for all layers, when the drafts are verified
+ * and may be captured into one CUDA graph: no call allocates, synchronises or
+ * reads a length on the host.
+ *
+ * Layout.  d_k and d_v are [num_layers][num_pages][H][page_tokens][D]: one
+ * page of one kv-head is contiguous (Spin page, section 2B, head-wise pages).
+ * Token j of request r is row j % page_tokens of page
+ * d_tables[r][j / page_tokens]; its slot is page * page_tokens + row.  The
+ * first d_len[r] tokens of a request are committed; a step's new tokens follow
+ * them.  New tokens are ragged: request r owns rows d_first[r] ..
+ * d_first[r + 1] of every per-token array.  Free page ids are a stack:
+ * d_free[0 .. d_free_count[0]).
+ *
+ * Errors.  Host checks return a code and enqueue nothing.  What only the
+ * device can see (a page id outside the pool, too few free pages, a path that
+ * is not increasing) is latched in d_error = {code, request, position, 0}; the
+ * first error stays, and every later call on the same d_error does nothing on
+ * the device until the caller zeroes it.  All memory is the caller's, on the
+ * current device (INVALID_ARG for pages of another one), and must stay valid
+ * until the enqueued work is done.  Calls on several streams are independent
+ * as long as nothing that one of them writes is used by another at a time.
+ */
+#define AVSG_BF16 0
+#define AVSG_F16 1
+
+typedef struct avsg_pages {
+  int32_t num_requests; /* R, 1 .. 8192 */
+  int32_t num_layers;   /* >= 1 */
+  int32_t num_pages;    /* pages of the pool; num_pages * page_tokens < 2^31 */
+  int32_t num_kv_heads; /* H */
+  int32_t page_tokens;  /* a power of two, 1 .. 256 */
+  int32_t head_dim;     /* D, a multiple of 8 */
+  int32_t max_pages;    /* columns of d_tables */
+  int32_t dtype;        /* AVSG_BF16 or AVSG_F16 */
+  void* d_k;            /* 16-byte aligned */
+  void* d_v;
+  int32_t* d_tables;    /* [R][max_pages] */
+  int32_t* d_len;       /* [R] committed tokens */
+  int32_t* d_free;      /* [num_pages] stack of free page ids */
+  int32_t* d_free_count;/* [1] */
+  int32_t* d_error;     /* [4], zeroed by the caller at first, 16-byte aligned */
+} avsg_pages;
+
+/*
+ * avsg_page_plan -- tables, slots and positions of a step's new tokens.
+ *   d_new   : int32 [R], new tokens per request (0 is allowed).
+ *   d_mask  : uint64 [tokens] or NULL: ancestors of each draft (see
+ *             avsg_tree_attention); position = len + depth, with depth the
+ *             number of bits - 1.  NULL or a zero word: len + index.
+ *   capacity: entries of d_slot and d_pos.
+ *   d_first : int32 [R + 1], receives the exclusive sum of d_new.
+ *   d_slot  : int32 [capacity], receives each token's slot, -1 behind the last.
+ *   d_pos   : int32 [capacity], receives positions, 0 behind the last.
+ *   d_free_count_out: int32 [1], may be d_free_count itself.
+ * Pages are taken from the top of the stack in request order and entered in
+ * d_tables; entries that do not change are not written.  Latched errors
+ * (CAPACITY: too few free pages, table columns or entries; BAD_SELECTION: a
+ * negative length or a page id outside the pool) leave everything as it was.
+ */
+int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const uint64_t* d_mask,
+                   int32_t capacity, int32_t* d_first, int32_t* d_slot, int32_t* d_pos,
+                   int32_t* d_free_count_out, void* stream);
+
+/*
+ * avsg_rotary_frequencies -- host only: the table of avsg_rotary_write.
+ *   out[i], i < rot_dim / 2: turns per position of pair i as a 64-bit binary
+ *   fraction (2^64 = one turn) of w_i = base^(-2i / rot_dim), scaled for long
+ *   contexts: by 1 / factor when original is 0; else pairs that turn at least
+ *   high_turns times in `original` tokens keep w_i, pairs below low_turns get
+ *   w_i / factor, with a linear ramp in the turns between.
+ */
+int avsg_rotary_frequencies(int32_t rot_dim, double base, double factor, double low_turns,
+                            double high_turns, double original, uint64_t* out);
+
+typedef struct avsg_rotary {
+  int32_t num_tokens;         /* T */
+  int32_t num_q_heads;        /* a multiple of num_kv_heads */
+  int32_t rot_dim;            /* rotated values per head, even, 0 .. D */
+  int32_t rot_offset;         /* first rotated value; the others keep theirs */
+  int32_t interleaved;        /* 1: pairs (2i, 2i + 1); 0: (i, i + rot_dim / 2) */
+  int32_t q_f32;              /* 1: d_q_out is fp32 (avsg_step's q), else the cache's type */
+  int32_t tokens_per_request; /* n: d_q_out is [T / n][H][n][G][D]; 1 is [T][heads][D] */
+  int32_t layer;
+  int64_t q_stride, k_stride, v_stride; /* values between tokens' rows */
+  float magnitude;            /* factor on cos and sin (1 for none) */
+  int32_t reserved0;          /* must be 0 */
+  const void* d_q;            /* [T] rows of num_q_heads * D values, the cache's type */
+  const void* d_k;            /* [T] rows of H * D */
+  const void* d_v;            /* [T] rows of H * D */
+  const uint64_t* d_freq;     /* [rot_dim / 2] */
+  const int32_t* d_pos;       /* [T] */
+  const int32_t* d_slot;      /* [T] or NULL: slot t for token t */
+  void* d_q_out;
+} avsg_rotary;
+
+/*
+ * avsg_rotary_write -- rotates q and k by their tokens' positions, writes q to
+ * d_q_out and k, v to their slots of the given layer.  Angles are exact at any
+ * int32 position; arithmetic is fp32, rounded once.  A token with slot -1 is
+ * skipped whole (padding); a slot past the pool is skipped and latched
+ * (BAD_SELECTION).  Slots must be distinct.  d_q_out may be d_q when the types
+ * agree, tokens_per_request is 1 and q_stride is num_q_heads * D; otherwise
+ * outputs must not overlap inputs.  With page_tokens 1, num_pages T and no
+ * slots, d_k and d_v are the [R][H][D] rows avsg_append takes, and with q_f32
+ * and tokens_per_request n_tok, d_q_out is the d_q of avsg_step.
+ */
+int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream);
+
+/*
+ * avsg_tree_keep -- keeps the accepted drafts and ends requests.
+ *   d_first : as written by the step's avsg_page_plan.
+ *   d_keep  : int32 [R]: number of kept new tokens, or -1: the request ends
+ *             (its length becomes 0 and all its pages are free).
+ *   d_path  : int32 [tokens] or NULL: the kept tokens' indices within their
+ *             request, strictly increasing, at d_path[d_first[r] + i]; NULL
+ *             keeps the first d_keep[r].
+ * Row len + path[i] moves to len + i in every layer; d_len_out (may be d_len)
+ * receives the new lengths; the pages past them return to the stack in the
+ * reverse order of taking, and d_free_count_out (may be d_free_count) counts
+ * them.  Latched errors (BAD_SELECTION: a bad count, path or page id;
+ * CAPACITY: more pages than the pool) leave everything as it was.
+ */
+int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const int32_t* d_path,
+                   const int32_t* d_keep, int32_t* d_len_out, int32_t* d_free_count_out,
+                   void* stream);
+
 /* Error text, and the cudaError_t behind the last AVSG_ERR_CUDA of a handle. */
 const char* avsg_strerror(int code);
 int avsg_cuda_error(avsg_handle h);
