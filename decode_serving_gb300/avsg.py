@@ -128,6 +128,28 @@ class avsg_rotary(ctypes.Structure):
     ]
 
 
+class avsg_tree(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32),
+        ("q_per_kv", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("layer", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("d_q", ctypes.c_void_p),
+        ("d_first", ctypes.c_void_p),
+        ("d_mask", ctypes.c_void_p),
+        ("d_slopes", ctypes.c_void_p),
+        ("d_out", ctypes.c_void_p),
+        ("d_lse", ctypes.c_void_p),
+        ("d_work", ctypes.c_void_p),
+        ("work_bytes", ctypes.c_size_t),
+    ]
+
+
 AVSG_NUM_KERNELS = 8
 
 
@@ -165,6 +187,9 @@ SIGNATURES = {
     "avsg_page_plan": [ctypes.POINTER(avsg_pages), _P, _P, _I32, _P, _P, _P, _P, _P],
     "avsg_rotary_frequencies": [_I32] + [ctypes.c_double] * 5 + [_P],
     "avsg_rotary_write": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_rotary), _P],
+    "avsg_tree_attention_workspace": [ctypes.POINTER(avsg_pages), _I32, _I32,
+                                      ctypes.POINTER(ctypes.c_size_t)],
+    "avsg_tree_attention": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_tree), _P],
     "avsg_tree_keep": [ctypes.POINTER(avsg_pages), _P, _P, _P, _P, _P, _P],
     "avsg_read_rows": [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, _I32, _P, _P],
 }
@@ -329,6 +354,18 @@ def avsg_rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, hi
 
 def avsg_rotary_write(pages: avsg_pages, args: "avsg_rotary", stream=0) -> None:
     _check(load_library().avsg_rotary_write(pages, args, stream or None), "avsg_rotary_write")
+
+
+def avsg_tree_attention_workspace(pages: avsg_pages, q_per_kv, max_new) -> int:
+    """Bytes of workspace avsg_tree_attention needs."""
+    n = ctypes.c_size_t()
+    _check(load_library().avsg_tree_attention_workspace(pages, q_per_kv, max_new, ctypes.byref(n)),
+           "avsg_tree_attention_workspace")
+    return n.value
+
+
+def avsg_tree_attention(pages: avsg_pages, args: avsg_tree, stream=0) -> None:
+    _check(load_library().avsg_tree_attention(pages, args, stream or None), "avsg_tree_attention")
 
 
 def avsg_tree_keep(pages: avsg_pages, d_first, d_path, d_keep, d_len_out, d_free_count_out,

@@ -129,6 +129,41 @@ class PagedCache:
             v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
             0 if slots is None else slots.data_ptr(), q_out.data_ptr()), stream)
 
+    def attention_workspace(self, q_per_kv, max_new) -> torch.Tensor:
+        """Scratch of ``attend``; calls that may overlap need one each."""
+        n = C.avsg_tree_attention_workspace(self._pages, q_per_kv, max_new)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, first, out, max_new, work, mask=None, lse=None, layer=0, scale=0.0,
+               softcap=0.0, window=0, slopes=None, stream=0):
+        """Attention of the step's new tokens over their requests' pages.
+
+        q [T][q_heads][head_dim] (any stride between tokens), out like it and
+        contiguous, lse [T][q_heads] float32 or None; first from ``plan``;
+        max_new bounds every request's new tokens; mask [tokens] int64 words
+        (None: chains); slopes [q_heads] float32 or None."""
+        heads = q.shape[1] // self.head_dim if q.dim() == 2 else q.shape[1]
+        stride = self._rows("q", q, heads)
+        tokens = q.shape[0]
+        if heads % self.kv_heads:
+            raise ValueError("q: a multiple of the cache's heads is wanted")
+        self._check("out", out, self.dtype, None)
+        if out.numel() != tokens * heads * self.head_dim:
+            raise ValueError("out: as many values as q has")
+        self._check("first", first, torch.int32, (self.requests + 1,))
+        self._check("work", work, torch.uint8, None)
+        if mask is not None:
+            self._check("mask", mask, torch.int64, (mask.numel(),))
+        if lse is not None:
+            self._check("lse", lse, torch.float32, (tokens, heads))
+        if slopes is not None:
+            self._check("slopes", slopes, torch.float32, (heads,))
+        C.avsg_tree_attention(self._pages, C.avsg_tree(
+            tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride,
+            q.data_ptr(), first.data_ptr(), 0 if mask is None else mask.data_ptr(),
+            0 if slopes is None else slopes.data_ptr(), out.data_ptr(),
+            0 if lse is None else lse.data_ptr(), work.data_ptr(), work.numel()), stream)
+
     def keep(self, first, path, keep, lens_out=None, free_count_out=None, stream=0):
         """Keeps the accepted drafts of every layer and frees the pages past the
         new lengths.  keep [requests] int32: kept tokens, or -1: the request

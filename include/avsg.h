@@ -450,6 +450,60 @@ typedef struct avsg_rotary {
 int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream);
 
 /*
+ * avsg_tree_attention -- attention of a step's new tokens over the pages.
+ * Per new token and query head:  s = scale q.k;  softcap > 0: s = softcap *
+ * tanh(s / softcap);  d_slopes: s -= slope * (position of q - position of k);
+ * out = softmax(s) v over the visible keys, lse = log of the sum of exp(s).
+ * New token i of a request sees every committed token and, of its new ones,
+ * those in its mask word (bit j: new token j of the same request; an ancestor
+ * mask holds the token's own bit).  d_mask NULL, or a request with more than
+ * 64 new tokens: the new tokens up to itself (a chain, or a prompt chunk).
+ * Positions: a committed token's index; a new token's len + number of mask
+ * bits - 1, len + i for a chain or a zero word.  window > 0: only keys with
+ * position of q - position of k < window.  The new tokens' own K and V must
+ * be in the pages (avsg_rotary_write).  A row without a visible key gives
+ * zeros and -infinity.  What a row does not see does not reach it, whatever
+ * it holds; neither does what lies in the pages behind the last new token.
+ * A weight that rounds to 0 in the cache's type counts as 0.
+ */
+typedef struct avsg_tree {
+  int32_t num_tokens;   /* rows of d_q, d_out and d_lse (at least d_first[R]; the
+                           rows behind d_first[R] are left as they are) */
+  int32_t q_per_kv;     /* G: query heads per kv-head, 1 .. 64 */
+  int32_t max_new;      /* no request has more new tokens (else CAPACITY is latched) */
+  int32_t layer;
+  int32_t window;       /* 0: none */
+  float softmax_scale;  /* 0 selects 1/sqrt(D) */
+  float softcap;        /* 0: none */
+  int32_t reserved0;    /* must be 0 */
+  int64_t q_stride;     /* values between tokens of d_q, even */
+  const void* d_q;      /* rows of [H][G][D], the cache's type, 4-byte aligned */
+  const int32_t* d_first; /* [R + 1] */
+  const uint64_t* d_mask; /* [tokens] or NULL */
+  const float* d_slopes;  /* [H * G] or NULL */
+  void* d_out;          /* [num_tokens][H][G][D], the cache's type, 16-byte aligned */
+  float* d_lse;         /* [num_tokens][H][G] or NULL */
+  void* d_work;         /* 256-byte aligned, any contents */
+  size_t work_bytes;    /* at least avsg_tree_attention_workspace */
+} avsg_tree;
+
+/*
+ * Bytes of d_work for the device of p->d_k.  The size depends on D, q_per_kv
+ * and max_new, not on lengths.  Calls that may run at the same time (two
+ * streams, two graphs) need a workspace each.
+ */
+int avsg_tree_attention_workspace(const avsg_pages* p, int32_t q_per_kv, int32_t max_new,
+                                  size_t* bytes);
+
+/*
+ * D of 64, 128 or 256 (UNSUPPORTED else).  Latched errors: BAD_SELECTION (a
+ * page id outside the pool, a negative length, rows past num_tokens; position
+ * = the key), CAPACITY (more than max_new new tokens, or than the table
+ * holds); d_out of such a call is undefined, nothing else is written.
+ */
+int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void* stream);
+
+/*
  * avsg_tree_keep -- keeps the accepted drafts and ends requests.
  *   d_first : as written by the step's avsg_page_plan.
  *   d_keep  : int32 [R]: number of kept new tokens, or -1: the request ends

@@ -67,10 +67,11 @@ def turns_of(pos, freq):
 
 def attention(q, k, v, length, mask=None, scale=None, cap=0.0, window=0, slopes=None):
     """One request and one kv-head: q [n, G, D], k and v [length + n, D] float64,
-    mask n words or None (a chain), slopes [G].  (out [n, G, D], lse [n, G])."""
+    mask n words or None (a chain), slopes [G].  Returns out [n, G, D], lse [n, G] and
+    the sums of weights times |v| (what a rounding of the weights scales with)."""
     n, groups, dim = q.shape
     scale = dim ** -0.5 if scale is None else scale
-    out, lse = np.zeros_like(q), np.full((n, groups), -math.inf)
+    out, lse, size = np.zeros_like(q), np.full((n, groups), -math.inf), np.zeros_like(q)
     depth = np.arange(n)
     if mask is not None:
         bits = np.array([popcount(m) for m in mask])
@@ -95,4 +96,5 @@ def attention(q, k, v, length, mask=None, scale=None, cap=0.0, window=0, slopes=
             e = np.exp(s - m)
             lse[t, g] = m + math.log(e.sum())
             out[t, g] = (e / e.sum()) @ v[see]
-    return out, lse
+            size[t, g] = (e / e.sum()) @ np.abs(v[see])
+    return out, lse, size

@@ -79,6 +79,35 @@ def test_bad_rotary(lib, kw, code):
     assert lib.avsg_rotary_write(p, avsg.avsg_rotary(**f), None) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(num_tokens=-1), -1), (dict(q_per_kv=0), -1), (dict(q_per_kv=65), -7), (dict(max_new=0), -1),
+    (dict(layer=2), -1), (dict(layer=-1), -1), (dict(window=-1), -1), (dict(softmax_scale=-1.0), -1),
+    (dict(softmax_scale=math.inf), -1), (dict(softcap=-1.0), -1), (dict(softcap=math.nan), -1),
+    (dict(reserved0=1), -1), (dict(q_stride=255), -1), (dict(q_stride=257), -1), (dict(d_q=None), -1),
+    (dict(d_q=2), -1), (dict(d_first=None), -1), (dict(d_out=None), -1), (dict(d_out=8), -1),
+    (dict(d_work=None), -1), (dict(d_work=128), -1),
+])
+def test_bad_attention(lib, kw, code):
+    from decode_serving_gb300 import avsg
+    p, at = pages()
+    f = dict(num_tokens=4, q_per_kv=2, max_new=4, layer=1, q_stride=256, d_q=at, d_first=at, d_out=at,
+             d_work=(at + 255) // 256 * 256, work_bytes=1 << 30)
+    f.update(kw)
+    assert lib.avsg_tree_attention(p, avsg.avsg_tree(**f), None) == code
+
+
+def test_attention_shapes(lib):
+    from decode_serving_gb300 import avsg
+    n = ctypes.c_size_t()
+    assert lib.avsg_tree_attention_workspace(pages(head_dim=96)[0], 4, 1, ctypes.byref(n)) == -7
+    assert lib.avsg_tree_attention_workspace(pages()[0], 0, 1, ctypes.byref(n)) == -1
+    assert lib.avsg_tree_attention_workspace(pages()[0], 4, 0, ctypes.byref(n)) == -1
+    assert lib.avsg_tree_attention_workspace(pages()[0], 4, 1, None) == -1
+    assert lib.avsg_tree_attention(pages()[0], None, None) == -1
+    assert lib.avsg_tree_attention(pages(page_tokens=3)[0], avsg.avsg_tree(q_per_kv=1, max_new=1), None) == -7
+    assert lib.avsg_tree_attention(pages()[0], avsg.avsg_tree(q_per_kv=1, max_new=1), None) == 0
+
+
 def test_no_tokens_is_no_work(lib):
     from decode_serving_gb300 import avsg
     p, _ = pages()
@@ -89,7 +118,8 @@ def test_no_tokens_is_no_work(lib):
 def test_struct_layouts(tmp_path):
     from decode_serving_gb300 import avsg
     names = [("avsg_pages", "d_k"), ("avsg_pages", "d_error"), ("avsg_rotary", "q_stride"),
-             ("avsg_rotary", "magnitude"), ("avsg_rotary", "d_q_out")]
+             ("avsg_rotary", "magnitude"), ("avsg_rotary", "d_q_out"), ("avsg_tree", "q_stride"),
+             ("avsg_tree", "d_first"), ("avsg_tree", "work_bytes")]
     src = tmp_path / "layout.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "avsg.h"\nint main(void){'
                    + "".join(f'printf("%zu %zu\\n", sizeof({s}), offsetof({s}, {f}));' for s, f in names)
