@@ -7,25 +7,34 @@ namespace {
 
 constexpr int kMostGroups = 64;
 
-// Warps along the rows of an m-tile: 16 rows a warp, the fewest that hold all
-// rows of a request and kv-head (up to 64); the other warps split the keys.
-// At least one token's query heads have to fit.
-int rows_warps(int G, int max_new) {
+// Which kernel a call runs and how its rows are cut.
+struct Plan {
+  bool umma;
+  int wm;      // the other kernel's warps along the rows
+  int MT;      // rows per m-tile
+  int ctas;
+};
+Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   const int64_t rows = (int64_t)G * max_new;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  Plan x;
+  // tcgen05: boxes of whole 8-row groups, an output that fits the tensor memory twice
+  x.umma = p->page_tokens >= 8 && p->head_dim <= 128 && rows > 16;
+  // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
+  x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  x.MT = x.umma ? 256 : 16 * x.wm;
+  x.ctas = x.umma || p->head_dim == 256 ? sms : 2 * sms;
+  return x;
 }
-
-int ctas_per_sm(int D) { return D == 256 ? 1 : 2; }
 
 struct Workspace {
   size_t ml, part, bytes;  // byte offsets; the heads lie at 0
 };
-Workspace layout(int ctas, int MT, int D) {
+Workspace layout(const Plan& x, int D) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Workspace w;
-  w.ml = up((size_t)ctas * sizeof(int4));
-  w.part = w.ml + up((size_t)2 * ctas * MT * 2 * sizeof(float));
-  w.bytes = w.part + up((size_t)2 * ctas * MT * D * sizeof(float));
+  w.ml = up((size_t)x.ctas * sizeof(int4));
+  w.part = w.ml + up((size_t)2 * x.ctas * x.MT * 2 * sizeof(float));
+  w.bytes = w.part + up((size_t)2 * x.ctas * x.MT * D * sizeof(float));
   return w;
 }
 
@@ -51,7 +60,7 @@ extern "C" int avsg_tree_attention_workspace(const avsg_pages* p, int32_t q_per_
   int dev = 0, sms = 0;
   const int rd = paged_device(p->d_k, &dev, &sms);
   if (rd != AVSG_OK) return rd;
-  *bytes = layout(sms * ctas_per_sm(p->head_dim), 16 * rows_warps(q_per_kv, max_new), p->head_dim).bytes;
+  *bytes = layout(plan_attention(p, q_per_kv, max_new, sms), p->head_dim).bytes;
   return AVSG_OK;
 }
 
@@ -72,9 +81,9 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   int dev = 0, sms = 0;
   rc = paged_device(p->d_k, &dev, &sms);
   if (rc != AVSG_OK) return rc;
-  const int wm = rows_warps(t->q_per_kv, t->max_new), MT = 16 * wm, D = p->head_dim;
-  const int ctas = sms * ctas_per_sm(D);
-  const Workspace w = layout(ctas, MT, D);
+  const int D = p->head_dim;
+  const Plan x = plan_attention(p, t->q_per_kv, t->max_new, sms);
+  const Workspace w = layout(x, D);
   if (t->work_bytes < w.bytes) return AVSG_ERR_CAPACITY;
   const size_t layer = (size_t)p->num_pages * p->num_kv_heads * p->page_tokens * D * 2;
   unsigned char* work = static_cast<unsigned char*>(t->d_work);
@@ -104,9 +113,9 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   a.max_pages = p->max_pages;
   a.num_pages = p->num_pages;
   a.max_new = t->max_new;
-  a.tpm = MT / a.G;
+  a.tpm = x.MT / a.G;
   a.window = t->window;
-  a.ctas = ctas;
+  a.ctas = x.ctas;
   a.min_tiles = 2;
   a.score_log2 = scale * log2e;
   if (t->softcap > 0.f) {
@@ -114,8 +123,9 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
     a.cap_out = t->softcap * log2e;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = D == 64    ? launch_tree_d64(a, p->dtype, wm, dev, st)
-                  : D == 128 ? launch_tree_d128(a, p->dtype, wm, dev, st)
-                             : launch_tree_d256(a, p->dtype, wm, dev, st);
+  cudaError_t e = x.umma     ? launch_tree_umma(a, p->dtype, D, dev, st)
+                  : D == 64  ? launch_tree_d64(a, p->dtype, x.wm, dev, st)
+                  : D == 128 ? launch_tree_d128(a, p->dtype, x.wm, dev, st)
+                             : launch_tree_d256(a, p->dtype, x.wm, dev, st);
   return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
 }

@@ -64,14 +64,17 @@ struct TreeArgs {
 cudaError_t launch_tree_d64(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 cudaError_t launch_tree_d128(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 cudaError_t launch_tree_d256(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
+// D of 64 or 128, pages of at least 8 tokens, up to 256 rows per m-tile (avsg_tree_umma.cu).
+cudaError_t launch_tree_umma(const TreeArgs& a, int dtype, int D, int dev, cudaStream_t st);
 
 namespace tree {
 
 constexpr int KT = 64;           // keys per tile
 constexpr int kThreads = 128;
-// fp16 weights are held times 2^12: the smallest normal one is then 2^-26 of
-// the largest, not 2^-14, and 2^12 itself is far from the type's end.
-constexpr float kHalfShift = 12.f;
+// fp16 weights are held times 2^6: the smallest normal one is then 2^-20 of
+// the largest, not 2^-14; with the 2^8 that a weight may reach relative to a
+// maximum not yet followed (avsg_tree_umma.cu) it is far from the type's end.
+constexpr float kHalfShift = 6.f;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -140,13 +143,48 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// One request as the kernel sees it.  A request with a bad length is latched
-// and has no work.
+// sum of floor((a i + b) / m) over i < n (the Euclid-like recursion on lattice points)
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const long long x = m;
+    m = a;
+    a = x;
+  }
+  return sum;
+}
+
+// One request as the kernels see it.  A request with a bad length is latched
+// and has no work.  Its rows are cut into mts units of tpm tokens per kv-head.
+template <int KT>
 struct Req {
-  int len, n, f, lo, tiles, mts;
+  int len, n, f, lo, mts;
+  bool chain;
+
+  // Tiles of unit mt, counted from key lo: up to the last key that a row may see.
+  __device__ int tiles(int mt, int tpm) const {
+    return (len - lo + (chain ? min(n, (mt + 1) * tpm) : n) + KT - 1) / KT;
+  }
+  // Tiles of the units before mt.
+  __device__ long long before(int mt, int tpm) const {
+    if (mt == 0) return 0;
+    if (!chain) return (long long)mt * tiles(0, tpm);
+    return floor_sum(mt, KT, tpm, (long long)(len - lo) + tpm + KT - 1);
+  }
+  __device__ long long per_head(int tpm) const {
+    return n ? before(mts - 1, tpm) + tiles(mts - 1, tpm) : 0;
+  }
 };
-__device__ __forceinline__ Req load_req(const TreeArgs& a, int r) {
-  Req q;
+template <int KT>
+__device__ __forceinline__ Req<KT> load_req(const TreeArgs& a, int r) {
+  Req<KT> q;
   q.f = a.first[r];
   const int end = a.first[r + 1];
   q.len = a.len[r];
@@ -158,16 +196,130 @@ __device__ __forceinline__ Req load_req(const TreeArgs& a, int r) {
     code = AVSG_ERR_CAPACITY;
   if (code) {
     raise_error(a.err, code, r, -1);
-    q.n = 0;
+    q.n = q.len = 0;
   }
+  q.chain = !a.mask || q.n > kMaxDrafts;
   q.lo = a.window > 0 && q.len >= a.window ? (q.len - a.window + 1) & ~(KT - 1) : 0;
-  q.tiles = (q.len + q.n - q.lo + KT - 1) / KT;
   q.mts = (q.n + a.tpm - 1) / a.tpm;
   return q;
 }
-__device__ __forceinline__ long long req_weight(const TreeArgs& a, const Req& q) {
-  return q.n ? (long long)q.tiles * q.mts * a.H : 0;
-}
+
+// A CTA's piece of a unit.
+struct Piece {
+  int r, h, f, len, n;                     // request
+  int tok0, ntok;                          // the unit's tokens
+  int j0, count;                           // first key of the first tile; tiles
+  // Keys that some row may see, keys that every row sees (the window aside),
+  // the largest position a row can have.
+  int limit, all_see, far_pos;
+  int last;                                // CTA of the unit's last tile
+  bool chain, whole, begins;               // begins: the unit's first tile is in this piece
+
+  // Whether some row sees only part of tile t.
+  template <int KT>
+  __device__ bool edge(int t, int window) const {
+    const int j = j0 + t * KT;
+    return j + KT > all_see || (window > 0 && far_pos - j >= window);
+  }
+};
+
+// The CTA's share of the list: every thread walks it alike.
+template <int KT>
+struct Walk {
+  Req<KT> q;
+  long long at, end, W;                    // list positions, length of the list
+  int C;                                   // CTAs with a share
+  int r, h, mt, ta;
+
+  // Finds the share (all threads of the block; a barrier inside).  False: no work.
+  __device__ bool begin(const TreeArgs& a, long long* s_warp, long long* s_base, int* s_r) {
+    const int per = (a.R + blockDim.x - 1) / blockDim.x;
+    const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
+    long long mine = 0;
+    for (int i = r0; i < r1; ++i) mine += load_req<KT>(a, i).per_head(a.tpm) * a.H;
+    long long before = block_exclusive(mine, s_warp, &W);
+    const long long fit = W / a.min_tiles;
+    C = fit < 1 ? 1 : fit < a.ctas ? (int)fit : a.ctas;
+    const int cta = blockIdx.x;
+    if (W == 0 || cta >= C) return false;  // (the same for the whole block)
+    at = cta * W / C;
+    end = (cta + 1) * W / C;
+    if (before <= at && at < before + mine)
+      for (int i = r0; i < r1; ++i) {
+        const long long w = load_req<KT>(a, i).per_head(a.tpm) * a.H;
+        if (at < before + w) {
+          *s_r = i;
+          *s_base = before;
+          break;
+        }
+        before += w;
+      }
+    __syncthreads();
+    r = *s_r;
+    q = load_req<KT>(a, r);
+    const long long head = q.per_head(a.tpm), off = at - *s_base;
+    h = (int)(off / head);
+    const long long rest = off - h * head;
+    int lo = 0, hi = q.mts;                // before(lo) <= rest < before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (q.before(mid, a.tpm) <= rest) lo = mid;
+      else hi = mid;
+    }
+    mt = lo;
+    ta = (int)(rest - q.before(lo, a.tpm));
+    return true;
+  }
+
+  // The next piece with work; false at the end of the share.
+  __device__ bool next(const TreeArgs& a, Piece& p) {
+    while (at < end) {
+      const int all = q.tiles(mt, a.tpm);
+      const int t0 = ta, t1 = (int)min((long long)all, ta + (end - at));
+      const long long unit_end = at - ta + all;
+      const int lo = q.lo;                 // (q may move on below)
+      p.r = r;
+      p.h = h;
+      p.f = q.f;
+      p.len = q.len;
+      p.n = q.n;
+      p.chain = q.chain;
+      p.tok0 = mt * a.tpm;
+      p.ntok = min(a.tpm, q.n - p.tok0);
+      p.limit = q.len + (q.chain ? p.tok0 + p.ntok : q.n);
+      p.all_see = q.len + (q.chain ? p.tok0 + 1 : 0);
+      p.far_pos = q.len + (q.chain ? p.tok0 + p.ntok : q.n) - 1;
+      // tiles that lie before the window of every row have no work
+      int skip = 0;
+      if (a.window > 0 && q.chain)
+        skip = max(0, (q.len + p.tok0 - a.window + 1 - q.lo) / KT);
+      at += t1 - t0;
+      ta = t1;
+      if (t1 == all) {
+        ta = 0;
+        if (++mt == q.mts) {
+          mt = 0;
+          if (++h == a.H) {
+            h = 0;
+            if (at < end) {
+              do q = load_req<KT>(a, ++r); // (one with work follows: at < end <= W)
+              while (q.n == 0 && r + 1 < a.R);
+            }
+          }
+        }
+      }
+      const int from = max(t0, skip);
+      if (from >= t1) continue;
+      p.j0 = lo + from * KT;
+      p.count = t1 - from;
+      p.begins = t0 <= skip;
+      p.whole = p.begins && t1 == all;
+      p.last = (int)((unit_end * C - 1) / W);
+      return true;
+    }
+    return false;
+  }
+};
 
 template <typename T_, int D_, int WM_>
 struct Shape {
@@ -206,75 +358,22 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
   int4 head = make_int4(0, 0, 0, 0);
 
   griddep_wait();
-  bool idle = __syncthreads_or(load_err(a.err) != 0);
-  // This CTA's share [at, end) of the list.
-  long long at = 0, end = 0, W = 0;
-  int C = 1;
-  if (!idle) {
-    const int per = (a.R + kThreads - 1) / kThreads;
-    const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += req_weight(a, load_req(a, r));
-    long long before = block_exclusive(mine, s_warp, &W);
-    const long long fit = W / a.min_tiles;
-    C = fit < 1 ? 1 : fit < a.ctas ? (int)fit : a.ctas;
-    idle = W == 0 || cta >= C;
-    if (!idle) {
-      at = cta * W / C;
-      end = (cta + 1) * W / C;
-      if (before <= at && at < before + mine)
-        for (int r = r0; r < r1; ++r) {
-          const long long w = req_weight(a, load_req(a, r));
-          if (at < before + w) {
-            s_r = r;
-            s_base = before;
-            break;
-          }
-          before += w;
-        }
-    }
-  }
-  if (idle) {
+  Walk<KT> walk;
+  if (__syncthreads_or(load_err(a.err) != 0) || !walk.begin(a, s_warp, &s_base, &s_r)) {
     if (tid == 0) a.head[cta] = head;
     return;
   }
-  __syncthreads();
-  int r = s_r;
-  long long base = s_base;
 
-  while (at < end) {
-    const Req rq = load_req(a, r);
-    const long long weight = req_weight(a, rq);
-    if (at >= base + weight) {                       // (empty requests too)
-      base += weight;
-      if (++r >= a.R) break;
-      continue;
-    }
-    const int unit = (int)((at - base) / rq.tiles);
-    const int ta = (int)((at - base) - (long long)unit * rq.tiles);
-    const long long unit_at = at - ta;               // list position of the unit's first tile
-    const int tb = (int)min((long long)rq.tiles, ta + (end - at));
-    at += tb - ta;
-    const int h = unit / rq.mts, mt = unit - h * rq.mts;
-    const int tok0 = mt * a.tpm;                     // the m-tile's first token
-    const int ntok = min(a.tpm, rq.n - tok0), rows = ntok * a.G;
-    const bool chain = !a.mask || rq.n > kMaxDrafts;
-    // Keys that some row of the m-tile may see, and those that every row sees
-    // (the window aside); tiles behind the former have no work.
-    const int limit = rq.len + (chain ? tok0 + ntok : rq.n);
-    const int all_see = rq.len + (chain ? tok0 + 1 : 0);
-    const int far_pos = rq.len + rq.n - 1;           // no row's position is larger
-    const int live = (limit - rq.lo + KT - 1) / KT;  // tiles of the unit with work
-    if (ta >= live) continue;
-    const int tc = min(tb, live), count = tc - ta;
-
-    const int32_t* table = a.tables + (size_t)r * a.max_pages;
+  Piece pc;
+  while (walk.next(a, pc)) {
+    const int rows = pc.ntok * a.G, count = pc.count, h = pc.h;
+    const int32_t* table = a.tables + (size_t)pc.r * a.max_pages;
     auto find_row = [&](int i) -> long long {        // row of key (tid % KT) of the i-th tile
-      const int j = rq.lo + (ta + i) * KT + (tid & (KT - 1));
-      if (i >= count || j >= limit) return -1;
+      const int j = pc.j0 + i * KT + (tid & (KT - 1));
+      if (i >= count || j >= pc.limit) return -1;
       const int32_t page = __ldg(table + (j >> a.shift));
       if (page < 0 || page >= a.num_pages) {
-        raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, j);
+        raise_error(a.err, AVSG_ERR_BAD_SELECTION, pc.r, j);
         return -1;
       }
       return (((long long)page * a.H + h) << a.shift) + (j & ((1 << a.shift) - 1));
@@ -301,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
 #pragma unroll
       for (int i = 0; i < S - 1; ++i) s_row[i * KT + tid] = rr[i];
     }
-    if (!chain && tid >= KT && tid - KT < rq.n) {
-      const unsigned long long w = a.mask[rq.f + tid - KT];
+    if (!pc.chain && tid >= KT && tid - KT < pc.n) {
+      const unsigned long long w = a.mask[pc.f + tid - KT];
       s_depth[tid - KT] = w ? __popcll(w) - 1 : tid - KT;
     }
     __syncthreads();
@@ -323,14 +422,14 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
       const int rl = wm * 16 + g + 8 * x;
       const int lt = rl / a.G, gg = rl - lt * a.G;
       const bool ok = rl < rows;
-      tok[x] = ok ? tok0 + lt : -1;                  // -1: a padding row, sees no new token
-      q_pos[x] = rq.len + max(tok[x], 0);
-      if (!chain && ok) {
-        bits[x] = a.mask[rq.f + tok[x]];
-        if (bits[x]) q_pos[x] = rq.len + __popcll(bits[x]) - 1;
+      tok[x] = ok ? pc.tok0 + lt : -1;                  // -1: a padding row, sees no new token
+      q_pos[x] = pc.len + max(tok[x], 0);
+      if (!pc.chain && ok) {
+        bits[x] = a.mask[pc.f + tok[x]];
+        if (bits[x]) q_pos[x] = pc.len + __popcll(bits[x]) - 1;
       }
       if (a.slopes && ok) slope[x] = a.slopes[h * a.G + gg] * 1.4426950408889634f;
-      q_row[x] = ok ? a.q + ((long long)(rq.f + tok[x]) * a.q_stride + (long long)(h * a.G + gg) * D) * 2
+      q_row[x] = ok ? a.q + ((long long)(pc.f + tok[x]) * a.q_stride + (long long)(h * a.G + gg) * D) * 2
                     : nullptr;
     }
     uint32_t qf[SH::Q_SMEM ? 1 : D / 16][4];
@@ -403,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
         }
       }
 
-      const int j0 = rq.lo + (ta + i) * KT;          // the tile's first key
-      const bool edge = j0 + KT > all_see || (a.window > 0 && far_pos - j0 >= a.window);
+      const int j0 = pc.j0 + i * KT;                 // the tile's first key
+      const bool edge = pc.edge<KT>(i, a.window);
       // (in an edge tile) values that some rows must not see
       bool bad_v = false;
       if (edge) {
@@ -435,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int j = j0 + wk * NK + x * 8 + 2 * c + (y & 1), row = y >> 1;
-            const int jd = j - rq.len;
+            const int jd = j - pc.len;
             bool see = true;
             int k_pos = j;
             if (jd >= 0) {
-              if (chain) {
+              if (pc.chain) {
                 see = jd <= tok[row];
               } else {
-                see = jd < rq.n && ((bits[row] >> (jd & 63)) & 1);
-                k_pos = rq.len + s_depth[jd & 63];
+                see = jd < pc.n && ((bits[row] >> (jd & 63)) & 1);
+                k_pos = pc.len + s_depth[jd & 63];
               }
             }
             const int far = q_pos[row] - k_pos;
@@ -553,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
       for (int row = 0; row < 2; ++row)
         *reinterpret_cast<float2*>(s_o + (wk * MT + wm * 16 + g + 8 * row) * SH::OP + x * 8 + 2 * c) =
             make_float2(acc[x][2 * row], acc[x][2 * row + 1]);
-    const bool whole = ta == 0 && tc == live;
-    const int slot = 2 * cta + (ta > 0 ? 0 : 1);
+    const bool whole = pc.whole;
+    const int slot = 2 * cta + (pc.begins ? 1 : 0);
     if (tid < rows) {
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -572,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
       if (whole) {
         if (a.lse) {
           const int lt = tid / a.G, gg = tid - lt * a.G;
-          a.lse[(long long)(rq.f + tok0 + lt) * a.H * a.G + h * a.G + gg] =
+          a.lse[(long long)(pc.f + pc.tok0 + lt) * a.H * a.G + h * a.G + gg] =
               sum == 0.f ? -INFINITY
                          : (top - (HALF ? kHalfShift : 0.f)) * 0.6931471805599453f + logf(sum);
         }
@@ -595,18 +694,14 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
       }
       if (whole) {
         const int lt = row / a.G, gg = row - lt * a.G;
-        const long long at_row = (long long)(rq.f + tok0 + lt) * a.H * a.G + h * a.G + gg;
+        const long long at_row = (long long)(pc.f + pc.tok0 + lt) * a.H * a.G + h * a.G + gg;
         *reinterpret_cast<uint2*>(a.out + (at_row * D + c4) * 2) =
             make_uint2(pack<T>(o.x, o.y), pack<T>(o.z, o.w));
       } else {
         *reinterpret_cast<float4*>(a.part + ((long long)slot * MT + row) * D + c4) = o;
       }
     }
-    if (!whole && ta == 0) {
-      // the CTA whose share holds the unit's last tile with work
-      const int last = (int)(((unit_at + live) * C - 1) / W);
-      head = make_int4(last - cta + 1, rq.f + tok0, h, rows);
-    }
+    if (!whole && pc.begins) head = make_int4(pc.last - cta + 1, pc.f + pc.tok0, h, rows);
   }
   griddep_launch();
   if (tid == 0) a.head[cta] = head;
@@ -688,6 +783,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a
   }
 }
 
+// Joins after the attention, whose m-tiles hold MT rows.
+template <typename T, int D>
+cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
+  const int most = a.max_new < a.tpm ? a.max_new : a.tpm;
+  const int rows = most * a.G;
+  // Many units: few pieces each, a warp per row; few units: many pieces, four.
+  if (a.R * a.H >= 16)
+    return launch_pdl(tree_merge_kernel<T, D, 1>, dim3(a.ctas, (rows + kMergeWarps - 1) / kMergeWarps),
+                      dim3(kMergeWarps * 32), 0, st, a, MT);
+  return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, dim3(a.ctas, rows), dim3(kMergeWarps * 32), 0,
+                    st, a, MT);
+}
+
 template <typename T, int D, int WM>
 cudaError_t launch_one(const TreeArgs& a, int dev, cudaStream_t st) {
   using SH = Shape<T, D, WM>;
@@ -695,15 +803,7 @@ cudaError_t launch_one(const TreeArgs& a, int dev, cudaStream_t st) {
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(tree_attn_kernel<SH>), SH::SMEM, dev);
   if (e == cudaSuccess)
     e = launch_pdl(tree_attn_kernel<SH>, dim3(a.ctas), dim3(kThreads), SH::SMEM, st, a);
-  if (e != cudaSuccess) return e;
-  const int most = a.max_new < a.tpm ? a.max_new : a.tpm;
-  const int rows = most * a.G;
-  // Many units: few pieces each, a warp per row; few units: many pieces, four.
-  if (a.R * a.H >= 16)
-    return launch_pdl(tree_merge_kernel<T, D, 1>, dim3(a.ctas, (rows + kMergeWarps - 1) / kMergeWarps),
-                      dim3(kMergeWarps * 32), 0, st, a, SH::MT);
-  return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, dim3(a.ctas, rows), dim3(kMergeWarps * 32), 0,
-                    st, a, SH::MT);
+  return e != cudaSuccess ? e : launch_merge<T, D>(a, SH::MT, st);
 }
 
 template <int D>
