@@ -12,19 +12,26 @@
 //                   output there when the maximum has grown by more than 2^8
 //                   (until then weights up to 2^8 stand in for it: the same
 //                   quotient, no pass over the output);
-//   warp 8          K and V tiles by TMA, one box per page and 64 columns, a
-//                   lane each, into a ring of five 32 KB buffers that runs on
-//                   into the next unit;
-//   warp 9          issues the products: S = Q K^T (both in shared memory),
-//                   O += P V (P in tensor memory);
-//   warps 10, 11    in tiles that some rows see only in part: V's rows behind
-//                   the last key and values that are not finite become 0.
-// Two streams keep the tensor cores busy while the other's softmax runs.
+//   warps 8, 10     K and V tiles by TMA, one box per page, a lane each, into a
+//                   ring of five buffers that runs on into the next unit;
+//   warps 9, 11     issue the products of stream 0 and 1: S = Q K^T (both in
+//                   shared memory), O += P V (P in tensor memory).  An issuing
+//                   warp is held up by the products before, so that one warp's
+//                   waits for P would leave the tensor cores idle: with one warp
+//                   for both streams a tile of 256 rows took 4000 cycles.
+// In tiles that some rows see only in part, the softmax warps also make V's
+// rows behind the last key and its values that are not finite 0 before the
+// product (0 times them would be NaN in rows that do not see them);
+// add_bad_values gives the latter back to the rows that do.
+// A stream works on halves of a tile (64 keys) with two places for scores, so
+// that the scores of its next half are there when it has finished one: its
+// softmax follows its softmax, and the products of both streams run beside.
 // More than 128 rows: stream x holds rows 128x .. and both use every tile (K
 // and V are read once for 256 rows).  Up to 128 rows: the streams take the
 // even and the odd tiles, with an output each, joined at the end of the unit.
 //
-// Tensor memory (512 columns): S/P of stream x at 128 x, O at 256 + 128 x.
+// Tensor memory (512 columns): S/P of stream x at 128 x + 64 (half & 1), O at
+// 256 + 128 x.
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
 // the waits after it return at once.
 #include <cuda.h>
@@ -38,6 +45,7 @@ namespace {
 constexpr int UT = 128;                    // keys per tile
 constexpr int UM = 128;                    // rows per stream
 constexpr int kUmmaThreads = 384;
+constexpr int UH = 64;                     // keys per half tile
 constexpr int kRing = 5;
 constexpr float kLazy = 8.f;               // growth of the maximum (log2) that O is scaled for
 constexpr long long kWaitClocks = 4000000000LL;
@@ -88,10 +96,19 @@ __device__ __forceinline__ void bar_wait(uint32_t b, uint32_t parity, volatile i
     }
   }
 }
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+// One lane of a converged warp, always the same one.  (Code under it keeps the operands of
+// the tensor and copy instructions in uniform registers; under `lane == 0` each of them cost
+// 90 to 180 cycles to issue.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int group, int page) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
-          "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %3, %3, %4, %5}], [%2];" ::
+          "r"(dst), "l"(map), "r"(bar), "r"(0), "r"(group), "r"(page)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -164,13 +181,50 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* r) {
       : "memory");
 }
 
-// Shared-memory operand of 128-byte swizzled rows (8 rows of 128 bytes make an
-// atom of 1024 bytes).  Rows along M or N: groups of 8 rows lie 1024 bytes
-// apart.  Rows along K (V): blocks of 64 columns lie `block` bytes apart.
-__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t block) {
-  return (uint64_t)((at & 0x3FFFF) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Two fp32 values at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
 }
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Shared-memory operand of 128-byte swizzled rows: atoms of 8 rows by 64
+// columns (1024 bytes), the COLS atoms of 8 whole rows beside each other, so
+// groups of 8 rows lie 1024 * COLS bytes apart and blocks of 64 columns 1024.
+// A box of one page thus lands in one piece: its TMA dimensions are 64
+// columns, 8 rows, COLS blocks, row groups and the page.
+// The low word holds the address, the rest is the same for all operands.
+__device__ __forceinline__ uint32_t operand_low(uint32_t at) { return (at >> 4) | ((1024 >> 4) << 16); }
+template <int COLS>
+__device__ __forceinline__ uint64_t operand(uint32_t low) {
+  constexpr uint32_t high = (1024 * COLS >> 4) | (1u << 14) | (2u << 29);
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(low), "n"(high));
+  return x;
+}
+// A value that all lanes hold, known to the compiler to be one (it then stays in a uniform
+// register, where the tensor instructions want their operands: without it every operand is moved
+// there lane by lane, 57 cycles an instruction).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
 template <typename T>
 __device__ constexpr uint32_t instruction(int n, bool b_along_k) {
   const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -237,7 +291,8 @@ __device__ __noinline__ void add_bad_values(const TreeArgs& a, const Piece& s, c
   }
 }
 
-template <typename T, int D>
+// EXTRA: with a score cap or a distance bias.
+template <typename T, int D, bool EXTRA>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
     tree_umma_kernel(UmmaArgs ua, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
@@ -259,11 +314,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   const uint32_t bars = smem + M::BARS;
   auto full = [&](int b) { return bars + 8 * b; };
   auto empty = [&](int b) { return bars + 8 * (kRing + b); };
-  auto s_full = [&](int x) { return bars + 8 * (2 * kRing + x); };
-  auto p_full = [&](int x) { return bars + 8 * (2 * kRing + 2 + x); };
-  auto o_full = [&](int x) { return bars + 8 * (2 * kRing + 4 + x); };
-  const uint32_t q_full = bars + 8 * (2 * kRing + 6), v_in = bars + 8 * (2 * kRing + 7),
-                 v_ok = bars + 8 * (2 * kRing + 8);
+  auto s_full = [&](int x, int b) { return bars + 8 * (2 * kRing + 2 * x + b); };
+  auto p_full = [&](int x, int b) { return bars + 8 * (2 * kRing + 4 + 2 * x + b); };
+  auto o_done = [&](int x) { return bars + 8 * (2 * kRing + 8 + x); };
+  auto o_last = [&](int x) { return bars + 8 * (2 * kRing + 10 + x); };
+  auto q_full = [&](int x) { return bars + 8 * (2 * kRing + 12 + x); };
 
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
@@ -272,18 +327,19 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   }
   if (tid == 0) {
     for (int b = 0; b < kRing; ++b) {
-      bar_init(full(b), 1);
-      bar_init(empty(b), 1);
+      bar_init(full(b), 2);
+      bar_init(empty(b), 2);
     }
     for (int x = 0; x < 2; ++x) {
-      bar_init(s_full(x), 1);
-      bar_init(p_full(x), UM);
-      bar_init(o_full(x), 1);
+      for (int b = 0; b < 2; ++b) {
+        bar_init(s_full(x, b), 1);
+        bar_init(p_full(x, b), UM);
+      }
+      bar_init(o_done(x), 1);
+      bar_init(o_last(x), 1);
+      bar_init(q_full(x), UM);
     }
-    bar_init(q_full, 2 * UM);
-    bar_init(v_in, 1);
-    bar_init(v_ok, 64);
-    s_give_up = 0;
+    s_give_up = s_bad[0] = s_bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   griddep_wait();
@@ -300,214 +356,43 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   volatile int* give_up = &s_give_up;
   Piece s;
 
-  if (warp == 8) {
-    // ---- loads.  Order of a segment: two streams over all tiles: K0 V0 K1 V1 ...; one tile
-    // each in turn: K0 K1 V0 K2 V1 K3 ... -- the order in which the products use them.
-    int idx = 0;
-    const int boxes = UT / ua.box_rows;
-    const int bi = lane / COLS, col = lane % COLS;
-    while (walk.next(a, s)) {
-      const bool two = s.ntok * a.G > UM;
-      const int32_t* table = a.tables + (size_t)s.r * a.max_pages;
-      for (int x = 0; x < 2 * s.count; ++x, ++idx) {
-        int t;
-        bool is_v;
-        if (two) {
-          t = x >> 1;
-          is_v = x & 1;
-        } else if (x < 2) {                // K0, then K1 (or V0 of a single tile)
-          is_v = x == 1 && s.count == 1;
-          t = is_v ? 0 : x;
-        } else {                           // pairs V_t K_{t + 2}, then the last V
-          const int y = x - 2, pairs = 2 * (s.count - 2);
-          is_v = y >= pairs || !(y & 1);
-          t = y >= pairs ? s.count - 2 + y - pairs : (y >> 1) + ((y & 1) ? 2 : 0);
-        }
-        const int j = s.j0 + t * UT + bi * ua.box_rows;
-        int page = -1;
-        if (bi < boxes && j < s.limit) {
-          page = __ldg(table + (j >> a.shift));
-          if (page < 0 || page >= a.num_pages) {
-            raise_error(a.err, AVSG_ERR_BAD_SELECTION, s.r, j);
-            page = -1;
-          }
-        }
-        const int b = idx % kRing;
-        const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        bar_wait(empty(b), ((idx / kRing) & 1) ^ 1, give_up, a.err);
-        if (lane == 0) bar_expect(full(b), n * ua.box_rows * 128);
-        __syncwarp();
-        if (page >= 0)
-          tma_box(smem + M::RING + b * M::TILE + col * (UT * 128) + bi * ua.box_rows * 128,
-                  is_v ? &v_map : &k_map, full(b), col * 64, (s.h << a.shift) + (j & ((1 << a.shift) - 1)),
-                  page);
-      }
-    }
-    // every copy has landed before the CTA may end
-    for (int b = 0; b < kRing && b < idx; ++b) {
-      const int last = (idx - 1 - b) / kRing;  // use number of buffer b's last load
-      bar_wait(full(b), last & 1, give_up, a.err);
-    }
-  } else if (warp == 9) {
-    // ---- products
-    int idx = 0, seg = 0, pv[2] = {0, 0}, edges = 0;
-    const uint32_t id_s = instruction<T>(UT, false), id_o = instruction<T>(D, true);
-    auto wait_load = [&](int place) -> uint32_t {
-      const int i = idx + place, b = i % kRing;
-      bar_wait(full(b), (i / kRing) & 1, give_up, a.err);
-      return smem + M::RING + b * M::TILE;
-    };
-    auto scores = [&](int x, int q, uint32_t k) {
-      if (lane == 0) {
-        const uint32_t qa = smem + q * M::Q;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * (UT * 128) + (ks % 4) * 32;
-          mma_ss(tmem + 128 * x, operand(qa + off, 16), operand(k + off, 16), id_s, ks > 0);
-        }
-        mma_commit(s_full(x));
-      }
-    };
-    auto output = [&](int x, uint32_t v, bool first) {
-      if (lane == 0) {
-#pragma unroll
-        for (int ks = 0; ks < UT / 16; ++ks)
-          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + ks * 8, operand(v + ks * 2048, UT * 128), id_o,
-                 !first || ks > 0);
-      }
-    };
-    auto release = [&](int place) {
-      if (lane == 0) mma_commit(empty((idx + place) % kRing));
-    };
-    auto finish = [&](int x) {
-      if (lane == 0) mma_commit(o_full(x));
-    };
-    auto wait_p = [&](int x) {
-      bar_wait(p_full(x), pv[x] & 1, give_up, a.err);
-      ++pv[x];
-      tc_fence_after();
-    };
-    auto wait_v = [&](bool two, int t) -> uint32_t {
-      const uint32_t v = wait_load(v_place(two, t, s.count));
-      if (s.edge<UT>(t, a.window)) {
-        if (lane == 0) bar_arrive(v_in);
-        bar_wait(v_ok, edges & 1, give_up, a.err);
-        ++edges;
-      }
-      tc_fence_after();
-      return v;
-    };
-    while (walk.next(a, s)) {
-      const bool two = s.ntok * a.G > UM;
-      bar_wait(q_full, seg & 1, give_up, a.err);
-      ++seg;
-      tc_fence_after();
-      if (two) {
-        uint32_t k = wait_load(0);
-        scores(0, 0, k);
-        scores(1, 1, k);
-        release(0);
-        for (int t = 0; t < s.count; ++t) {
-          const uint32_t v = wait_v(true, t);
-          const bool more = t + 1 < s.count;
-          wait_p(0);
-          output(0, v, t == 0);
-          if (more) {
-            k = wait_load(2 * t + 2);
-            scores(0, 0, k);
-          } else {
-            finish(0);
-          }
-          wait_p(1);
-          output(1, v, t == 0);
-          release(2 * t + 1);
-          if (more) {
-            scores(1, 1, k);
-            release(2 * t + 2);
-          } else {
-            finish(1);
-          }
-        }
-      } else {
-        for (int t = 0; t < 2 && t < s.count; ++t) {
-          scores(t, 0, wait_load(t));
-          release(t);
-        }
-        for (int t = 0; t < s.count; ++t) {
-          const int x = t & 1;
-          const uint32_t v = wait_v(false, t);
-          wait_p(x);
-          output(x, v, t < 2);
-          const int place = v_place(false, t, s.count);
-          release(place);
-          if (t + 2 < s.count) {
-            scores(x, 0, wait_load(place + 1));
-            release(place + 1);
-          } else {
-            finish(x);
-          }
-        }
-      }
-      idx += 2 * s.count;
-      __syncwarp();
-    }
-  } else if (warp >= 10) {
-    // ---- V of tiles that some rows see in part
-    // (warp 9 says when such a tile has come: these warps do not follow every load, and a
-    // barrier's parity alone does not tell a phase from the one two before it)
-    int idx = 0, seg = 0, edges = 0;
-    const int me = tid - 320;              // 0 .. 63
-    while (walk.next(a, s)) {
-      const bool two = s.ntok * a.G > UM;
-      if (me == 0) s_bad[seg & 1] = 0;
-      __syncwarp();
-      asm volatile("bar.sync 2, 64;" ::: "memory");
-      for (int t = 0; t < s.count; ++t) {
-        if (!s.edge<UT>(t, a.window)) continue;
-        const int b = (idx + v_place(two, t, s.count)) % kRing;
-        bar_wait(v_in, edges & 1, give_up, a.err);
-        ++edges;
-        unsigned char* v = smem_raw + (smem - smem_u32(smem_raw)) + M::RING + b * M::TILE;
-        const int rows = min(UT, s.limit - s.j0 - t * UT);
-        bool bad = false;
-        for (int x = me; x < M::TILE / 16; x += 64) {
-          const int row = (x / 8) % UT;    // 8 chunks a row, 64 columns a block
-          uint4* p = reinterpret_cast<uint4*>(v + x * 16);
-          if (row >= rows) {
-            *p = make_uint4(0u, 0u, 0u, 0u);
-            continue;
-          }
-          uint4 w = *p;
-          uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-          bool here = false;
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (not_finite<T>(e[y])) {
-              if (not_finite<T>(e[y] & 0xffffu)) e[y] &= 0xffff0000u;
-              if (not_finite<T>(e[y] & 0xffff0000u)) e[y] &= 0xffffu;
-              here = true;
-            }
-          if (here) {
-            *p = w;
-            bad = true;
-          }
-        }
-        if (bad) s_bad[seg & 1] = 1;
-        async_fence();
-        bar_arrive(v_ok);
-      }
-      idx += 2 * s.count;
-      __syncwarp();
-      asm volatile("bar.sync 1, 320;" ::: "memory");  // with the softmax warps: s_bad stands
-      ++seg;
-    }
-  } else {
+  if (warp < 8) {
     // ---- softmax: one row per thread
     const int x = warp >> 2, row = tid & (UM - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16 and up
-    const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
+    const uint32_t to = tmem + lanes + 256 + 128 * x;
     int4 head = make_int4(0, 0, 0, 0);
-    int tiles_done = 0, outs1 = 0, seg = 0;
+    int hh = 0, outs = 0, seg = 0, idx = 0;  // hh: halves of this stream since the start
+    // V of tile t, made safe to multiply: see above.  Both streams may do the same tile: they
+    // write the same values.  Its load's number follows those of loads that this tile's scores
+    // needed by less than kRing, so the parity tells its phase.
+    auto clean_v = [&](bool two, int t) {
+      const int n = idx + v_place(two, t, s.count), b = n % kRing;
+      bar_wait(full(b), (n / kRing) & 1, give_up, a.err);
+      unsigned char* v = smem_raw + (smem - smem_u32(smem_raw)) + M::RING + b * M::TILE;
+      const int rows = min(UT, s.limit - s.j0 - t * UT);
+      bool bad = false;
+#pragma unroll 4
+      for (int y = row; y < M::TILE / 16; y += UM) {
+        const int vr = y / (64 * COLS) * 8 + (y / 8) % 8;  // 8 chunks a row of an atom
+        uint4* at = reinterpret_cast<uint4*>(v + y * 16);
+        uint4 c = *at;
+        uint32_t e[4] = {c.x, c.y, c.z, c.w};
+        bool here = false;
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (not_finite<T>(e[z])) {
+            if (not_finite<T>(e[z] & 0xffffu)) e[z] &= 0xffff0000u;
+            if (not_finite<T>(e[z] & 0xffff0000u)) e[z] &= 0xffffu;
+            here = true;
+          }
+        if (vr >= rows) *at = make_uint4(0u, 0u, 0u, 0u);
+        else if (here) *at = make_uint4(e[0], e[1], e[2], e[3]);
+        bad |= here && vr < rows;
+      }
+      if (bad) s_bad[seg & 1] = 1;
+      async_fence();
+    };
     while (walk.next(a, s)) {
       const bool two = s.ntok * a.G > UM;
       const int rl = two ? x * UM + row : row;
@@ -536,7 +421,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       }
       // this row of q
       if (two || x == 0) {
-        unsigned char* q = smem_raw + (smem - smem_u32(smem_raw)) + x * M::Q + row * 128;
+        unsigned char* q = smem_raw + (smem - smem_u32(smem_raw)) + x * M::Q + (row / 8) * (1024 * COLS) + (row & 7) * 128;
         const unsigned char* src =
             a.q + ((long long)(s.f + max(tok, 0)) * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
 #pragma unroll
@@ -550,131 +435,159 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               w = make_uint4(p[0], p[1], p[2], p[3]);
             }
           }
-          *reinterpret_cast<uint4*>(q + (c / 8) * (UT * 128) + (((c & 7) ^ (row & 7)) << 4)) = w;
+          *reinterpret_cast<uint4*>(q + (c / 8) * 1024 + (((c & 7) ^ (row & 7)) << 4)) = w;
         }
+        async_fence();
+        bar_arrive(q_full(x));
       }
-      async_fence();
-      bar_arrive(q_full);
 
       float m = -INFINITY, l = 0.f;
-      const int my_tiles = two ? s.count : (s.count - x + 1) >> 1;
-      for (int i = 0; i < my_tiles; ++i, ++tiles_done) {
-        const int t = two ? i : 2 * i + x;
-        const int j0 = s.j0 + t * UT;
+      const bool warp_live = rl - lane < s.ntok * a.G;
+      const int halves = 2 * (two ? s.count : (s.count - x + 1) >> 1);
+      for (int i = 0; i < halves; ++i, ++hh) {
+        const int t = two ? i >> 1 : 2 * (i >> 1) + x;
+        const int j0 = s.j0 + t * UT + (hh & 1) * UH;
         const bool edge = s.edge<UT>(t, a.window);
-        const bool plain = !edge && a.cap_in == 0.f && !a.slopes;
-        bar_wait(s_full(x), tiles_done & 1, give_up, a.err);
+        const uint32_t ts = tmem + lanes + 128 * x + 64 * (hh & 1);
+        bar_wait(s_full(x, hh & 1), (hh >> 1) & 1, give_up, a.err);
         __syncwarp();                      // (tensor-memory accesses are the whole warp's)
         tc_fence_after();
-        float top = -INFINITY;
-        uint32_t w[32];
-        if (plain) {
+        if (!warp_live) {                  // only padding: nobody reads what these rows give
+          if (edge && !(hh & 1)) clean_v(two, t);
+          __syncwarp();
+          tc_fence_before();
+          bar_arrive(p_full(x, hh & 1));
+          continue;
+        }
+        uint32_t w[2][32];
+        tm_ld32(ts, w[0]);
+        tm_ld32(ts + 32, w[1]);
+        tm_wait_ld(w[0]);
+        tm_wait_ld(w[1]);
+        float scale = a.score_log2;
+        if constexpr (EXTRA) {
+          // capped and biased, in units of log 2
+          scale = 1.f;
 #pragma unroll
-          for (int c = 0; c < UT / 32; ++c) {
-            tm_ld32(ts + c * 32, w);
-            tm_wait_ld(w);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) top = fmaxf(top, __uint_as_float(w[y]));
-          }
-          top *= a.score_log2;
-        } else {
-          // scores in units of log 2, capped, biased, -inf where not visible; back to their place
-#pragma unroll 1
-          for (int c = 0; c < UT / 32; ++c) {
-            tm_ld32(ts + c * 32, w);
-            tm_wait_ld(w);
+          for (int c = 0; c < 2; ++c) {
             const int j = j0 + c * 32;
-            uint32_t see = 0xffffffffu;
-            if (edge) {
-              // committed tokens (a chain: up to this one) below, the window's begin above
-              const int below = s.len + (s.chain ? tok + 1 : 0) - j;
-              see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
-              if (a.window > 0) {
-                const int from = q_pos - a.window + 1 - j;
-                see &= from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
-              }
-              const int d = j - s.len;     // draft of the chunk's first key
-              if (!s.chain && d > -32 && d < 64)
-                see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
-            }
-            float far = slope * (float)(q_pos - j);
+            const float far = slope * (float)(q_pos - j);
             const bool drafts = a.slopes && !s.chain && j + 32 > s.len;
 #pragma unroll
             for (int y = 0; y < 32; ++y) {
-              float v = __uint_as_float(w[y]);
+              float v = __uint_as_float(w[c][y]);
               if (a.cap_in != 0.f) v = a.cap_out * (1.f - __fdividef(2.f, ex2(v * a.cap_in) + 1.f));
               else v *= a.score_log2;
-              if (a.slopes) {
-                float bias = far - slope * (float)y;
-                if (drafts && j + y >= s.len)
-                  bias = slope * (float)(q_pos - s.len - s_depth[x][(j + y - s.len) & 63]);
-                v -= bias;
-              }
-              v = (see >> y) & 1 ? v : -INFINITY;
-              top = fmaxf(top, v);
-              w[y] = __float_as_uint(v);
+              if (!drafts) v += slope * (float)y - far;
+              w[c][y] = __float_as_uint(v);
             }
-            __syncwarp();
-            tm_st32(ts + c * 32, w);
+            if (drafts)
+#pragma unroll
+              for (int y = 0; y < 32; ++y) {
+                const int d = j + y - s.len;
+                const float bias = d >= 0 ? slope * (float)(q_pos - s.len - s_depth[x][d & 63])
+                                          : far - slope * (float)y;
+                w[c][y] = __float_as_uint(__uint_as_float(w[c][y]) - bias);
+              }
           }
-          tm_wait_st();
         }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            // committed tokens (a chain: up to this one) below, the window's begin above
+            const int j = j0 + c * 32;
+            const int below = s.len + (s.chain ? tok + 1 : 0) - j;
+            uint32_t see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
+            if (a.window > 0) {
+              const int from = q_pos - a.window + 1 - j;
+              see &= from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+            }
+            const int d = j - s.len;       // draft of the chunk's first key
+            if (!s.chain && d > -32 && d < 64)
+              see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!((see >> y) & 1)) w[c][y] = 0xff800000u;
+          }
+        }
+        float tops[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t* e = w[z >> 1] + 16 * (z & 1);
+          tops[z] = __uint_as_float(e[0]);
+#pragma unroll
+          for (int y = 1; y < 15; y += 2)
+            tops[z] = max3(tops[z], __uint_as_float(e[y]), __uint_as_float(e[y + 1]));
+          tops[z] = fmaxf(tops[z], __uint_as_float(e[15]));
+        }
+        const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
         // the maximum that the weights are relative to
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         const float now = grow ? top : m;
         const float use = now == -INFINITY ? 0.f : now;
+        __syncwarp();
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(m - use) : 1.f;
           l *= f;
           m = now;
           if (i > 0) {
+            // the product before this one has to be done (the one before it is: these scores
+            // came after it)
+            bar_wait(o_done(x), (hh - 1) & 1, give_up, a.err);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t o[32];
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              tm_ld32(to + c * 32, w);
-              tm_wait_ld(w);
+              tm_ld32(to + c * 32, o);
+              tm_wait_ld(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) w[y] = __float_as_uint(__uint_as_float(w[y]) * f);
-              tm_st32(to + c * 32, w);
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tm_st32(to + c * 32, o);
             }
           }
         }
-        const float scale = plain ? a.score_log2 : 1.f, minus = SHIFT - use;
-        float sum0 = 0.f, sum1 = 0.f;
+        const uint64_t scale2 = pair(scale, scale), minus2 = pair(SHIFT - use, SHIFT - use);
+        uint64_t sums[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < UT / 32; ++c) {
-          uint32_t p[16];
-          tm_ld32(ts + c * 32, w);
-          tm_wait_ld(w);
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int y = 0; y < 16; ++y) {
-            const float p0 = ex2(fmaf(__uint_as_float(w[2 * y]), scale, minus));
-            const float p1 = ex2(fmaf(__uint_as_float(w[2 * y + 1]), scale, minus));
-            sum0 += p0;
-            sum1 += p1;
-            p[y] = pack<T>(p0, p1);
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(w[c][2 * y]), __uint_as_float(w[c][2 * y + 1])), scale2, minus2),
+                   p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sums[y & 1] = add2(sums[y & 1], pair(p0, p1));
+            w[c][y] = pack<T>(p0, p1);
           }
-          tm_st16(ts + c * 16, p);         // over scores that have been read
+          tm_st16(ts + c * 16, w[c]);      // over scores that have been read
         }
+        float sum0, sum1;
+        unpair(add2(sums[0], sums[1]), sum0, sum1);
         l += sum0 + sum1;
+        if (edge && !(hh & 1)) clean_v(two, t);
+        __syncwarp();
         tm_wait_st();
         tc_fence_before();
-        bar_arrive(p_full(x));
+        bar_arrive(p_full(x, hh & 1));
       }
 
       // ---- the end of the piece
       // (stream 1 has no tile, and no output, in a piece of one tile with up to 128 rows)
-      const bool both = two || s.count > 1;
-      const bool other = !two && both && x == 0;  // stream 0 joins stream 1's output to its own
-      if (x == 0) bar_wait(o_full(0), seg & 1, give_up, a.err);
-      if (both && (x == 1 || other)) bar_wait(o_full(1), outs1 & 1, give_up, a.err);
-      if (both) ++outs1;
+      const bool other = !two && s.count > 1 && x == 0;  // stream 0 joins stream 1's output to its own
+      if (halves > 0) {
+        bar_wait(o_last(x), outs & 1, give_up, a.err);
+        ++outs;
+      }
       if (!two && x == 1) {
         s_m[row] = m;
         s_l[row] = l;
       }
       __syncwarp();
       tc_fence_after();
-      asm volatile("bar.sync 1, 320;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      tc_fence_after();
       const bool bad = s_bad[seg & 1] != 0;
       if (two || x == 0) {
         const float m1 = other ? s_m[row] : -INFINITY, l1 = other ? s_l[row] : 0.f;
@@ -733,13 +646,185 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             a.lse[at] = sum == 0.f ? -INFINITY : (top - SHIFT) * 0.6931471805599453f + logf(sum);
         }
       }
+      if (tid == 0) s_bad[(seg + 1) & 1] = 0;
       if (!s.whole && s.begins) head = make_int4(s.last - cta + 1, s.f + s.tok0, s.h, s.ntok * a.G);
       tc_fence_before();
       __syncwarp();
       asm volatile("bar.sync 5, 256;" ::: "memory");  // both outputs are read
+      idx += 2 * s.count;
       ++seg;
     }
     if (tid == 0) a.head[cta] = head;
+  } else if (warp == 8 || warp == 10) {
+    // ---- loads, the boxes of a tile shared by two warps.  Order of a segment: two streams over
+    // all tiles: K0 V0 K1 V1 ...; one tile each in turn: K0 K1 V0 K2 V1 K3 ... -- the order in
+    // which the products use them.  Page ids are looked up one load ahead.
+    const int part = warp == 8 ? 0 : 1;
+    const int boxes = UT / ua.box_rows, own = max(boxes / 2, 1), y = part * own + lane;
+    const bool lane_on = lane < own && y < boxes;
+    int idx = 0;
+    int page = -1, group = 0, is_v = 0;    // the next load's box of this lane
+    bool more = walk.next(a, s);
+    int x = 0;
+    auto look_up = [&]() {
+      const bool two = s.ntok * a.G > UM;
+      int t;
+      if (two) {
+        t = x >> 1;
+        is_v = x & 1;
+      } else if (x < 2) {                  // K0, then K1 (or V0 of a single tile)
+        is_v = x == 1 && s.count == 1;
+        t = is_v ? 0 : x;
+      } else {                             // pairs V_t K_{t + 2}, then the last two V
+        const int z = x - 2, pairs = 2 * (s.count - 2);
+        is_v = z >= pairs || !(z & 1);
+        t = z >= pairs ? s.count - 2 + z - pairs : (z >> 1) + ((z & 1) ? 2 : 0);
+      }
+      const int j = s.j0 + t * UT + y * ua.box_rows;
+      page = -1;
+      if (lane_on && j < s.limit) {
+        page = __ldg(a.tables + (size_t)s.r * a.max_pages + (j >> a.shift));
+        group = ((s.h << a.shift) + (j & ((1 << a.shift) - 1))) >> 3;
+        if (page < 0 || page >= a.num_pages) {
+          raise_error(a.err, AVSG_ERR_BAD_SELECTION, s.r, j);
+          page = -1;
+        }
+      }
+      if (++x == 2 * s.count) {
+        x = 0;
+        more = walk.next(a, s);
+      }
+    };
+    if (more) look_up();
+    bool last = false;
+    while (!last) {
+      const int now = page, now_group = group, now_v = is_v, b = idx % kRing;
+      last = !more;
+      if (more) look_up();
+      const int n = __popc(__ballot_sync(0xffffffffu, now >= 0));
+      bar_wait(empty(b), ((idx / kRing) & 1) ^ 1, give_up, a.err);
+      if (lane == 0) bar_expect(full(b), n * ua.box_rows * D * 2);
+      __syncwarp();
+      if (now >= 0)
+        tma_box(smem + M::RING + b * M::TILE + y * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
+                now_group, now);
+      ++idx;
+    }
+    // every copy has landed before the CTA may end
+    for (int b = 0; b < kRing && b < idx; ++b) {
+      const int use = (idx - 1 - b) / kRing;  // use number of buffer b's last load
+      bar_wait(full(b), use & 1, give_up, a.err);
+    }
+  } else {
+      // ---- products.  Warp 9 has stream 0, and stream 1 too where the streams take turns (K and
+      // V then come as fast as one warp can use them); warp 11 has stream 1 otherwise.
+      const int me = warp == 9 ? 0 : 1;
+      int idx = 0, qs = 0;
+      int ps[2] = {0, 0};                  // halves of each stream since the start
+      const uint32_t id_s = instruction<T>(UH, false), id_o = instruction<T>(D, true);
+      constexpr uint32_t HALF_TILE = UH / 8 * 1024 * COLS;
+      auto wait_load = [&](int place) -> uint32_t {
+        const int i = idx + place, b = i % kRing;
+        bar_wait(full(b), (i / kRing) & 1, give_up, a.err);
+        return smem + M::RING + b * M::TILE;
+      };
+      // Scores of half hh (of the stream's halves since the start) from rows q and the keys at k.
+      auto scores = [&](int x, int q, uint32_t k, int hh) {
+        __syncwarp();
+        const uint32_t qa = uniform(operand_low(smem + q * M::Q)), to = uniform(tmem + 128 * x + 64 * (hh & 1));
+        const uint32_t ka = uniform(operand_low(k + (hh & 1) * HALF_TILE)), bar = uniform(s_full(x, hh & 1));
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks / 4) * 1024 + (ks % 4) * 32) >> 4;
+            mma_ss(to, operand<COLS>(qa + off), operand<COLS>(ka + off), id_s, ks > 0);
+          }
+          mma_commit(bar);
+        }
+      };
+      // P V of half hh of stream x; v: its tile.
+      auto output = [&](int x, uint32_t v, int hh, bool first) {
+        bar_wait(p_full(x, hh & 1), (hh >> 1) & 1, give_up, a.err);
+        tc_fence_after();
+        __syncwarp();
+        const uint32_t va = uniform(operand_low(v + (hh & 1) * HALF_TILE)), bar = uniform(o_done(x));
+        const uint32_t from = uniform(tmem + 128 * x + 64 * (hh & 1)), to = uniform(tmem + 256 + 128 * x);
+        const uint32_t add = uniform(first ? 0 : 1);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < UH / 16; ++ks)
+            mma_ts(to, from + ks * 8, operand<COLS>(va + ks * (2048 * COLS >> 4)), id_o, ks > 0 ? 1 : add);
+          mma_commit(bar);
+        }
+      };
+      auto finish = [&](int x) {
+        if (elect_one()) mma_commit(o_last(x));
+      };
+      auto release = [&](int place) {
+        const uint32_t bar = uniform(empty((idx + place) % kRing));
+        if (elect_one()) mma_commit(bar);
+      };
+      while (walk.next(a, s)) {
+        const bool two = s.ntok * a.G > UM;
+        if (two || me == 0) {
+          bar_wait(q_full(me), qs & 1, give_up, a.err);
+          ++qs;
+          tc_fence_after();
+        }
+        if (two) {
+          const int x = me, hh = ps[x];
+          uint32_t k = wait_load(0);
+          scores(x, x, k, 0);
+          scores(x, x, k, 1);
+          release(0);
+          for (int t = 0; t < s.count; ++t) {
+            const uint32_t v = wait_load(2 * t + 1);
+            const bool more = t + 1 < s.count;
+            output(x, v, hh + 2 * t, t == 0);
+            if (more) {
+              k = wait_load(2 * t + 2);
+              scores(x, x, k, 0);
+            }
+            output(x, v, hh + 2 * t + 1, false);
+            release(2 * t + 1);
+            if (more) {
+              scores(x, x, k, 1);
+              release(2 * t + 2);
+            }
+          }
+          finish(x);
+        } else if (me == 0) {
+          for (int t = 0; t < 2 && t < s.count; ++t) {
+            const uint32_t k = wait_load(t);
+            scores(t, 0, k, 0);
+            scores(t, 0, k, 1);
+            release(t);
+            release(t);                    // (for both)
+          }
+          for (int t = 0; t < s.count; ++t) {
+            const int x = t & 1, place = v_place(false, t, s.count), hh = ps[x] + (t & ~1);
+            const bool more = t + 2 < s.count;
+            const uint32_t v = wait_load(place);
+            output(x, v, hh, t < 2);
+            const uint32_t k = more ? wait_load(place + 1) : 0;
+            if (more) scores(x, 0, k, 0);
+            output(x, v, hh + 1, false);
+            release(place);
+            release(place);
+            if (more) {
+              scores(x, 0, k, 1);
+              release(place + 1);
+              release(place + 1);
+            } else {
+              finish(x);
+            }
+          }
+        }
+        ps[0] += 2 * (two ? s.count : (s.count + 1) >> 1);
+        ps[1] += 2 * (two ? s.count : s.count >> 1);
+        idx += 2 * s.count;
+        __syncwarp();
+      }
   }
   griddep_launch();
   tc_fence_before();
@@ -765,23 +850,25 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Pages as [num_pages][H * page][D], in boxes of 64 columns and min(page, 128) tokens.
+// Pages as [num_pages][H * page / 8 groups][D / 64 blocks][8 rows][64 columns]
+// (strides of the plain layout), in boxes of min(page, 128) whole rows.
 bool encode_pages(CUtensorMap* map, const unsigned char* pages, const TreeArgs& a, int dtype, int D, int box) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H << a.shift, (cuuint64_t)a.num_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, ((cuuint64_t)a.H << a.shift) * D * 2};
-  const cuuint32_t size[3] = {64, (cuuint32_t)box, 1}, step[3] = {1, 1, 1};
-  return encode(map, dtype == AVSG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  const cuuint64_t row = (cuuint64_t)D * 2, rows = (cuuint64_t)a.H << a.shift;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, rows / 8, (cuuint64_t)a.num_pages};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, rows * row};
+  const cuuint32_t size[5] = {64, 8, (cuuint32_t)D / 64, (cuuint32_t)box / 8, 1}, step[5] = {1, 1, 1, 1, 1};
+  return encode(map, dtype == AVSG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                 const_cast<unsigned char*>(pages), dims, strides, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D>
-cudaError_t launch_umma(const TreeArgs& a, int dtype, int dev, cudaStream_t st) {
+template <typename T, int D, bool EXTRA>
+cudaError_t launch_umma_one(const TreeArgs& a, int dtype, int dev, cudaStream_t st) {
   static SmemLimit limit;
-  auto kernel = tree_umma_kernel<T, D>;
+  auto kernel = tree_umma_kernel<T, D, EXTRA>;
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(kernel), Mem<D>::SMEM, dev);
   if (e != cudaSuccess) return e;
   UmmaArgs u{};
@@ -793,6 +880,12 @@ cudaError_t launch_umma(const TreeArgs& a, int dtype, int dev, cudaStream_t st) 
     return cudaErrorInvalidValue;
   e = launch_pdl(kernel, dim3(a.ctas), dim3(kUmmaThreads), Mem<D>::SMEM, st, u, k_map, v_map);
   return e != cudaSuccess ? e : launch_merge<T, D>(a, 2 * UM, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_umma(const TreeArgs& a, int dtype, int dev, cudaStream_t st) {
+  return a.cap_in != 0.f || a.slopes ? launch_umma_one<T, D, true>(a, dtype, dev, st)
+                                     : launch_umma_one<T, D, false>(a, dtype, dev, st);
 }
 
 }  // namespace
