@@ -62,7 +62,7 @@ struct Mem {
   static constexpr int TILE = UT * D * 2;
   static constexpr int RING = 2 * Q;
   static constexpr int BARS = RING + kRing * TILE;
-  static constexpr int SMEM = BARS + 256 + 1024;  // + alignment of the base to 1024
+  static constexpr int SMEM = BARS + 256;
 };
 
 __device__ __forceinline__ void bar_init(uint32_t b, int count) {
@@ -82,6 +82,21 @@ __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
       : "r"(b), "r"(parity)
       : "memory");
   return ok != 0;
+}
+// The same without the wait that the hardware may put into a try.
+__device__ __forceinline__ bool bar_test(uint32_t b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// One arrival for a warp (32 of them to one barrier cost 300 cycles).
+__device__ __forceinline__ void warp_arrive(uint32_t b, int lane) {
+  __syncwarp();
+  if (lane == 0) bar_arrive(b);
 }
 // Waits for the phase of the given parity, a few seconds at most.
 __device__ __forceinline__ void bar_wait(uint32_t b, uint32_t parity, volatile int* gave_up, DevErr* err) {
@@ -300,17 +315,22 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   constexpr bool HALF = std::is_same<T, __half>::value;
   constexpr float SHIFT = HALF ? kHalfShift : 0.f;
   constexpr int COLS = D / 64;             // blocks of 64 columns
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ long long s_warp[kUmmaThreads / 32];
   __shared__ long long s_base;
   __shared__ int s_r, s_give_up, s_bad[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_depth[2][kMaxDrafts];
-  __shared__ float s_m[UM], s_l[UM];
+  __shared__ unsigned char s_depth[2][kMaxDrafts];
+  // The softmax warps' walk: its state would cost registers that the scores need.
+  __shared__ Walk<UT> s_walk;
+  __shared__ Piece s_piece[2];
+  __shared__ int s_more[2];
   const TreeArgs& a = ua.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
-  const uint32_t smem = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t smem = smem_u32(smem_raw);
+  float* s_m = reinterpret_cast<float*>(smem_raw + M::Q);  // (where up to 128 rows leave stream 1's q free)
+  float* s_l = s_m + UM;
   const uint32_t bars = smem + M::BARS;
   auto full = [&](int b) { return bars + 8 * b; };
   auto empty = [&](int b) { return bars + 8 * (kRing + b); };
@@ -333,11 +353,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         bar_init(s_full(x, b), 1);
-        bar_init(p_full(x, b), UM);
+        bar_init(p_full(x, b), UM / 32);
       }
       bar_init(o_done(x), 1);
       bar_init(o_last(x), 1);
-      bar_init(q_full(x), UM);
+      bar_init(q_full(x), UM / 32);
     }
     s_give_up = s_bad[0] = s_bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -354,7 +374,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     return;
   }
   volatile int* give_up = &s_give_up;
-  Piece s;
+  if (tid == 0) {
+    if (smem & 1023) raise_error(a.err, AVSG_ERR_INTERNAL, -1, -1);  // (atoms are 1024-byte aligned)
+    s_walk = walk;
+    s_more[0] = s_walk.next(a, s_piece[0]);
+  }
+  __syncthreads();
 
   if (warp < 8) {
     // ---- softmax: one row per thread
@@ -366,10 +391,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     // V of tile t, made safe to multiply: see above.  Both streams may do the same tile: they
     // write the same values.  Its load's number follows those of loads that this tile's scores
     // needed by less than kRing, so the parity tells its phase.
-    auto clean_v = [&](bool two, int t) {
+    auto clean_v = [&](const Piece& s, bool two, int t) {
       const int n = idx + v_place(two, t, s.count), b = n % kRing;
       bar_wait(full(b), (n / kRing) & 1, give_up, a.err);
-      unsigned char* v = smem_raw + (smem - smem_u32(smem_raw)) + M::RING + b * M::TILE;
+      unsigned char* v = smem_raw + M::RING + b * M::TILE;
       const int rows = min(UT, s.limit - s.j0 - t * UT);
       bool bad = false;
 #pragma unroll 4
@@ -393,7 +418,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       if (bad) s_bad[seg & 1] = 1;
       async_fence();
     };
-    while (walk.next(a, s)) {
+    for (; s_more[seg & 1]; ++seg) {
+      const Piece& s = s_piece[seg & 1];
       const bool two = s.ntok * a.G > UM;
       const int rl = two ? x * UM + row : row;
       const bool mine = rl < s.ntok * a.G;
@@ -421,7 +447,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       }
       // this row of q
       if (two || x == 0) {
-        unsigned char* q = smem_raw + (smem - smem_u32(smem_raw)) + x * M::Q + (row / 8) * (1024 * COLS) + (row & 7) * 128;
+        unsigned char* q = smem_raw + x * M::Q + (row / 8) * (1024 * COLS) + (row & 7) * 128;
         const unsigned char* src =
             a.q + ((long long)(s.f + max(tok, 0)) * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
 #pragma unroll
@@ -438,139 +464,169 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           *reinterpret_cast<uint4*>(q + (c / 8) * 1024 + (((c & 7) ^ (row & 7)) << 4)) = w;
         }
         async_fence();
-        bar_arrive(q_full(x));
+        warp_arrive(q_full(x), lane);
       }
 
       float m = -INFINITY, l = 0.f;
       const bool warp_live = rl - lane < s.ntok * a.G;
       const int halves = 2 * (two ? s.count : (s.count - x + 1) >> 1);
-      for (int i = 0; i < halves; ++i, ++hh) {
-        const int t = two ? i >> 1 : 2 * (i >> 1) + x;
-        const int j0 = s.j0 + t * UT + (hh & 1) * UH;
-        const bool edge = s.edge<UT>(t, a.window);
-        const uint32_t ts = tmem + lanes + 128 * x + 64 * (hh & 1);
-        bar_wait(s_full(x, hh & 1), (hh >> 1) & 1, give_up, a.err);
+      // tiles e0 .. e1 - 1 of the piece are seen whole by every row (Piece::edge)
+      const int e1 = min(s.count, max(0, s.all_see - s.j0) / UT);
+      const int e0 = a.window > 0 ? max(0, (s.far_pos - a.window - s.j0 + UT) / UT) : 0;
+      auto wait_scores = [&](int n) {
+        bar_wait(s_full(x, n & 1), (n >> 1) & 1, give_up, a.err);
         __syncwarp();                      // (tensor-memory accesses are the whole warp's)
         tc_fence_after();
+      };
+      const uint32_t ts0 = tmem + lanes + 128 * x;
+      uint32_t w[2][32];
+      if (halves > 0 && warp_live) {
+        wait_scores(hh);
+        tm_ld32(ts0 + 64 * (hh & 1), w[0]);
+        tm_ld32(ts0 + 64 * (hh & 1) + 32, w[1]);
+      }
+      for (int i = 0; i < halves; ++i, ++hh) {
+        const int t = two ? i >> 1 : (i & ~1) + x;
+        const bool edge = t < e0 || t >= e1;
+        const uint32_t ts = ts0 + 64 * (hh & 1);
         if (!warp_live) {                  // only padding: nobody reads what these rows give
-          if (edge && !(hh & 1)) clean_v(two, t);
-          __syncwarp();
+          wait_scores(hh);
+          if (__builtin_expect(edge && !(hh & 1), 0)) clean_v(s, two, t);
           tc_fence_before();
-          bar_arrive(p_full(x, hh & 1));
+          warp_arrive(p_full(x, hh & 1), lane);
           continue;
         }
-        uint32_t w[2][32];
-        tm_ld32(ts, w[0]);
-        tm_ld32(ts + 32, w[1]);
-        tm_wait_ld(w[0]);
-        tm_wait_ld(w[1]);
-        float scale = a.score_log2;
-        if constexpr (EXTRA) {
-          // capped and biased, in units of log 2
-          scale = 1.f;
+        // The weights are taken relative to the maximum so far while this half's is found: neither
+        // waits for the other.  Where it turns out to have grown too far, once per piece and
+        // seldom after, the scores are read again.
+        float sum;
+        for (bool again = true; again;) {
+          tm_wait_ld(w[0]);
+          tm_wait_ld(w[1]);
+          float scale = a.score_log2;
+          if constexpr (EXTRA) {
+            // capped and biased, in units of log 2
+            scale = 1.f;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int j = j0 + c * 32;
-            const float far = slope * (float)(q_pos - j);
-            const bool drafts = a.slopes && !s.chain && j + 32 > s.len;
-#pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              float v = __uint_as_float(w[c][y]);
-              if (a.cap_in != 0.f) v = a.cap_out * (1.f - __fdividef(2.f, ex2(v * a.cap_in) + 1.f));
-              else v *= a.score_log2;
-              if (!drafts) v += slope * (float)y - far;
-              w[c][y] = __float_as_uint(v);
-            }
-            if (drafts)
+            for (int c = 0; c < 2; ++c) {
+              const int j = s.j0 + t * UT + (hh & 1) * UH + c * 32;
+              const float far = slope * (float)(q_pos - j);
+              const bool drafts = a.slopes && !s.chain && j + 32 > s.len;
 #pragma unroll
               for (int y = 0; y < 32; ++y) {
-                const int d = j + y - s.len;
-                const float bias = d >= 0 ? slope * (float)(q_pos - s.len - s_depth[x][d & 63])
-                                          : far - slope * (float)y;
-                w[c][y] = __float_as_uint(__uint_as_float(w[c][y]) - bias);
+                float v = __uint_as_float(w[c][y]);
+                if (a.cap_in != 0.f) v = a.cap_out * (1.f - __fdividef(2.f, ex2(v * a.cap_in) + 1.f));
+                else v *= a.score_log2;
+                if (!drafts) v += slope * (float)y - far;
+                w[c][y] = __float_as_uint(v);
               }
-          }
-        }
-        if (edge) {
+              if (drafts)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // committed tokens (a chain: up to this one) below, the window's begin above
-            const int j = j0 + c * 32;
-            const int below = s.len + (s.chain ? tok + 1 : 0) - j;
-            uint32_t see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
-            if (a.window > 0) {
-              const int from = q_pos - a.window + 1 - j;
-              see &= from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+                for (int y = 0; y < 32; ++y) {
+                  const int d = j + y - s.len;
+                  const float bias = d >= 0 ? slope * (float)(q_pos - s.len - s_depth[x][d & 63])
+                                            : far - slope * (float)y;
+                  w[c][y] = __float_as_uint(__uint_as_float(w[c][y]) - bias);
+                }
             }
-            const int d = j - s.len;       // draft of the chunk's first key
-            if (!s.chain && d > -32 && d < 64)
-              see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!((see >> y) & 1)) w[c][y] = 0xff800000u;
           }
-        }
-        float tops[4];
+          if (__builtin_expect(edge, 0)) {
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const uint32_t* e = w[z >> 1] + 16 * (z & 1);
-          tops[z] = __uint_as_float(e[0]);
+            for (int c = 0; c < 2; ++c) {
+              // committed tokens (a chain: up to this one) below, the window's begin above
+              const int j = s.j0 + t * UT + (hh & 1) * UH + c * 32;
+              const int below = s.len + (s.chain ? tok + 1 : 0) - j;
+              uint32_t see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
+              if (a.window > 0) {
+                const int from = q_pos - a.window + 1 - j;
+                see &= from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+              }
+              const int d = j - s.len;       // draft of the chunk's first key
+              if (!s.chain && d > -32 && d < 64)
+                see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
 #pragma unroll
-          for (int y = 1; y < 15; y += 2)
-            tops[z] = max3(tops[z], __uint_as_float(e[y]), __uint_as_float(e[y + 1]));
-          tops[z] = fmaxf(tops[z], __uint_as_float(e[15]));
-        }
-        const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
-        // the maximum that the weights are relative to
-        const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
-        const float now = grow ? top : m;
-        const float use = now == -INFINITY ? 0.f : now;
-        __syncwarp();
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(m - use) : 1.f;
-          l *= f;
-          m = now;
-          if (i > 0) {
-            // the product before this one has to be done (the one before it is: these scores
-            // came after it)
-            bar_wait(o_done(x), (hh - 1) & 1, give_up, a.err);
-            __syncwarp();
-            tc_fence_after();
-            uint32_t o[32];
+              for (int y = 0; y < 32; ++y)
+                if (!((see >> y) & 1)) w[c][y] = 0xff800000u;
+            }
+          }
+          float tops[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const uint32_t* e = w[z >> 1] + 16 * (z & 1);
+            tops[z] = __uint_as_float(e[0]);
+#pragma unroll
+            for (int y = 1; y < 15; y += 2)
+              tops[z] = max3(tops[z], __uint_as_float(e[y]), __uint_as_float(e[y + 1]));
+            tops[z] = fmaxf(tops[z], __uint_as_float(e[15]));
+          }
+          const float use = m == -INFINITY ? 0.f : m;
+          const uint64_t scale2 = pair(scale, scale), minus2 = pair(SHIFT - use, SHIFT - use);
+          uint64_t sums[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              float p0, p1;
+              unpair(fma2(pair(__uint_as_float(w[c][2 * y]), __uint_as_float(w[c][2 * y + 1])), scale2, minus2),
+                     p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sums[y & 1] = add2(sums[y & 1], pair(p0, p1));
+              w[c][y] = pack<T>(p0, p1);
+            }
+          float sum1;
+          unpair(add2(sums[0], sums[1]), sum, sum1);
+          sum += sum1;
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+          const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+          __syncwarp();
+          again = __any_sync(0xffffffffu, grow);
+          if (__builtin_expect(again, 0)) {
+            const float f = grow ? ex2(m - top) : 1.f;
+            l *= f;
+            m = grow ? top : m;
+            if (i > 0) {
+              // the product before this one has to be done (the one before it is: these scores
+              // came after it)
+              bar_wait(o_done(x), (hh - 1) & 1, give_up, a.err);
+              __syncwarp();
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tm_ld32(to + c * 32, o);
-              tm_wait_ld(o);
+              for (int c = 0; c < D / 32; ++c) {
+                tm_ld32(to + c * 32, w[0]);
+                tm_wait_ld(w[0]);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tm_st32(to + c * 32, o);
+                for (int y = 0; y < 32; ++y) w[0][y] = __float_as_uint(__uint_as_float(w[0][y]) * f);
+                tm_st32(to + c * 32, w[0]);
+              }
+              tm_wait_st();
             }
+            tm_ld32(ts, w[0]);
+            tm_ld32(ts + 32, w[1]);
           }
         }
-        const uint64_t scale2 = pair(scale, scale), minus2 = pair(SHIFT - use, SHIFT - use);
-        uint64_t sums[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            float p0, p1;
-            unpair(fma2(pair(__uint_as_float(w[c][2 * y]), __uint_as_float(w[c][2 * y + 1])), scale2, minus2),
-                   p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sums[y & 1] = add2(sums[y & 1], pair(p0, p1));
-            w[c][y] = pack<T>(p0, p1);
-          }
-          tm_st16(ts + c * 16, w[c]);      // over scores that have been read
-        }
-        float sum0, sum1;
-        unpair(add2(sums[0], sums[1]), sum0, sum1);
-        l += sum0 + sum1;
-        if (edge && !(hh & 1)) clean_v(two, t);
+        tm_st16(ts, w[0]);                 // over scores that have been read
+        tm_st16(ts + 16, w[1]);
+        l += sum;
+        if (__builtin_expect(edge && !(hh & 1), 0)) clean_v(s, two, t);
         __syncwarp();
+        // the next half's scores come while P is stored, where they are there already
+        const bool more = i + 1 < halves;
+        const bool early =
+            more && __all_sync(0xffffffffu, bar_test(s_full(x, ~hh & 1), ((hh + 1) >> 1) & 1));
+        if (early) {
+          tc_fence_after();
+          tm_ld32(ts0 + 64 * (~hh & 1), w[0]);
+          tm_ld32(ts0 + 64 * (~hh & 1) + 32, w[1]);
+        }
         tm_wait_st();
         tc_fence_before();
-        bar_arrive(p_full(x, hh & 1));
+        warp_arrive(p_full(x, hh & 1), lane);
+        if (more && !early) {
+          wait_scores(hh + 1);
+          tm_ld32(ts0 + 64 * (~hh & 1), w[0]);
+          tm_ld32(ts0 + 64 * (~hh & 1) + 32, w[1]);
+        }
       }
 
       // ---- the end of the piece
@@ -597,11 +653,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         const float inv = s.whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         const long long at = (long long)(s.f + max(tok, 0)) * a.H * a.G + s.h * a.G + gg;
         const long long slot = ((long long)(2 * cta + (s.begins ? 1 : 0)) * (2 * UM) + rl);
-        uint32_t w[32], w1[32];
+        uint32_t w0[32], w1[32];
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          tm_ld32(to + c * 32, w);
-          tm_wait_ld(w);
+          tm_ld32(to + c * 32, w0);
+          tm_wait_ld(w0);
           if (other) {
             tm_ld32(to + 128 + c * 32, w1);
             tm_wait_ld(w1);
@@ -609,7 +665,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           float o[32];
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
-            o[y] = f0 == 0.f ? 0.f : __uint_as_float(w[y]) * f0;
+            o[y] = f0 == 0.f ? 0.f : __uint_as_float(w0[y]) * f0;
             if (other && f1 != 0.f) o[y] += __uint_as_float(w1[y]) * f1;
           }
           if (!mine) {
@@ -646,19 +702,22 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             a.lse[at] = sum == 0.f ? -INFINITY : (top - SHIFT) * 0.6931471805599453f + logf(sum);
         }
       }
-      if (tid == 0) s_bad[(seg + 1) & 1] = 0;
+      idx += 2 * s.count;
+      if (tid == 0) {
+        s_bad[(seg + 1) & 1] = 0;
+        s_more[(seg + 1) & 1] = s_walk.next(a, s_piece[(seg + 1) & 1]);
+      }
       if (!s.whole && s.begins) head = make_int4(s.last - cta + 1, s.f + s.tok0, s.h, s.ntok * a.G);
       tc_fence_before();
       __syncwarp();
       asm volatile("bar.sync 5, 256;" ::: "memory");  // both outputs are read
-      idx += 2 * s.count;
-      ++seg;
     }
     if (tid == 0) a.head[cta] = head;
   } else if (warp == 8 || warp == 10) {
     // ---- loads, the boxes of a tile shared by two warps.  Order of a segment: two streams over
     // all tiles: K0 V0 K1 V1 ...; one tile each in turn: K0 K1 V0 K2 V1 K3 ... -- the order in
     // which the products use them.  Page ids are looked up one load ahead.
+    Piece s;
     const int part = warp == 8 ? 0 : 1;
     const int boxes = UT / ua.box_rows, own = max(boxes / 2, 1), y = part * own + lane;
     const bool lane_on = lane < own && y < boxes;
@@ -718,6 +777,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   } else {
       // ---- products.  Warp 9 has stream 0, and stream 1 too where the streams take turns (K and
       // V then come as fast as one warp can use them); warp 11 has stream 1 otherwise.
+      Piece s;
       const int me = warp == 9 ? 0 : 1;
       int idx = 0, qs = 0;
       int ps[2] = {0, 0};                  // halves of each stream since the start
