@@ -161,6 +161,14 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
   return sum;
 }
 
+// What the beginning and the end of a unit cost a CTA (its q rows, the first
+// scores, the output), in tiles of its kernel: the shares count it, or a CTA
+// with many short units would finish late.  Measured on eight units of one
+// tile: 6 us each where a tile of 128 keys takes 1.5 us, about 2 us with the
+// tiles of 64 keys.
+template <int KT>
+__host__ __device__ constexpr int kBegin() { return KT == 128 ? 4 : 1; }
+
 // One request as the kernels see it.  A request with a bad length is latched
 // and has no work.  Its rows are cut into mts units of tpm tokens per kv-head.
 template <int KT>
@@ -168,18 +176,19 @@ struct Req {
   int len, n, f, lo, mts;
   bool chain;
 
-  // Tiles of unit mt, counted from key lo: up to the last key that a row may see.
-  __device__ int tiles(int mt, int tpm) const {
-    return (len - lo + (chain ? min(n, (mt + 1) * tpm) : n) + KT - 1) / KT;
+  // Places of unit mt in the list: kBegin<KT>() for its beginning, then its
+  // tiles, counted from key lo, up to the last key that a row may see.
+  __device__ int places(int mt, int tpm) const {
+    return kBegin<KT>() + (len - lo + (chain ? min(n, (mt + 1) * tpm) : n) + KT - 1) / KT;
   }
-  // Tiles of the units before mt.
+  // Places of the units before mt.
   __device__ long long before(int mt, int tpm) const {
     if (mt == 0) return 0;
-    if (!chain) return (long long)mt * tiles(0, tpm);
-    return floor_sum(mt, KT, tpm, (long long)(len - lo) + tpm + KT - 1);
+    if (!chain) return (long long)mt * places(0, tpm);
+    return (long long)mt * kBegin<KT>() + floor_sum(mt, KT, tpm, (long long)(len - lo) + tpm + KT - 1);
   }
   __device__ long long per_head(int tpm) const {
-    return n ? before(mts - 1, tpm) + tiles(mts - 1, tpm) : 0;
+    return n ? before(mts - 1, tpm) + places(mts - 1, tpm) : 0;
   }
 };
 template <int KT>
@@ -229,7 +238,7 @@ struct Walk {
   Req<KT> q;
   long long at, end, W;                    // list positions, length of the list
   int C;                                   // CTAs with a share
-  int r, h, mt, ta;
+  int r, h, mt, ta;                        // ta: the next place of the unit
 
   // Finds the share (all threads of the block; a barrier inside).  False: no work.
   __device__ bool begin(const TreeArgs& a, long long* s_warp, long long* s_base, int* s_r) {
@@ -274,7 +283,7 @@ struct Walk {
   // The next piece with work; false at the end of the share.
   __device__ bool next(const TreeArgs& a, Piece& p) {
     while (at < end) {
-      const int all = q.tiles(mt, a.tpm);
+      const int all = q.places(mt, a.tpm);
       const int t0 = ta, t1 = (int)min((long long)all, ta + (end - at));
       const long long unit_end = at - ta + all;
       const int lo = q.lo;                 // (q may move on below)
@@ -290,9 +299,9 @@ struct Walk {
       p.all_see = q.len + (q.chain ? p.tok0 + 1 : 0);
       p.far_pos = q.len + (q.chain ? p.tok0 + p.ntok : q.n) - 1;
       // tiles that lie before the window of every row have no work
-      int skip = 0;
+      int skip = kBegin<KT>();
       if (a.window > 0 && q.chain)
-        skip = max(0, (q.len + p.tok0 - a.window + 1 - q.lo) / KT);
+        skip += max(0, (q.len + p.tok0 - a.window + 1 - q.lo) / KT);
       at += t1 - t0;
       ta = t1;
       if (t1 == all) {
@@ -310,7 +319,7 @@ struct Walk {
       }
       const int from = max(t0, skip);
       if (from >= t1) continue;
-      p.j0 = lo + from * KT;
+      p.j0 = lo + (from - kBegin<KT>()) * KT;
       p.count = t1 - from;
       p.begins = t0 <= skip;
       p.whole = p.begins && t1 == all;

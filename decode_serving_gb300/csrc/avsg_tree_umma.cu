@@ -263,7 +263,7 @@ __device__ __noinline__ void add_bad_values(const TreeArgs& a, const Piece& s, c
   for (int t = 0; t < s.count; ++t) {
     if (!s.edge<UT>(t, a.window)) continue;
     const int end = min(s.j0 + (t + 1) * UT, s.limit);
-    for (int j = s.j0 + t * UT; j < end; ++j) {
+    for (int j = a.window > 0 ? s.j0 + t * UT : max(s.j0 + t * UT, s.all_see); j < end; ++j) {
       const int page = a.tables[(size_t)s.r * a.max_pages + (j >> a.shift)];
       if (page < 0 || page >= a.num_pages) continue;
       const long long at = ((((long long)page * a.H + s.h) << a.shift) + (j & ((1 << a.shift) - 1))) * D;
@@ -388,19 +388,26 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t to = tmem + lanes + 256 + 128 * x;
     int4 head = make_int4(0, 0, 0, 0);
     int hh = 0, outs = 0, seg = 0, idx = 0;  // hh: halves of this stream since the start
-    // V of tile t, made safe to multiply: see above.  Both streams may do the same tile: they
-    // write the same values.  Its load's number follows those of loads that this tile's scores
-    // needed by less than kRing, so the parity tells its phase.
+    // V of tile t, made safe to multiply: see above.  Rows that every query sees are left alone
+    // (what they hold reaches every query anyway), which without a window are all but the new
+    // tokens'.  Both streams may do the same tile: they write the same values.  Its load's number
+    // follows those of loads that this tile's scores needed by less than kRing, so the parity
+    // tells its phase.
     auto clean_v = [&](const Piece& s, bool two, int t) {
       const int n = idx + v_place(two, t, s.count), b = n % kRing;
+      const int j = s.j0 + t * UT, rows = min(UT, s.limit - j);
+      const int from = a.window > 0 ? 0 : max(0, s.all_see - j);
       bar_wait(full(b), (n / kRing) & 1, give_up, a.err);
       unsigned char* v = smem_raw + M::RING + b * M::TILE;
-      const int rows = min(UT, s.limit - s.j0 - t * UT);
       bool bad = false;
-#pragma unroll 4
-      for (int y = row; y < M::TILE / 16; y += UM) {
-        const int vr = y / (64 * COLS) * 8 + (y / 8) % 8;  // 8 chunks a row of an atom
-        uint4* at = reinterpret_cast<uint4*>(v + y * 16);
+      for (int y = from * (D / 8) + row; y < UT * (D / 8); y += UM) {
+        const int vr = y / (D / 8), ch = y % (D / 8);  // row, 16-byte chunk of it (of any order)
+        uint4* at = reinterpret_cast<uint4*>(v + (vr / 8) * (1024 * COLS) + (ch / 8) * 1024 + (vr & 7) * 128 +
+                                             (ch & 7) * 16);
+        if (vr >= rows) {
+          *at = make_uint4(0u, 0u, 0u, 0u);
+          continue;
+        }
         uint4 c = *at;
         uint32_t e[4] = {c.x, c.y, c.z, c.w};
         bool here = false;
@@ -411,9 +418,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (not_finite<T>(e[z] & 0xffff0000u)) e[z] &= 0xffffu;
             here = true;
           }
-        if (vr >= rows) *at = make_uint4(0u, 0u, 0u, 0u);
-        else if (here) *at = make_uint4(e[0], e[1], e[2], e[3]);
-        bad |= here && vr < rows;
+        if (here) {
+          *at = make_uint4(e[0], e[1], e[2], e[3]);
+          bad = true;
+        }
       }
       if (bad) s_bad[seg & 1] = 1;
       async_fence();
@@ -467,6 +475,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         warp_arrive(q_full(x), lane);
       }
 
+      if (tid == 0) {                      // the next piece, while the first scores are on their way
+        s_bad[(seg + 1) & 1] = 0;
+        s_more[(seg + 1) & 1] = s_walk.next(a, s_piece[(seg + 1) & 1]);
+      }
       float m = -INFINITY, l = 0.f;
       const bool warp_live = rl - lane < s.ntok * a.G;
       const int halves = 2 * (two ? s.count : (s.count - x + 1) >> 1);
@@ -703,10 +715,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         }
       }
       idx += 2 * s.count;
-      if (tid == 0) {
-        s_bad[(seg + 1) & 1] = 0;
-        s_more[(seg + 1) & 1] = s_walk.next(a, s_piece[(seg + 1) & 1]);
-      }
       if (!s.whole && s.begins) head = make_int4(s.last - cta + 1, s.f + s.tok0, s.h, s.ntok * a.G);
       tc_fence_before();
       __syncwarp();
