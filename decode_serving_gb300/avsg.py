@@ -184,13 +184,13 @@ SIGNATURES = {
     "avsg_cuda_error": [_P],
     "avsg_attention_noalloc": [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P,
                                _P, _P, ctypes.c_float, _P],
-    "avsg_page_plan": [ctypes.POINTER(avsg_pages), _P, _P, _I32, _P, _P, _P, _P, _P],
+    "avsg_page_plan": [ctypes.POINTER(avsg_pages), _P, _P, _I32, _I32, _P, _P, _P, _P, _P],
     "avsg_rotary_frequencies": [_I32] + [ctypes.c_double] * 5 + [_P],
     "avsg_rotary_write": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_rotary), _P],
     "avsg_tree_attention_workspace": [ctypes.POINTER(avsg_pages), _I32, _I32,
                                       ctypes.POINTER(ctypes.c_size_t)],
     "avsg_tree_attention": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_tree), _P],
-    "avsg_tree_keep": [ctypes.POINTER(avsg_pages), _P, _P, _P, _P, _P, _P],
+    "avsg_tree_keep": [ctypes.POINTER(avsg_pages), _P, _P, _I32, _P, _P, _P, _P],
     "avsg_read_rows": [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, _I32, _P, _P],
 }
 
@@ -334,9 +334,9 @@ def avsg_read_rows(src, num_rows, row_bytes, d_idx, n, d_sink, ctas=0, stream=0)
                                          int(ctas), d_sink, stream or None), "avsg_read_rows")
 
 
-def avsg_page_plan(pages: avsg_pages, d_new, d_mask, capacity, d_first, d_slot, d_pos,
+def avsg_page_plan(pages: avsg_pages, d_new, d_mask, num_mask, capacity, d_first, d_slot, d_pos,
                    d_free_count_out, stream=0) -> None:
-    _check(load_library().avsg_page_plan(pages, d_new, d_mask or None, capacity, d_first,
+    _check(load_library().avsg_page_plan(pages, d_new, d_mask or None, num_mask, capacity, d_first,
                                          d_slot or None, d_pos or None, d_free_count_out,
                                          stream or None), "avsg_page_plan")
 
@@ -368,9 +368,9 @@ def avsg_tree_attention(pages: avsg_pages, args: avsg_tree, stream=0) -> None:
     _check(load_library().avsg_tree_attention(pages, args, stream or None), "avsg_tree_attention")
 
 
-def avsg_tree_keep(pages: avsg_pages, d_first, d_path, d_keep, d_len_out, d_free_count_out,
+def avsg_tree_keep(pages: avsg_pages, d_first, d_path, num_path, d_keep, d_len_out, d_free_count_out,
                    stream=0) -> None:
-    _check(load_library().avsg_tree_keep(pages, d_first, d_path or None, d_keep, d_len_out,
+    _check(load_library().avsg_tree_keep(pages, d_first, d_path or None, num_path, d_keep, d_len_out,
                                          d_free_count_out, stream or None), "avsg_tree_keep")
 
 

@@ -12,13 +12,15 @@
 // step whose drafts are all rejected leaves the stack as it found it.
 //
 // What bounds them: latency.  A plan of 8 requests moves under 200 bytes, one
-// of 100 000 tokens under 2 MB.  Hence one launch of one cluster (1 to 8 CTAs,
-// by the tokens): every CTA scans all lengths itself (a few loads a thread
-// that hit the L2) instead of waiting for a scan kernel, checks everything,
-// and after one hardware cluster barrier writes its share of the tokens.  The
-// barrier also separates every read of the free count and the lengths from
-// their writes, so the outputs may alias the inputs.  No CTA writes anything
-// unless all checks pass.
+// of 100 000 tokens under 2 MB.  Hence no scan kernel before them: every CTA
+// scans all lengths itself (a few loads a thread that hit the L2), checks
+// everything, so that all decide alike, and writes its share.  No CTA writes
+// anything unless all checks pass.
+// The outputs may alias the inputs.  The plan writes only one word that others
+// read, the free count: its CTAs count themselves as they finish (in the error
+// array's fourth word, which wraps to 0), and the last one writes it.  The
+// keep also writes lengths and the stack: it is one cluster of up to 8 CTAs,
+// whose hardware barriers separate reads from writes.
 #include <cooperative_groups.h>
 
 #include "avsg_paged.cuh"
@@ -29,7 +31,7 @@ namespace avsg {
 namespace {
 
 constexpr int kPlanThreads = 512;
-constexpr int kPlanTokensPerCta = 2048;  // tokens a CTA takes before another one is added
+constexpr int kPlanTokensPerCta = 2048;  // tokens per CTA: one round of 4 a thread
 constexpr int kPlanCluster = 8;
 
 // Largest r with start[r] <= x, start non-decreasing, start[0] = 0, x < start[n].
@@ -44,7 +46,8 @@ __device__ __forceinline__ int find_request(const int32_t* start, int n, int x) 
 }
 
 struct PlanArgs {
-  int R, shift, max_pages, num_pages, capacity;
+  int R, shift, max_pages, num_pages, capacity, num_mask;
+  int wide;                      // slot and pos are 16-byte aligned
   const int32_t* len;
   const int32_t* fresh;
   const unsigned long long* mask;
@@ -64,8 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
   int32_t* s_first = s_req;
   int32_t* s_base = s_req + a.R + 1;
   int32_t* s_len = s_base + a.R;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int rank = blockIdx.x, ctas = gridDim.x;
   const int tid = threadIdx.x;
   griddep_wait();
   bool ok = load_err(a.err) == 0;
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
   } else if (tid == 0 && (count < 0 || count > a.num_pages)) {
     bad = AVSG_ERR_BAD_SELECTION;
     if (rank == 0) raise_error(a.err, bad, -1, -1);
-  } else if (tid == 0 && (total_pages > count || total_tokens > a.capacity)) {
+  } else if (tid == 0 && (total_pages > count || total_tokens > a.capacity || (a.mask && total_tokens > a.num_mask))) {
     bad = AVSG_ERR_CAPACITY;
     if (rank == 0) raise_error(a.err, bad, -1, -1);
   }
@@ -131,40 +133,59 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
     }
   }
   ok = !__syncthreads_or(!ok || bad);
-  cluster.sync();  // every CTA has read what the writes below may alias
   griddep_launch();
+  // Everything that may alias the count has been read by this CTA; the last one writes it.
+  if (tid == 0) {
+    __threadfence();
+    if (atomicInc(reinterpret_cast<unsigned*>(&a.err->aux), (unsigned)ctas - 1) == (unsigned)ctas - 1 && ok)
+      *a.count_out = count - (int)total_pages;
+  }
   if (!ok) return;
 
   for (int r = rank * kPlanThreads + tid; r <= a.R; r += ctas * kPlanThreads) a.first[r] = s_first[r];
-  if (rank == 0 && tid == 0) *a.count_out = count - (int)total_pages;
-  for (int t = rank * kPlanThreads + tid; t < a.capacity; t += ctas * kPlanThreads) {
-    int32_t slot = -1, pos = 0;
-    if (t < (int)total_tokens) {
-      const int r = find_request(s_first, a.R, t);
+  for (long long t4 = 4LL * (rank * kPlanThreads + tid); t4 < a.capacity; t4 += 4LL * ctas * kPlanThreads) {
+    int32_t slot[4], pos[4];
+    int r = t4 < total_tokens ? find_request(s_first, a.R, (int)t4) : a.R;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int t = (int)t4 + x;
+      slot[x] = -1;
+      pos[x] = 0;
+      if (t >= (int)total_tokens) continue;
+      while (t >= s_first[r + 1]) ++r;
       const int i = t - s_first[r], len = s_len[r], p = len + i;
-      const int held = (len + page_mask) >> a.shift, x = p >> a.shift;
+      const int held = (len + page_mask) >> a.shift, at = p >> a.shift;
       int32_t* row = a.tables + (size_t)r * a.max_pages;
       int32_t page;
-      if (x < held) {
-        page = row[x];
+      if (at < held) {
+        page = row[at];
       } else {
-        page = a.free_list[count - 1 - (s_base[r] + x)];
-        if ((p & page_mask) == 0) row[x] = page;
+        page = a.free_list[count - 1 - (s_base[r] + at)];
+        if ((p & page_mask) == 0) row[at] = page;
       }
-      slot = (page << a.shift) + (p & page_mask);
-      pos = p;
+      slot[x] = (page << a.shift) + (p & page_mask);
+      pos[x] = p;
       if (a.mask) {
         const unsigned long long m = a.mask[t];
-        if (m) pos = len + __popcll(m) - 1;
+        if (m) pos[x] = len + __popcll(m) - 1;
       }
     }
-    a.slot[t] = slot;
-    a.pos[t] = pos;
+    if (a.wide && t4 + 4 <= a.capacity) {
+      *reinterpret_cast<int4*>(a.slot + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.pos + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (t4 + x < a.capacity) {
+          a.slot[t4 + x] = slot[x];
+          a.pos[t4 + x] = pos[x];
+        }
+    }
   }
 }
 
 struct KeepArgs {
-  int R, shift, max_pages, num_pages;
+  int R, shift, max_pages, num_pages, num_path;
   const int32_t* first;
   const int32_t* path;
   const int32_t* keep;
@@ -201,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) keep_lengths_kernel(KeepArgs a) 
     const long long need = (len + n + page_mask) >> a.shift;
     int code = 0;
     if (len < 0 || f < 0 || n < 0 || k < -1 || k > n) code = AVSG_ERR_BAD_SELECTION;
-    else if (need > a.max_pages) code = AVSG_ERR_CAPACITY;
+    else if (need > a.max_pages || (a.path && f + n > a.num_path)) code = AVSG_ERR_CAPACITY;
     if (code && !bad) {
       bad = code;
       bad_r = r;
@@ -357,12 +378,12 @@ SmemLimit g_plan_smem, g_keep_smem;
 using namespace avsg;
 
 extern "C" int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const uint64_t* d_mask,
-                              int32_t capacity, int32_t* d_first, int32_t* d_slot, int32_t* d_pos,
+                              int32_t num_mask, int32_t capacity, int32_t* d_first, int32_t* d_slot, int32_t* d_pos,
                               int32_t* d_free_count_out, void* stream) {
   int rc = check_pages(p);
   if (rc != AVSG_OK) return rc;
   if (!d_new || !d_first || capacity < 0 || (capacity > 0 && (!d_slot || !d_pos)) ||
-      !d_free_count_out)
+      !d_free_count_out || num_mask < 0)
     return AVSG_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   rc = paged_device(p->d_tables, &dev, &sms);
@@ -373,6 +394,8 @@ extern "C" int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const u
   a.max_pages = p->max_pages;
   a.num_pages = p->num_pages;
   a.capacity = capacity;
+  a.num_mask = num_mask;
+  a.wide = (reinterpret_cast<uintptr_t>(d_slot) | reinterpret_cast<uintptr_t>(d_pos)) % 16 == 0;
   a.len = p->d_len;
   a.fresh = d_new;
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
@@ -385,20 +408,21 @@ extern "C" int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const u
   a.pos = d_pos;
   a.err = reinterpret_cast<DevErr*>(p->d_error);
   const size_t smem = (3 * (size_t)a.R + 1) * sizeof(int32_t);
-  const int ctas = cluster_for(capacity);
+  // (no more CTAs than SMs: each one scans the lengths)
+  const int64_t want = ((int64_t)capacity + kPlanTokensPerCta - 1) / kPlanTokensPerCta;
+  const int ctas = want < 1 ? 1 : want < sms ? (int)want : sms;
   cudaError_t e = g_plan_smem.raise(reinterpret_cast<const void*>(page_plan_kernel), smem, dev);
   if (e == cudaSuccess)
-    e = launch_pdl_cluster(ctas, page_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem,
-                           static_cast<cudaStream_t>(stream), a);
+    e = launch_pdl(page_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream), a);
   return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
 }
 
 extern "C" int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const int32_t* d_path,
-                              const int32_t* d_keep, int32_t* d_len_out,
+                              int32_t num_path, const int32_t* d_keep, int32_t* d_len_out,
                               int32_t* d_free_count_out, void* stream) {
   int rc = check_pages(p);
   if (rc != AVSG_OK) return rc;
-  if (!d_first || !d_keep || !d_len_out || !d_free_count_out) return AVSG_ERR_INVALID_ARG;
+  if (!d_first || !d_keep || !d_len_out || !d_free_count_out || num_path < 0) return AVSG_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   rc = paged_device(p->d_tables, &dev, &sms);
   if (rc != AVSG_OK) return rc;
@@ -408,6 +432,7 @@ extern "C" int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const
   a.shift = page_shift_of(p->page_tokens);
   a.max_pages = p->max_pages;
   a.num_pages = p->num_pages;
+  a.num_path = num_path;
   a.first = d_first;
   a.path = d_path;
   a.keep = d_keep;

@@ -13,10 +13,10 @@
 //
 // What bounds it: bytes.  q, k and v are read once and written once; the
 // angles of a token are computed once per CTA into shared memory and used by
-// all its heads.  A thread owns one place of one head (the two chunks of a
-// pair group, 16 bytes each where widths and alignment allow) for the CTA's
-// tokens, so that the index arithmetic is paid once for several loads, which
-// are all in flight before the first is used.
+// all its heads.  A thread owns one place of one head -- two chunks of 16
+// bytes where widths and alignment allow: the two halves of pairs, or
+// neighbours -- for the CTA's tokens, so that the index arithmetic is paid
+// once for several loads, all in flight before the first is used.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,14 +25,14 @@
 namespace avsg {
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 256;  // at most
 constexpr int kRotTokens = 4;    // tokens per CTA of a long call
 constexpr int kMaxRot = 1024;
 
 struct RotArgs {
   int T, Hq, H, G, D, rot, offset, interleaved, n_tok, shift, num_pages;
   int unit_heads;                // heads of q, k and v together
-  int per_head;                  // units of one head: pair groups, then plain chunks
+  int per_head;                  // places of one head: pair groups, then plain chunks
   long long q_stride, k_stride, v_stride;
   float magnitude;
   const void* q;
@@ -88,7 +88,7 @@ __device__ __forceinline__ void store_vec(TO* p, const float* x) {
 // T: type of q, k, v and the cache; TQ: type of q_out; VEC: values per chunk;
 // TOK: tokens per CTA.
 template <typename T, typename TQ, int VEC, int TOK>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotArgs a) {
   extern __shared__ float2 s_cs[];            // [TOK][rot / 2] cos, sin
   const int tid = threadIdx.x, half = a.rot >> 1;
   const int t0 = blockIdx.x * TOK;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
       slot[j] = -1;
     }
   }
-  for (int x = tid; x < TOK * half; x += kRotThreads) {
+  for (int x = tid; x < TOK * half; x += blockDim.x) {
     const int j = x / half, i = x - j * half, t = t0 + j;
     if (t >= a.T) break;
     const unsigned long long turn = (unsigned long long)(long long)a.pos[t] * a.freq[i];
@@ -115,35 +115,37 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
   __syncthreads();
   griddep_launch();
 
-  const int pair_units = half / VEC;
+  const int groups = half / VEC;
   const int units = a.unit_heads * a.per_head;
-  for (int u = blockIdx.y * kRotThreads + tid; u < units; u += gridDim.y * kRotThreads) {
+  for (int u = blockIdx.y * blockDim.x + tid; u < units; u += gridDim.y * blockDim.x) {
     const int head = u / a.per_head, w = u - head * a.per_head;
     const bool is_v = head >= a.Hq + a.H, is_q = head < a.Hq;
     const int hh = is_q ? head : is_v ? head - a.Hq - a.H : head - a.Hq;
     const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
     const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-    // values d0 .. and d1 .. of the head (d1 < 0: one plain chunk)
-    int d0, d1 = -1;
-    const bool turns = w < pair_units;
-    if (is_v) {
-      d0 = w * VEC;
-      if (w >= a.D / VEC) continue;           // a v head has one plain chunk per unit
-    } else if (turns) {
+    // values d0 .. and d1 .. of the head (d1 < 0: one chunk alone)
+    const bool turns = !is_v && w < groups;
+    int d0, d1;
+    if (turns) {
       d0 = a.offset + (a.interleaved ? 2 * w * VEC : w * VEC);
       d1 = a.interleaved ? d0 + VEC : d0 + half;
     } else {
-      d0 = (w - pair_units) * VEC;            // the part that keeps its values
-      if (d0 >= a.offset) d0 += a.rot;
-      if (d0 >= a.D) continue;
+      // neighbouring chunks of what keeps its values
+      const int rot = is_v ? 0 : a.rot, c = 2 * (is_v ? w : w - groups);
+      d0 = c * VEC;
+      d1 = d0 + VEC;
+      if (d0 >= a.D - rot) continue;
+      if (d1 >= a.D - rot) d1 = -1;
+      if (rot && d0 >= a.offset) d0 += rot;
+      if (rot && d1 >= a.offset) d1 += rot;
     }
     Vec<T, VEC> x0[TOK], x1[TOK];
 #pragma unroll
     for (int j = 0; j < TOK; ++j) {
       if (slot[j] < 0) continue;
       const T* p = src + (t0 + j) * stride + (long long)hh * a.D;
-      x0[j].raw = *reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d0);
-      if (d1 >= 0) x1[j].raw = *reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d1);
+      x0[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d0));
+      if (d1 >= 0) x1[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d1));
     }
 #pragma unroll
     for (int j = 0; j < TOK; ++j) {
@@ -151,15 +153,18 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
       const int t = t0 + j;
       float y0[VEC], y1[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) y0[i] = to_f(x0[j].x[i]);
-      if (d1 >= 0) {
+      for (int i = 0; i < VEC; ++i) {
+        y0[i] = to_f(x0[j].x[i]);
+        y1[i] = to_f(x1[j].x[i]);
+      }
+      if (turns) {
         const float2* cs = s_cs + j * half + w * VEC;
         if (a.interleaved) {
           float z[2 * VEC];
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             z[i] = y0[i];
-            z[VEC + i] = to_f(x1[j].x[i]);
+            z[VEC + i] = y1[i];
           }
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             const float2 c = cs[i];
-            const float p = y0[i], q = to_f(x1[j].x[i]);
+            const float p = y0[i], q = y1[i];
             y0[i] = p * c.x - q * c.y;
             y1[i] = p * c.y + q * c.x;
           }
@@ -195,8 +200,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
         const long long row =
             ((((long long)(slot[j] >> a.shift) * a.H + hh) << a.shift) + (slot[j] & ((1 << a.shift) - 1)));
         T* o = static_cast<T*>(is_v ? a.vp : a.kp) + row * a.D;
-        if (is_v || d1 < 0) {                 // unchanged bits
+        if (!turns) {                         // unchanged bits
           *reinterpret_cast<typename Chunk<2 * VEC>::type*>(o + d0) = x0[j].raw;
+          if (d1 >= 0) *reinterpret_cast<typename Chunk<2 * VEC>::type*>(o + d1) = x1[j].raw;
         } else {
           store_vec<T, VEC>(o + d0, y0);
           store_vec<T, VEC>(o + d1, y1);
@@ -209,21 +215,23 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotArgs a) {
 template <typename T, typename TQ, int VEC>
 cudaError_t launch_rotary(const RotArgs& in, int sms, cudaStream_t st) {
   RotArgs a = in;
-  // v heads have D / VEC plain chunks, q and k heads fewer units: one count for all
-  const int qk = a.rot / 2 / VEC + (a.D - a.rot) / VEC;
-  a.per_head = a.D / VEC > qk ? a.D / VEC : qk;
+  const int qk = a.rot / 2 / VEC + ((a.D - a.rot) / VEC + 1) / 2, v = (a.D / VEC + 1) / 2;
+  a.per_head = v > qk ? v : qk;
   const int units = a.unit_heads * a.per_head;
+  // as many threads as share the places evenly
+  const int rounds = (units + kRotThreads - 1) / kRotThreads;
+  const int threads = ((units + rounds - 1) / rounds + 31) / 32 * 32;
   // Several tokens per CTA only when there are enough for every SM to hold
   // four CTAs; short calls spread a token's heads over CTAs instead.
   const bool many = a.T >= kRotTokens * 4 * sms;
   const int tok = many ? kRotTokens : 1;
   const int ctas = (a.T + tok - 1) / tok;
-  int split = (units + kRotThreads - 1) / kRotThreads;
+  int split = rounds;
   const int most = (4 * sms + ctas - 1) / ctas;
   if (split > most) split = most;
   const size_t smem = (size_t)tok * (a.rot / 2) * sizeof(float2);
-  if (many) return launch_pdl(rotary_kernel<T, TQ, VEC, kRotTokens>, dim3(ctas, split), dim3(kRotThreads), smem, st, a);
-  return launch_pdl(rotary_kernel<T, TQ, VEC, 1>, dim3(ctas, split), dim3(kRotThreads), smem, st, a);
+  if (many) return launch_pdl(rotary_kernel<T, TQ, VEC, kRotTokens>, dim3(ctas, split), dim3(threads), smem, st, a);
+  return launch_pdl(rotary_kernel<T, TQ, VEC, 1>, dim3(ctas, split), dim3(threads), smem, st, a);
 }
 
 template <typename T, typename TQ>

@@ -8,12 +8,19 @@ and devices are checked here (``ValueError``), the rest by the library
 """
 from __future__ import annotations
 
+import ctypes
+import struct
+
 import numpy as np
 import torch
 
 from . import avsg as C
 
 _TYPES = {torch.bfloat16: C.AVSG_BF16, torch.float16: C.AVSG_F16}
+# The argument structures as bytes: a third of the time that filling them field by field takes.
+_ROTARY = struct.Struct("8i3qfi7P")
+_TREE = struct.Struct("5i2fiq7PN")
+assert _ROTARY.size == ctypes.sizeof(C.avsg_rotary) and _TREE.size == ctypes.sizeof(C.avsg_tree)
 
 
 def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_turns=32.0,
@@ -21,6 +28,20 @@ def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_tu
     """The frequency table of ``PagedCache.rotary`` (a host tensor: 64-bit words as int64)."""
     t = C.avsg_rotary_frequencies(rot_dim, base, factor, low_turns, high_turns, original)
     return torch.from_numpy(t[:int(rot_dim) // 2].view(np.int64))
+
+
+_P, _I32 = ctypes.c_void_p, ctypes.c_int32
+_calls = {}
+
+
+def _library():
+    """The entry points by address and packed arguments (the binding's own take the structures)."""
+    if not _calls:
+        lib = C.load_library()
+        for name, args in (("avsg_page_plan", [_P, _P, _P, _I32, _I32] + [_P] * 5), ("avsg_rotary_write", [_P] * 3),
+                           ("avsg_tree_attention", [_P] * 3), ("avsg_tree_keep", [_P, _P, _P, _I32] + [_P] * 4)):
+            _calls[name] = ctypes.CFUNCTYPE(ctypes.c_int, *args)((name, lib))
+    return _calls
 
 
 class PagedCache:
@@ -39,21 +60,27 @@ class PagedCache:
         if k.device.type != "cuda":
             raise ValueError("the cache lives on a CUDA device")
         layers, pages, heads, page, dim = k.shape
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self._index = k.device, k.dtype, k.get_device()
         self.requests, self.kv_heads, self.head_dim = len(lens), heads, dim
         self.k, self.v, self.tables, self.lens = k, v, tables, lens
         self.free, self.free_count = free, free_count
-        self._check("k", k, k.dtype, None)
-        self._check("v", v, k.dtype, None)
-        self._check("tables", tables, torch.int32, (len(lens), tables.shape[-1]))
-        self._check("lens", lens, torch.int32, (len(lens),))
-        self._check("free", free, torch.int32, (pages,))
-        self._check("free_count", free_count, torch.int32, (1,))
+        self._check("k", k, k.dtype, k.numel())
+        self._check("v", v, k.dtype, k.numel())
+        if tables.dim() != 2 or tables.shape[0] != len(lens):
+            raise ValueError("tables: [requests][max_pages] is wanted")
+        self._check("tables", tables, torch.int32, tables.numel())
+        self._check("lens", lens, torch.int32, len(lens))
+        self._check("free", free, torch.int32, pages)
+        self._check("free_count", free_count, torch.int32, 1)
         self._error = torch.zeros(4, dtype=torch.int32, device=k.device)
         self._pages = C.avsg_pages(len(lens), layers, pages, heads, page, dim, tables.shape[1],
                                    _TYPES[k.dtype], k.data_ptr(), v.data_ptr(), tables.data_ptr(),
                                    lens.data_ptr(), free.data_ptr(), free_count.data_ptr(),
                                    self._error.data_ptr())
+        self._at = ctypes.addressof(self._pages)
+        calls = _library()
+        self._plan, self._rotary = calls["avsg_page_plan"], calls["avsg_rotary_write"]
+        self._attend, self._keep = calls["avsg_tree_attention"], calls["avsg_tree_keep"]
 
     @classmethod
     def allocate(cls, requests, max_pages, num_pages, kv_heads, page_tokens, head_dim, layers=1,
@@ -66,40 +93,53 @@ class PagedCache:
                    torch.zeros(requests, max_pages, **ints), torch.zeros(requests, **ints),
                    torch.arange(num_pages - 1, -1, -1, **ints), torch.full((1,), num_pages, **ints))
 
-    def _check(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or (
-                shape is not None and t.shape != shape):
-            raise ValueError(f"{name}: a contiguous {dtype} tensor on {self.device}"
-                             + (f" of shape {list(shape)}" if shape is not None else "")
-                             + f" is wanted, not {t.dtype} {list(t.shape)} on {t.device}")
+    def _check(self, name, t, dtype, count):
+        """t: contiguous, of this type and this many values, on the cache's device."""
+        if t.dtype is not dtype or t.get_device() != self._index or t.numel() != count or \
+                not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous {dtype} tensor of {count} values on {self.device} "
+                             f"is wanted, not {t.dtype} {list(t.shape)} on {t.device}")
 
-    def _rows(self, name, t, heads):
-        """Token rows of heads * head_dim values with any stride between tokens; the stride."""
-        if t.dtype != self.dtype or t.device != self.device or t.dim() not in (2, 3):
-            raise ValueError(f"{name}: {self.dtype} rows on {self.device} are wanted")
-        width = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
-        inner = t.stride(-1) == 1 and (t.dim() == 2 or t.shape[1] == 1 or t.stride(1) == t.shape[2])
-        if width != heads * self.head_dim or not (inner or t.numel() == 0):
-            raise ValueError(f"{name}: rows of {heads} x {self.head_dim} consecutive values are wanted")
-        return t.stride(0) if t.shape[0] > 1 else width
+    def _rows(self, name, t, width):
+        """Token rows of `width` consecutive values, any stride between tokens; the stride."""
+        if t.dtype is not self.dtype or t.get_device() != self._index:
+            raise ValueError(f"{name}: {self.dtype} rows on {self.device} are wanted, not {t.dtype} "
+                             f"on {t.device}")
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2:
+            ok = shape[1] == width and (stride[1] == 1 or width == 1)
+        else:
+            ok = len(shape) == 3 and shape[1] * shape[2] == width and stride[2] == 1 and (
+                shape[1] == 1 or stride[1] == shape[2])
+        if not ok:
+            raise ValueError(f"{name}: rows of {width} consecutive values are wanted, not "
+                             f"{list(shape)} with strides {list(stride)}")
+        return stride[0] if shape[0] > 1 else width
+
+    def _heads(self, t):
+        """Heads of a row tensor [T][heads * head_dim] or [T][heads][head_dim]."""
+        return t.shape[1] if t.dim() == 3 else t.shape[1] // self.head_dim
 
     def plan(self, new, first, slots, positions, mask=None, free_count_out=None, stream=0):
         """Tables, slots and positions of the step's new tokens.  new [requests],
         first [requests + 1], slots and positions [capacity] int32; mask
         [tokens] int64 words of ancestor bits; free_count_out defaults to the
         cache's own count."""
-        r = self.requests
+        r, capacity = self.requests, slots.numel()
         out = self.free_count if free_count_out is None else free_count_out
-        self._check("new", new, torch.int32, (r,))
-        self._check("first", first, torch.int32, (r + 1,))
-        self._check("slots", slots, torch.int32, (slots.numel(),))
-        self._check("positions", positions, torch.int32, slots.shape)
-        self._check("free_count_out", out, torch.int32, (1,))
+        self._check("new", new, torch.int32, r)
+        self._check("first", first, torch.int32, r + 1)
+        self._check("slots", slots, torch.int32, capacity)
+        self._check("positions", positions, torch.int32, capacity)
+        self._check("free_count_out", out, torch.int32, 1)
+        masks = 0
         if mask is not None:
-            self._check("mask", mask, torch.int64, (mask.numel(),))
-        C.avsg_page_plan(self._pages, new.data_ptr(), 0 if mask is None else mask.data_ptr(),
-                         slots.numel(), first.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-                         out.data_ptr(), stream)
+            masks = mask.numel()
+            self._check("mask", mask, torch.int64, masks)
+        rc = self._plan(self._at, new.data_ptr(), None if mask is None else mask.data_ptr(), masks, capacity,
+                        first.data_ptr(), slots.data_ptr(), positions.data_ptr(), out.data_ptr(), stream or None)
+        if rc:
+            raise C.AvsgError(rc, "avsg_page_plan")
 
     def rotary(self, q, k, v, positions, slots, freq, q_out, layer=0, rot_offset=0,
                interleaved=False, magnitude=1.0, tokens_per_request=1, stream=0):
@@ -109,25 +149,24 @@ class PagedCache:
         with kv_heads, any stride between tokens; slots [T] or None (slot t for
         token t); freq from ``rotary_frequencies``, on the device; q_out
         contiguous, the cache's type or float32."""
-        tokens = q.shape[0]
-        heads = q.shape[1] // self.head_dim if q.dim() == 2 else q.shape[1]
-        qs, ks, vs = self._rows("q", q, heads), self._rows("k", k, self.kv_heads), \
-            self._rows("v", v, self.kv_heads)
+        tokens, heads, dim = q.shape[0], self._heads(q), self.head_dim
+        kv = self.kv_heads * dim
+        qs, ks, vs = self._rows("q", q, heads * dim), self._rows("k", k, kv), self._rows("v", v, kv)
         if k.shape[0] != tokens or v.shape[0] != tokens:
             raise ValueError("q, k and v have one row per token")
-        f32 = q_out.dtype == torch.float32
-        self._check("q_out", q_out, torch.float32 if f32 else self.dtype, None)
-        if q_out.numel() != tokens * heads * self.head_dim:
-            raise ValueError("q_out: as many values as q has")
-        self._check("positions", positions, torch.int32, (tokens,))
-        self._check("freq", freq, torch.int64, (freq.numel(),))
+        f32 = q_out.dtype is torch.float32
+        pairs = freq.numel()
+        self._check("q_out", q_out, torch.float32 if f32 else self.dtype, tokens * heads * dim)
+        self._check("positions", positions, torch.int32, tokens)
+        self._check("freq", freq, torch.int64, pairs)
         if slots is not None:
-            self._check("slots", slots, torch.int32, (tokens,))
-        C.avsg_rotary_write(self._pages, C.avsg_rotary(
-            tokens, heads, 2 * freq.numel(), rot_offset, int(interleaved), int(f32),
-            tokens_per_request, layer, qs, ks, vs, magnitude, 0, q.data_ptr(), k.data_ptr(),
-            v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
-            0 if slots is None else slots.data_ptr(), q_out.data_ptr()), stream)
+            self._check("slots", slots, torch.int32, tokens)
+        rc = self._rotary(self._at, _ROTARY.pack(
+            tokens, heads, 2 * pairs, rot_offset, interleaved, f32, tokens_per_request, layer, qs, ks, vs,
+            magnitude, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
+            0 if slots is None else slots.data_ptr(), q_out.data_ptr()), stream or None)
+        if rc:
+            raise C.AvsgError(rc, "avsg_rotary_write")
 
     def attention_workspace(self, q_per_kv, max_new) -> torch.Tensor:
         """Scratch of ``attend``; calls that may overlap need one each."""
@@ -142,27 +181,28 @@ class PagedCache:
         contiguous, lse [T][q_heads] float32 or None; first from ``plan``;
         max_new bounds every request's new tokens; mask [tokens] int64 words
         (None: chains); slopes [q_heads] float32 or None."""
-        heads = q.shape[1] // self.head_dim if q.dim() == 2 else q.shape[1]
-        stride = self._rows("q", q, heads)
-        tokens = q.shape[0]
+        tokens, heads, dim = q.shape[0], self._heads(q), self.head_dim
+        stride = self._rows("q", q, heads * dim)
         if heads % self.kv_heads:
             raise ValueError("q: a multiple of the cache's heads is wanted")
-        self._check("out", out, self.dtype, None)
-        if out.numel() != tokens * heads * self.head_dim:
-            raise ValueError("out: as many values as q has")
-        self._check("first", first, torch.int32, (self.requests + 1,))
-        self._check("work", work, torch.uint8, None)
+        self._check("out", out, self.dtype, tokens * heads * dim)
+        self._check("first", first, torch.int32, self.requests + 1)
+        size = work.numel()
+        self._check("work", work, torch.uint8, size)
         if mask is not None:
-            self._check("mask", mask, torch.int64, (mask.numel(),))
+            if mask.numel() < tokens:
+                raise ValueError("mask: a word per row of q is wanted")
+            self._check("mask", mask, torch.int64, mask.numel())
         if lse is not None:
-            self._check("lse", lse, torch.float32, (tokens, heads))
+            self._check("lse", lse, torch.float32, tokens * heads)
         if slopes is not None:
-            self._check("slopes", slopes, torch.float32, (heads,))
-        C.avsg_tree_attention(self._pages, C.avsg_tree(
-            tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride,
-            q.data_ptr(), first.data_ptr(), 0 if mask is None else mask.data_ptr(),
-            0 if slopes is None else slopes.data_ptr(), out.data_ptr(),
-            0 if lse is None else lse.data_ptr(), work.data_ptr(), work.numel()), stream)
+            self._check("slopes", slopes, torch.float32, heads)
+        rc = self._attend(self._at, _TREE.pack(
+            tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
+            first.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if slopes is None else slopes.data_ptr(),
+            out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size), stream or None)
+        if rc:
+            raise C.AvsgError(rc, "avsg_tree_attention")
 
     def keep(self, first, path, keep, lens_out=None, free_count_out=None, stream=0):
         """Keeps the accepted drafts of every layer and frees the pages past the
@@ -171,14 +211,18 @@ class PagedCache:
         r = self.requests
         lens = self.lens if lens_out is None else lens_out
         count = self.free_count if free_count_out is None else free_count_out
-        self._check("first", first, torch.int32, (r + 1,))
-        self._check("keep", keep, torch.int32, (r,))
-        self._check("lens_out", lens, torch.int32, (r,))
-        self._check("free_count_out", count, torch.int32, (1,))
+        self._check("first", first, torch.int32, r + 1)
+        self._check("keep", keep, torch.int32, r)
+        self._check("lens_out", lens, torch.int32, r)
+        self._check("free_count_out", count, torch.int32, 1)
+        paths = 0
         if path is not None:
-            self._check("path", path, torch.int32, (path.numel(),))
-        C.avsg_tree_keep(self._pages, first.data_ptr(), 0 if path is None else path.data_ptr(),
-                         keep.data_ptr(), lens.data_ptr(), count.data_ptr(), stream)
+            paths = path.numel()
+            self._check("path", path, torch.int32, paths)
+        rc = self._keep(self._at, first.data_ptr(), None if path is None else path.data_ptr(), paths,
+                        keep.data_ptr(), lens.data_ptr(), count.data_ptr(), stream or None)
+        if rc:
+            raise C.AvsgError(rc, "avsg_tree_keep")
 
     def error(self):
         """(code, request, position) of the first latched device error, code 0

@@ -356,7 +356,7 @@ int avsg_read_rows(const void* src, int64_t num_rows, int64_t row_bytes, const i
  *
  * Errors.  Host checks return a code and enqueue nothing.  What only the
  * device can see (a page id outside the pool, too few free pages, a path that
- * is not increasing) is latched in d_error = {code, request, position, 0}; the
+ * is not increasing) is latched in d_error = {code, request, position}; the
  * first error stays, and every later call on the same d_error does nothing on
  * the device until the caller zeroes it.  All memory is the caller's, on the
  * current device (INVALID_ARG for pages of another one), and must stay valid
@@ -381,13 +381,13 @@ typedef struct avsg_pages {
   int32_t* d_len;       /* [R] committed tokens */
   int32_t* d_free;      /* [num_pages] stack of free page ids */
   int32_t* d_free_count;/* [1] */
-  int32_t* d_error;     /* [4], zeroed by the caller at first, 16-byte aligned */
+  int32_t* d_error;     /* [4], zeroed by the caller at first; the fourth is the library's */
 } avsg_pages;
 
 /*
  * avsg_page_plan -- tables, slots and positions of a step's new tokens.
  *   d_new   : int32 [R], new tokens per request (0 is allowed).
- *   d_mask  : uint64 [tokens] or NULL: ancestors of each draft (see
+ *   d_mask  : uint64 [num_mask] or NULL: ancestors of each draft (see
  *             avsg_tree_attention); position = len + depth, with depth the
  *             number of bits - 1.  NULL or a zero word: len + index.
  *   capacity: entries of d_slot and d_pos.
@@ -397,11 +397,11 @@ typedef struct avsg_pages {
  *   d_free_count_out: int32 [1], may be d_free_count itself.
  * Pages are taken from the top of the stack in request order and entered in
  * d_tables; entries that do not change are not written.  Latched errors
- * (CAPACITY: too few free pages, table columns or entries; BAD_SELECTION: a
+ * (CAPACITY: too few free pages, table columns, entries or masks; BAD_SELECTION: a
  * negative length or a page id outside the pool) leave everything as it was.
  */
 int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const uint64_t* d_mask,
-                   int32_t capacity, int32_t* d_first, int32_t* d_slot, int32_t* d_pos,
+                   int32_t num_mask, int32_t capacity, int32_t* d_first, int32_t* d_slot, int32_t* d_pos,
                    int32_t* d_free_count_out, void* stream);
 
 /*
@@ -508,17 +508,18 @@ int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void* stream);
  *   d_first : as written by the step's avsg_page_plan.
  *   d_keep  : int32 [R]: number of kept new tokens, or -1: the request ends
  *             (its length becomes 0 and all its pages are free).
- *   d_path  : int32 [tokens] or NULL: the kept tokens' indices within their
+ *   d_path  : int32 [num_path] or NULL: the kept tokens' indices within their
  *             request, strictly increasing, at d_path[d_first[r] + i]; NULL
  *             keeps the first d_keep[r].
  * Row len + path[i] moves to len + i in every layer; d_len_out (may be d_len)
  * receives the new lengths; the pages past them return to the stack in the
  * reverse order of taking, and d_free_count_out (may be d_free_count) counts
  * them.  Latched errors (BAD_SELECTION: a bad count, path or page id;
- * CAPACITY: more pages than the pool) leave everything as it was.
+ * CAPACITY: more pages than the pool, or more tokens than num_path) leave
+ * everything as it was.
  */
 int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const int32_t* d_path,
-                   const int32_t* d_keep, int32_t* d_len_out, int32_t* d_free_count_out,
+                   int32_t num_path, const int32_t* d_keep, int32_t* d_len_out, int32_t* d_free_count_out,
                    void* stream);
 
 /* Error text, and the cudaError_t behind the last AVSG_ERR_CUDA of a handle. */

@@ -145,6 +145,16 @@ def test_plan_errors_change_nothing_and_stay(what, code, request_):
         assert b.cache.error()[0] == 0 and (host(b.slots) >= 0).all()
 
 
+def test_plan_and_keep_refuse_short_masks_and_paths():
+    b = Batch([3, 40], 16, room=2, spare=6)
+    b.plan([5, 6], 11, mask=trees([5, 5], 1))                  # 10 words for 11 tokens
+    assert b.cache.error()[0] == -2 and (host(b.slots) == -77).all()
+    b.cache.clear_error()
+    b.plan([5, 6], 11)
+    b.cache.keep(b.first, dev(np.arange(10)), dev(np.array([1, 1])))
+    assert b.cache.error()[:2] == (-2, 1) and (host(b.cache.lens) == b.lens).all()
+
+
 def random_paths(new, kept, seed):
     r = np.random.default_rng(seed)
     out = []

@@ -46,7 +46,7 @@ class Step(Batch):
         self.q = torch.randn(total + extra, heads * groups, dim, generator=gen, device="cuda").to(dtype)
         self.out = torch.full_like(self.q, 3.0)
         self.lse = torch.full((total + extra, heads * groups), 3.0, device="cuda")
-        self.dmask = None if self.mask is None else dev(self.mask, torch.int64)
+        self.dmask = None if self.mask is None else dev(np.pad(self.mask, (0, extra)), torch.int64)
 
     def row(self, r, p):
         """(page, row) of token p of request r."""
@@ -225,7 +225,7 @@ def test_refusals():
     work = s.cache.attention_workspace(2, 2)
     call = lambda **kw: s.cache.attend(**{**dict(q=s.q, first=s.first, out=s.out, max_new=2, work=work), **kw})  # noqa: E731
     for kw in (dict(q=s.q.half()), dict(q=s.q[..., ::2]), dict(out=s.out[:1]), dict(first=s.first[:1]),
-               dict(first=s.first.long()), dict(mask=s.dmask.int()), dict(lse=s.lse[:, :1].contiguous()),
+               dict(first=s.first.long()), dict(mask=s.dmask.int()), dict(mask=s.dmask[:1]), dict(lse=s.lse[:, :1].contiguous()),
                dict(slopes=torch.zeros(3, device="cuda")), dict(q=s.q[:, :3]), dict(out=s.out.cpu())):
         with pytest.raises(ValueError):
             call(**kw)

@@ -41,22 +41,24 @@ BAD_PAGES = [
 def test_bad_pages(lib, kw, code):
     from decode_serving_gb300 import avsg
     p, at = pages(**kw)
-    assert lib.avsg_page_plan(p, at, None, 4, at, at, at, at, None) == code
-    assert lib.avsg_tree_keep(p, at, at, at, at, at, None) == code
+    assert lib.avsg_page_plan(p, at, None, 0, 4, at, at, at, at, None) == code
+    assert lib.avsg_tree_keep(p, at, at, 4, at, at, at, None) == code
     assert lib.avsg_rotary_write(p, avsg.avsg_rotary(), None) == code
 
 
 def test_null_arguments_of_plan_and_keep(lib):
     p, at = pages()
-    good = [at, None, 4, at, at, at, at]
-    for i in (0, 3, 4, 5, 6):
+    good = [at, None, 0, 4, at, at, at, at]
+    for i in (0, 4, 5, 6, 7):
         assert lib.avsg_page_plan(p, *[None if j == i else x for j, x in enumerate(good)], None) == -1
-    assert lib.avsg_page_plan(p, at, None, -1, at, at, at, at, None) == -1
-    for i in (0, 2, 3, 4):
-        args = [at] * 5
+    assert lib.avsg_page_plan(p, at, None, 0, -1, at, at, at, at, None) == -1
+    assert lib.avsg_page_plan(p, at, None, -1, 4, at, at, at, at, None) == -1
+    for i in (0, 3, 4, 5):
+        args = [at, at, 4, at, at, at]
         args[i] = None
         assert lib.avsg_tree_keep(p, *args, None) == -1
-    assert lib.avsg_page_plan(None, at, None, 4, at, at, at, at, None) == -1
+    assert lib.avsg_tree_keep(p, at, at, -1, at, at, at, None) == -1
+    assert lib.avsg_page_plan(None, at, None, 0, 4, at, at, at, at, None) == -1
 
 
 @pytest.mark.parametrize("kw,code", [
