@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
     return;
   }
 
+  griddep_launch();                                  // (the merge waits for the whole grid anyway)
   Piece pc;
   while (walk.next(a, pc)) {
     const int rows = pc.ntok * a.G, count = pc.count, h = pc.h;
@@ -712,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
     }
     if (!whole && pc.begins) head = make_int4(pc.last - cta + 1, pc.f + pc.tok0, h, rows);
   }
-  griddep_launch();
   if (tid == 0) a.head[cta] = head;
 }
 
@@ -724,71 +724,76 @@ template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a, int MT) {
   constexpr int RPC = kMergeWarps / WPR;             // rows per CTA
   constexpr int VPL = D / 32;                        // values per lane
-  __shared__ float s_o[kMergeWarps][D], s_max[kMergeWarps], s_sum[kMergeWarps];
+  __shared__ float s_o[kMergeWarps][D], s_sum[kMergeWarps];
   griddep_wait();
   const int cta = blockIdx.x;
   const int4 head = a.head[cta];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.y * RPC + warp / WPR, part = warp % WPR;
-  if (head.x == 0 || (int)blockIdx.y * RPC >= head.w) return;
-  const bool have = row < head.w;
-  // piece 0 is the second partial of its CTA (the unit begins there), the others the first
-  auto slot = [&](int i) { return (long long)(2 * (cta + i) + (i == 0 ? 1 : 0)) * MT + row; };
-  float top = -INFINITY;
-  if (have)
-    for (int i = lane; i < head.x; i += 32) top = fmaxf(top, a.ml[slot(i) * 2]);
+  const int part = warp % WPR;
+  if (head.x == 0) return;
+  for (int r0 = blockIdx.y * RPC; r0 < head.w; r0 += gridDim.y * RPC) {
+    const int row = r0 + warp / WPR;
+    const bool have = row < head.w;
+    // piece 0 is the second partial of its CTA (the unit begins there), the others the first
+    auto slot = [&](int i) { return (long long)(2 * (cta + i) + (i == 0 ? 1 : 0)) * MT + row; };
+    float top = -INFINITY;
+    if (have)
+      for (int i = lane; i < head.x; i += 32) top = fmaxf(top, a.ml[slot(i) * 2]);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float use = top == -INFINITY ? 0.f : top;
-  float o[VPL], sum = 0.f;
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float use = top == -INFINITY ? 0.f : top;
+    float o[VPL], sum = 0.f;
 #pragma unroll
-  for (int x = 0; x < VPL; ++x) o[x] = 0.f;
-  if (have)
+    for (int x = 0; x < VPL; ++x) o[x] = 0.f;
+    if (have)
 #pragma unroll 4
-    for (int i = part; i < head.x; i += WPR) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.ml + slot(i) * 2);
-      const float f = ex2(ml.x - use);
-      sum += ml.y * f;
-      const float* p = a.part + slot(i) * D + lane * VPL;
-      if constexpr (VPL >= 4) {
+      for (int i = part; i < head.x; i += WPR) {
+        const float2 ml = *reinterpret_cast<const float2*>(a.ml + slot(i) * 2);
+        const float f = ex2(ml.x - use);
+        sum += ml.y * f;
+        const float* p = a.part + slot(i) * D + lane * VPL;
+        if constexpr (VPL >= 4) {
 #pragma unroll
-        for (int x = 0; x < VPL; x += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(p + x);
-          o[x] += y.x * f;
-          o[x + 1] += y.y * f;
-          o[x + 2] += y.z * f;
-          o[x + 3] += y.w * f;
+          for (int x = 0; x < VPL; x += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p + x);
+            o[x] += y.x * f;
+            o[x + 1] += y.y * f;
+            o[x + 2] += y.z * f;
+            o[x + 3] += y.w * f;
+          }
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(p);
+          o[0] += y.x * f;
+          o[1] += y.y * f;
         }
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(p);
-        o[0] += y.x * f;
-        o[1] += y.y * f;
       }
+    if constexpr (WPR > 1) {
+#pragma unroll
+      for (int x = 0; x < VPL; ++x) s_o[warp][lane * VPL + x] = o[x];
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) {
+          sum += s_sum[warp + w];
+#pragma unroll
+          for (int x = 0; x < VPL; ++x) o[x] += s_o[warp + w][lane * VPL + x];
+        }
+      }
+      __syncthreads();
     }
-  if constexpr (WPR > 1) {
+    if (!have || part != 0) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int lt = row / a.G, gg = row - lt * a.G;
+    const long long at = (long long)(head.y + lt) * a.H * a.G + head.z * a.G + gg;
+    unsigned char* dst = a.out + (at * D + lane * VPL) * 2;
 #pragma unroll
-    for (int x = 0; x < VPL; ++x) s_o[warp][lane * VPL + x] = o[x];
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    if (part != 0) return;
-#pragma unroll
-    for (int w = 1; w < WPR; ++w) {
-      sum += s_sum[warp + w];
-#pragma unroll
-      for (int x = 0; x < VPL; ++x) o[x] += s_o[warp + w][lane * VPL + x];
+    for (int x = 0; x < VPL; x += 2)
+      *reinterpret_cast<uint32_t*>(dst + x * 2) = pack<T>(o[x] * inv, o[x + 1] * inv);
+    if (a.lse && lane == 0) {
+      constexpr float shift = std::is_same<T, __half>::value ? kHalfShift : 0.f;
+      a.lse[at] = sum == 0.f ? -INFINITY : (top - shift) * 0.6931471805599453f + logf(sum);
     }
-  }
-  if (!have) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int lt = row / a.G, gg = row - lt * a.G;
-  const long long at = (long long)(head.y + lt) * a.H * a.G + head.z * a.G + gg;
-  unsigned char* dst = a.out + (at * D + lane * VPL) * 2;
-#pragma unroll
-  for (int x = 0; x < VPL; x += 2)
-    *reinterpret_cast<uint32_t*>(dst + x * 2) = pack<T>(o[x] * inv, o[x + 1] * inv);
-  if (a.lse && lane == 0) {
-    constexpr float shift = std::is_same<T, __half>::value ? kHalfShift : 0.f;
-    a.lse[at] = sum == 0.f ? -INFINITY : (top - shift) * 0.6931471805599453f + logf(sum);
   }
 }
 
@@ -798,11 +803,12 @@ cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
   const int most = a.max_new < a.tpm ? a.max_new : a.tpm;
   const int rows = most * a.G;
   // Many units: few pieces each, a warp per row; few units: many pieces, four.
+  // (CTAs without a unit to join only cost their launch; looping over rows costs 1.5 us a round.)
+  const int groups = a.R * a.H >= 16 ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
+  const dim3 grid(a.ctas, groups < 64 ? groups : 64);
   if (a.R * a.H >= 16)
-    return launch_pdl(tree_merge_kernel<T, D, 1>, dim3(a.ctas, (rows + kMergeWarps - 1) / kMergeWarps),
-                      dim3(kMergeWarps * 32), 0, st, a, MT);
-  return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, dim3(a.ctas, rows), dim3(kMergeWarps * 32), 0,
-                    st, a, MT);
+    return launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
+  return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
 }
 
 template <typename T, int D, int WM>

@@ -12,8 +12,8 @@
 //                   output there when the maximum has grown by more than 2^8
 //                   (until then weights up to 2^8 stand in for it: the same
 //                   quotient, no pass over the output);
-//   warps 8, 10     K and V tiles by TMA, one box per page, a lane each, into a
-//                   ring of five buffers that runs on into the next unit;
+//   warps 8, 10     K and V tiles by TMA in turn, one box per page, a lane each, into a
+//                   ring of 160 KB that runs on into the next unit;
 //   warps 9, 11     issue the products of stream 0 and 1: S = Q K^T (both in
 //                   shared memory), O += P V (P in tensor memory).  An issuing
 //                   warp is held up by the products before, so that one warp's
@@ -46,7 +46,6 @@ constexpr int UT = 128;                    // keys per tile
 constexpr int UM = 128;                    // rows per stream
 constexpr int kUmmaThreads = 384;
 constexpr int UH = 64;                     // keys per half tile
-constexpr int kRing = 5;
 constexpr float kLazy = 8.f;               // growth of the maximum (log2) that O is scaled for
 constexpr long long kWaitClocks = 4000000000LL;
 
@@ -60,9 +59,10 @@ template <int D>
 struct Mem {
   static constexpr int Q = UM * D * 2;     // bytes of one stream's rows
   static constexpr int TILE = UT * D * 2;
+  static constexpr int BUFS = D == 128 ? 5 : 10;  // 160 KB either way
   static constexpr int RING = 2 * Q;
-  static constexpr int BARS = RING + kRing * TILE;
-  static constexpr int SMEM = BARS + 256;
+  static constexpr int BARS = RING + BUFS * TILE;
+  static constexpr int SMEM = BARS + 8 * (2 * BUFS + 14);
 };
 
 __device__ __forceinline__ void bar_init(uint32_t b, int count) {
@@ -196,6 +196,11 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Two fp32 values at once.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t x;
@@ -312,6 +317,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     tree_umma_kernel(UmmaArgs ua, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
   using M = Mem<D>;
+  constexpr int kRing = M::BUFS;
   constexpr bool HALF = std::is_same<T, __half>::value;
   constexpr float SHIFT = HALF ? kHalfShift : 0.f;
   constexpr int COLS = D / 64;             // blocks of 64 columns
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   }
   if (tid == 0) {
     for (int b = 0; b < kRing; ++b) {
-      bar_init(full(b), 2);
+      bar_init(full(b), 1);
       bar_init(empty(b), 2);
     }
     for (int x = 0; x < 2; ++x) {
@@ -373,6 +379,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
+  griddep_launch();
   volatile int* give_up = &s_give_up;
   if (tid == 0) {
     if (smem & 1023) raise_error(a.err, AVSG_ERR_INTERNAL, -1, -1);  // (atoms are 1024-byte aligned)
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     // V of tile t, made safe to multiply: see above.  Rows that every query sees are left alone
     // (what they hold reaches every query anyway), which without a window are all but the new
     // tokens'.  Both streams may do the same tile: they write the same values.  Its load's number
-    // follows those of loads that this tile's scores needed by less than kRing, so the parity
+    // follows those of loads that this tile's scores needed by less than the ring's length, so the parity
     // tells its phase.
     auto clean_v = [&](const Piece& s, bool two, int t) {
       const int n = idx + v_place(two, t, s.count), b = n % kRing;
@@ -516,30 +523,43 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           tm_wait_ld(w[0]);
           tm_wait_ld(w[1]);
           float scale = a.score_log2;
+          float away = 0.f;                // a row's part of the distance bias, the same for all keys
           if constexpr (EXTRA) {
-            // capped and biased, in units of log 2
+            // capped, in units of log 2: cap tanh(x / cap) = cap (1 - 2 / (exp(2 x / cap) + 1))
             scale = 1.f;
+            if (a.cap_in != 0.f) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int j = s.j0 + t * UT + (hh & 1) * UH + c * 32;
-              const float far = slope * (float)(q_pos - j);
-              const bool drafts = a.slopes && !s.chain && j + 32 > s.len;
+              for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int y = 0; y < 32; ++y) {
-                float v = __uint_as_float(w[c][y]);
-                if (a.cap_in != 0.f) v = a.cap_out * (1.f - __fdividef(2.f, ex2(v * a.cap_in) + 1.f));
-                else v *= a.score_log2;
-                if (!drafts) v += slope * (float)y - far;
-                w[c][y] = __float_as_uint(v);
+                for (int y = 0; y < 32; ++y)
+                  w[c][y] = __float_as_uint(
+                      fmaf(reciprocal(ex2(__uint_as_float(w[c][y]) * a.cap_in) + 1.f), -2.f * a.cap_out, a.cap_out));
+            } else {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int y = 0; y < 32; ++y) w[c][y] = __float_as_uint(__uint_as_float(w[c][y]) * a.score_log2);
+            }
+            if (a.slopes) {
+              // slope (pos_q - pos_k), less what is the same for the half's keys
+              const int j = s.j0 + t * UT + (hh & 1) * UH;
+              away = slope * (float)(q_pos - j);
+              if (s.chain || j + UH <= s.len) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                  for (int y = 0; y < 32; ++y)
+                    w[c][y] = __float_as_uint(fmaf(slope, (float)(c * 32 + y), __uint_as_float(w[c][y])));
+              } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) {
+                    const int d = j + c * 32 + y - s.len;
+                    const float at = d >= 0 ? (float)(s.len + s_depth[x][d & 63] - j) : (float)(c * 32 + y);
+                    w[c][y] = __float_as_uint(fmaf(slope, at, __uint_as_float(w[c][y])));
+                  }
               }
-              if (drafts)
-#pragma unroll
-                for (int y = 0; y < 32; ++y) {
-                  const int d = j + y - s.len;
-                  const float bias = d >= 0 ? slope * (float)(q_pos - s.len - s_depth[x][d & 63])
-                                            : far - slope * (float)y;
-                  w[c][y] = __float_as_uint(__uint_as_float(w[c][y]) - bias);
-                }
             }
           }
           if (__builtin_expect(edge, 0)) {
@@ -572,7 +592,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             tops[z] = fmaxf(tops[z], __uint_as_float(e[15]));
           }
           const float use = m == -INFINITY ? 0.f : m;
-          const uint64_t scale2 = pair(scale, scale), minus2 = pair(SHIFT - use, SHIFT - use);
+          const uint64_t scale2 = pair(scale, scale), minus2 = pair(SHIFT - use - away, SHIFT - use - away);
           uint64_t sums[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -589,7 +609,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           float sum1;
           unpair(add2(sums[0], sums[1]), sum, sum1);
           sum += sum1;
-          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale - away;
           const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
           __syncwarp();
           again = __any_sync(0xffffffffu, grow);
@@ -722,17 +742,16 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     }
     if (tid == 0) a.head[cta] = head;
   } else if (warp == 8 || warp == 10) {
-    // ---- loads, the boxes of a tile shared by two warps.  Order of a segment: two streams over
-    // all tiles: K0 V0 K1 V1 ...; one tile each in turn: K0 K1 V0 K2 V1 K3 ... -- the order in
-    // which the products use them.  Page ids are looked up one load ahead.
+    // ---- loads, taken in turn by two warps.  Order of a segment: two streams over all tiles:
+    // K0 V0 K1 V1 ...; one tile each in turn: K0 K1 V0 K2 V1 K3 ... -- the order in which the
+    // products use and release them.  Page ids are looked up one load ahead.
     Piece s;
     const int part = warp == 8 ? 0 : 1;
-    const int boxes = UT / ua.box_rows, own = max(boxes / 2, 1), y = part * own + lane;
-    const bool lane_on = lane < own && y < boxes;
-    int idx = 0;
+    const int boxes = UT / ua.box_rows;
+    int idx = part;
     int page = -1, group = 0, is_v = 0;    // the next load's box of this lane
     bool more = walk.next(a, s);
-    int x = 0;
+    int x = part;
     auto look_up = [&]() {
       const bool two = s.ntok * a.G > UM;
       int t;
@@ -747,9 +766,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         is_v = z >= pairs || !(z & 1);
         t = z >= pairs ? s.count - 2 + z - pairs : (z >> 1) + ((z & 1) ? 2 : 0);
       }
-      const int j = s.j0 + t * UT + y * ua.box_rows;
+      const int j = s.j0 + t * UT + lane * ua.box_rows;
       page = -1;
-      if (lane_on && j < s.limit) {
+      if (lane < boxes && j < s.limit) {
         page = __ldg(a.tables + (size_t)s.r * a.max_pages + (j >> a.shift));
         group = ((s.h << a.shift) + (j & ((1 << a.shift) - 1))) >> 3;
         if (page < 0 || page >= a.num_pages) {
@@ -757,8 +776,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           page = -1;
         }
       }
-      if (++x == 2 * s.count) {
-        x = 0;
+      if ((x += 2) >= 2 * s.count) {
+        x = part;
         more = walk.next(a, s);
       }
     };
@@ -773,15 +792,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       if (lane == 0) bar_expect(full(b), n * ua.box_rows * D * 2);
       __syncwarp();
       if (now >= 0)
-        tma_box(smem + M::RING + b * M::TILE + y * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
+        tma_box(smem + M::RING + b * M::TILE + lane * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
                 now_group, now);
-      ++idx;
+      idx += 2;
     }
-    // every copy has landed before the CTA may end
-    for (int b = 0; b < kRing && b < idx; ++b) {
-      const int use = (idx - 1 - b) / kRing;  // use number of buffer b's last load
-      bar_wait(full(b), use & 1, give_up, a.err);
-    }
+    // every copy of this warp has landed before the CTA may end
+    for (int n = max(part, idx - 2 * kRing); n < idx; n += 2)
+      if (n + kRing >= idx) bar_wait(full(n % kRing), (n / kRing) & 1, give_up, a.err);
   } else {
       // ---- products.  Warp 9 has stream 0, and stream 1 too where the streams take turns (K and
       // V then come as fast as one warp can use them); warp 11 has stream 1 otherwise.
@@ -894,7 +911,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         __syncwarp();
       }
   }
-  griddep_launch();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
