@@ -62,7 +62,7 @@ struct Mem {
   static constexpr int BUFS = D == 128 ? 5 : 10;  // 160 KB either way
   static constexpr int RING = 2 * Q;
   static constexpr int BARS = RING + BUFS * TILE;
-  static constexpr int SMEM = BARS + 8 * (2 * BUFS + 14);
+  static constexpr int SMEM = BARS + 8 * (2 * BUFS + 16);
 };
 
 __device__ __forceinline__ void bar_init(uint32_t b, int count) {
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   const int cta = blockIdx.x;
   const uint32_t smem = smem_u32(smem_raw);
   float* s_m = reinterpret_cast<float*>(smem_raw + M::Q);  // (where up to 128 rows leave stream 1's q free)
-  float* s_l = s_m + UM;
+  float* s_l = s_m + 2 * UM;
   const uint32_t bars = smem + M::BARS;
   auto full = [&](int b) { return bars + 8 * b; };
   auto empty = [&](int b) { return bars + 8 * (kRing + b); };
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   auto p_full = [&](int x, int b) { return bars + 8 * (2 * kRing + 4 + 2 * x + b); };
   auto o_done = [&](int x) { return bars + 8 * (2 * kRing + 8 + x); };
   auto o_last = [&](int x) { return bars + 8 * (2 * kRing + 10 + x); };
-  auto q_full = [&](int x) { return bars + 8 * (2 * kRing + 12 + x); };
+  auto q_full = [&](int x) { return bars + 8 * (2 * kRing + 12 + x); };  // 129 to 256 rows
+  const uint32_t q_one = bars + 8 * (2 * kRing + 14);                     // up to 128
 
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       bar_init(o_last(x), 1);
       bar_init(q_full(x), UM / 32);
     }
+    bar_init(q_one, UM / 32);
     s_give_up = s_bad[0] = s_bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16 and up
     const uint32_t to = tmem + lanes + 256 + 128 * x;
     int4 head = make_int4(0, 0, 0, 0);
-    int hh = 0, outs = 0, seg = 0, idx = 0;  // hh: halves of this stream since the start
+    int hh = 0, seg = 0, idx = 0;  // hh: halves of this stream since the start
     // V of tile t, made safe to multiply: see above.  Rows that every query sees are left alone
     // (what they hold reaches every query anyway), which without a window are all but the new
     // tokens'.  Both streams may do the same tile: they write the same values.  Its load's number
@@ -439,6 +441,36 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int rl = two ? x * UM + row : row;
       const bool mine = rl < s.ntok * a.G;
       const int lt = rl / a.G, gg = rl - lt * a.G;
+      // q into shared memory, a row by D / 8 lanes; rows past the unit's are zeros
+      const bool warp_live = rl - lane < s.ntok * a.G;
+      bool q_loading = false;
+      if (two || x == 0) {
+        if (warp_live) {
+          constexpr int LPR = D / 8, RPI = 32 / LPR;
+          const int ch = lane % LPR, rows = s.ntok * a.G, G = a.G;
+          int r = rl - lane + lane / LPR, at = (warp & 3) * 32 + lane / LPR, t = r / G, g = r - t * G;
+          const unsigned char* base =
+              a.q + ((long long)(s.f + s.tok0) * a.q_stride + (long long)s.h * G * D) * 2 + ch * 16;
+          const uint32_t to = smem + x * M::Q + (ch / 8) * 1024;
+#pragma unroll 4
+          for (int it = 0; it < 32 / RPI; ++it) {
+            const bool ok = r < rows;
+            const unsigned char* src = ok ? base + (t * a.q_stride + g * D) * 2 : a.q;
+            const uint32_t dst = to + (at / 8) * (1024 * COLS) + (at & 7) * 128 + (((ch & 7) ^ (at & 7)) << 4);
+            if (ua.q_vec) {
+              cp_async16(dst, src, ok ? 16 : 0);
+            } else {
+#pragma unroll
+              for (int z = 0; z < 4; ++z) cp_async4(dst + 4 * z, src + 4 * z, ok ? 4 : 0);
+            }
+            r += RPI;
+            at += RPI;
+            for (g += RPI; g >= G; g -= G) ++t;
+          }
+          cp_commit();
+          q_loading = true;
+        }
+      }
       const int tok = mine ? s.tok0 + lt : -1;
       int q_pos = s.len + max(tok, 0);
       unsigned long long bits = 0;
@@ -460,34 +492,17 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           for (int d = 0; d < s.n; ++d)
             if (q_pos - (s.len + s_depth[x][d]) >= a.window) bits &= ~(1ull << d);
       }
-      // this row of q
-      if (two || x == 0) {
-        unsigned char* q = smem_raw + x * M::Q + (row / 8) * (1024 * COLS) + (row & 7) * 128;
-        const unsigned char* src =
-            a.q + ((long long)(s.f + max(tok, 0)) * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (mine) {
-            if (ua.q_vec) {
-              w = *reinterpret_cast<const uint4*>(src + c * 16);
-            } else {
-              const uint32_t* p = reinterpret_cast<const uint32_t*>(src + c * 16);
-              w = make_uint4(p[0], p[1], p[2], p[3]);
-            }
-          }
-          *reinterpret_cast<uint4*>(q + (c / 8) * 1024 + (((c & 7) ^ (row & 7)) << 4)) = w;
-        }
+      if (q_loading) {
+        cp_wait<0>();
         async_fence();
-        warp_arrive(q_full(x), lane);
       }
+      if (two || x == 0) warp_arrive(two ? q_full(x) : q_one, lane);
 
       if (tid == 0) {                      // the next piece, while the first scores are on their way
         s_bad[(seg + 1) & 1] = 0;
         s_more[(seg + 1) & 1] = s_walk.next(a, s_piece[(seg + 1) & 1]);
       }
       float m = -INFINITY, l = 0.f;
-      const bool warp_live = rl - lane < s.ntok * a.G;
       const int halves = 2 * (two ? s.count : (s.count - x + 1) >> 1);
       // tiles e0 .. e1 - 1 of the piece are seen whole by every row (Piece::edge)
       const int e1 = min(s.count, max(0, s.all_see - s.j0) / UT);
@@ -662,76 +677,84 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       }
 
       // ---- the end of the piece
-      // (stream 1 has no tile, and no output, in a piece of one tile with up to 128 rows)
-      const bool other = !two && s.count > 1 && x == 0;  // stream 0 joins stream 1's output to its own
-      if (halves > 0) {
-        bar_wait(o_last(x), outs & 1, give_up, a.err);
-        ++outs;
-      }
-      if (!two && x == 1) {
-        s_m[row] = m;
-        s_l[row] = l;
+      // Up to 128 rows the two streams' outputs are joined here (stream 1 has none in a piece of
+      // one tile), half of the columns by either stream's warps.
+      const bool join = !two && s.count > 1;
+      bar_wait(o_last(x), seg & 1, give_up, a.err);
+      if (!two) {
+        s_m[UM * x + row] = m;
+        s_l[UM * x + row] = l;
       }
       __syncwarp();
       tc_fence_after();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tc_fence_after();
       const bool bad = s_bad[seg & 1] != 0;
-      if (two || x == 0) {
-        const float m1 = other ? s_m[row] : -INFINITY, l1 = other ? s_l[row] : 0.f;
-        const float top = fmaxf(m, m1), use = top == -INFINITY ? 0.f : top;
-        const float f0 = ex2(m - use), f1 = ex2(m1 - use);
-        const float sum = l * f0 + l1 * f1;
-        const float inv = s.whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        const long long at = (long long)(s.f + max(tok, 0)) * a.H * a.G + s.h * a.G + gg;
-        const long long slot = ((long long)(2 * cta + (s.begins ? 1 : 0)) * (2 * UM) + rl);
+      float m1 = -INFINITY, l1 = 0.f;
+      if (!two) {
+        m = s_m[row];
+        l = s_l[row];
+        if (join) {
+          m1 = s_m[UM + row];
+          l1 = s_l[UM + row];
+        }
+      }
+      const float top = fmaxf(m, m1), use = top == -INFINITY ? 0.f : top;
+      const float f0 = ex2(m - use), f1 = ex2(m1 - use);
+      const float sum = l * f0 + l1 * f1;
+      const float inv = s.whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      const long long at = (long long)(s.f + max(tok, 0)) * a.H * a.G + s.h * a.G + gg;
+      const long long slot = ((long long)(2 * cta + (s.begins ? 1 : 0)) * (2 * UM) + rl);
+      if (warp_live) {
+        const uint32_t from = two ? to : tmem + lanes + 256;
+        const float g0 = f0 * inv, g1 = f1 * inv;  // (inv is 1 where the output is not divided yet)
         uint32_t w0[32], w1[32];
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          tm_ld32(to + c * 32, w0);
+        for (int c = two ? 0 : x * (D / 64); c < (two ? D / 32 : (x + 1) * (D / 64)); ++c) {
+          tm_ld32(from + c * 32, w0);
+          if (join) tm_ld32(from + 128 + c * 32, w1);
           tm_wait_ld(w0);
-          if (other) {
-            tm_ld32(to + 128 + c * 32, w1);
-            tm_wait_ld(w1);
-          }
-          float o[32];
+          tm_wait_ld(w1);
+          // (a factor of 0 stands for a stream that saw nothing, whatever its output holds)
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
-            o[y] = f0 == 0.f ? 0.f : __uint_as_float(w0[y]) * f0;
-            if (other && f1 != 0.f) o[y] += __uint_as_float(w1[y]) * f1;
+            float o = g0 == 0.f ? 0.f : __uint_as_float(w0[y]) * g0;
+            if (join) o += g1 == 0.f ? 0.f : __uint_as_float(w1[y]) * g1;
+            w0[y] = __float_as_uint(o);
           }
+          auto o = [&](int y) { return __uint_as_float(w0[y]); };
           if (!mine) {
           } else if (s.whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + (at * D + c * 32) * 2);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              dst[y] = make_uint4(pack<T>(o[8 * y] * inv, o[8 * y + 1] * inv),
-                                  pack<T>(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
-                                  pack<T>(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
-                                  pack<T>(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+              dst[y] = make_uint4(pack<T>(o(8 * y), o(8 * y + 1)), pack<T>(o(8 * y + 2), o(8 * y + 3)),
+                                  pack<T>(o(8 * y + 4), o(8 * y + 5)), pack<T>(o(8 * y + 6), o(8 * y + 7)));
           } else {
             float4* dst = reinterpret_cast<float4*>(a.part + slot * D + c * 32);
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
-              dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            for (int y = 0; y < 8; ++y) dst[y] = make_float4(o(4 * y), o(4 * y + 1), o(4 * y + 2), o(4 * y + 3));
           }
           __syncwarp();
         }
-        if (mine) {
-          if (bad) {
-            const unsigned char* q =
-                a.q + ((long long)(s.f + tok) * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
-            if (s.whole)
-              add_bad_values<T, T, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, inv,
-                                      reinterpret_cast<T*>(a.out) + at * D);
-            else
-              add_bad_values<T, float, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, 1.f,
-                                          a.part + slot * D);
-          }
+        if (mine && (two || x == 0)) {
           if (!s.whole)
             *reinterpret_cast<float2*>(a.ml + slot * 2) = make_float2(top, sum);
           else if (a.lse)
             a.lse[at] = sum == 0.f ? -INFINITY : (top - SHIFT) * 0.6931471805599453f + logf(sum);
+        }
+      }
+      if (__builtin_expect(bad, 0)) {
+        __syncwarp();
+        asm volatile("bar.sync 6, 256;" ::: "memory");  // the rows are written
+        if (mine && (two || x == 0)) {
+          const unsigned char* q =
+              a.q + ((long long)(s.f + tok) * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
+          if (s.whole)
+            add_bad_values<T, T, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, inv,
+                                    reinterpret_cast<T*>(a.out) + at * D);
+          else
+            add_bad_values<T, float, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, 1.f, a.part + slot * D);
         }
       }
       idx += 2 * s.count;
@@ -800,12 +823,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     for (int n = max(part, idx - 2 * kRing); n < idx; n += 2)
       if (n + kRing >= idx) bar_wait(full(n % kRing), (n / kRing) & 1, give_up, a.err);
   } else {
-      // ---- products.  Warp 9 has stream 0, and stream 1 too where the streams take turns (K and
-      // V then come as fast as one warp can use them); warp 11 has stream 1 otherwise.
+      // ---- products.  Up to 128 rows, both warps follow every load, in order: a tile that is the
+      // other stream's is passed on, so that a buffer is filled again only when both have seen it
+      // (a barrier's parity does not tell a phase from the one two before it).
       Piece s;
       const int me = warp == 9 ? 0 : 1;
-      int idx = 0, qs = 0;
-      int ps[2] = {0, 0};                  // halves of each stream since the start
+      int idx = 0, qs = 0, q1 = 0;
+      int ps = 0;                          // halves of this stream since the start
       const uint32_t id_s = instruction<T>(UH, false), id_o = instruction<T>(D, true);
       constexpr uint32_t HALF_TILE = UH / 8 * 1024 * COLS;
       auto wait_load = [&](int place) -> uint32_t {
@@ -845,19 +869,22 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       auto finish = [&](int x) {
         if (elect_one()) mma_commit(o_last(x));
       };
+      auto pass_on = [&](int place) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty((idx + place) % kRing));
+      };
       auto release = [&](int place) {
         const uint32_t bar = uniform(empty((idx + place) % kRing));
         if (elect_one()) mma_commit(bar);
       };
       while (walk.next(a, s)) {
         const bool two = s.ntok * a.G > UM;
-        if (two || me == 0) {
-          bar_wait(q_full(me), qs & 1, give_up, a.err);
+        const int x = me;
+        if (two) {
+          const int hh = ps;
+          bar_wait(q_full(x), qs & 1, give_up, a.err);
           ++qs;
           tc_fence_after();
-        }
-        if (two) {
-          const int x = me, hh = ps[x];
           uint32_t k = wait_load(0);
           scores(x, x, k, 0);
           scores(x, x, k, 1);
@@ -877,36 +904,46 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               release(2 * t + 2);
             }
           }
-          finish(x);
-        } else if (me == 0) {
+        } else {
+          bar_wait(q_one, q1 & 1, give_up, a.err);
+          ++q1;
+          tc_fence_after();
           for (int t = 0; t < 2 && t < s.count; ++t) {
             const uint32_t k = wait_load(t);
-            scores(t, 0, k, 0);
-            scores(t, 0, k, 1);
+            if (t != me) {
+              pass_on(t);
+              continue;
+            }
+            scores(x, 0, k, 0);
+            scores(x, 0, k, 1);
             release(t);
-            release(t);                    // (for both)
           }
           for (int t = 0; t < s.count; ++t) {
-            const int x = t & 1, place = v_place(false, t, s.count), hh = ps[x] + (t & ~1);
+            const int place = v_place(false, t, s.count), hh = ps + (t & ~1);
             const bool more = t + 2 < s.count;
             const uint32_t v = wait_load(place);
+            if ((t & 1) != me) {
+              pass_on(place);
+              if (more) {
+                wait_load(place + 1);
+                pass_on(place + 1);
+              }
+              continue;
+            }
             output(x, v, hh, t < 2);
             const uint32_t k = more ? wait_load(place + 1) : 0;
             if (more) scores(x, 0, k, 0);
             output(x, v, hh + 1, false);
             release(place);
-            release(place);
             if (more) {
               scores(x, 0, k, 1);
               release(place + 1);
-              release(place + 1);
-            } else {
-              finish(x);
             }
           }
         }
-        ps[0] += 2 * (two ? s.count : (s.count + 1) >> 1);
-        ps[1] += 2 * (two ? s.count : s.count >> 1);
+        // (also where stream 1 has no tile: its softmax warps wait for this warp to have come by)
+        finish(x);
+        ps += 2 * (two ? s.count : (s.count + 1 - me) >> 1);
         idx += 2 * s.count;
         __syncwarp();
       }
