@@ -376,3 +376,23 @@ def test_a_step_gives_the_definition():
                 all_k = np.concatenate([old_k, k[rows, h]])
                 terms = 64 ** -0.5 * np.abs(q[rows, hs].reshape(-1, 64)).max(0) @ np.abs(all_k).max(0)
                 assert (np.abs(got - want) <= size * (2 * 2.0**-7 * terms + 2.0**-8) + 2.0**-8 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("spare", [0, 2000])
+@pytest.mark.parametrize("lens,new,groups,dim,dtype", [
+    ([0, 1, 127, 128, 129, 700], [1, 1, 1, 1, 1, 1], 4, 128, BF16),
+    ([513, 0, 64], [2, 3, 1], 5, 64, F16),
+])
+def test_few_rows_with_a_small_and_a_large_pool(lens, new, groups, dim, dtype, spare):
+    """Up to 16 rows per kv-head run on either kernel, by the pool's tokens per request."""
+    s = Step(lens, new, 16, 2, groups, dim, dtype, False)
+    if spare:
+        from decode_serving_gb300.paged import PagedCache
+        pool = s.k.shape[1] + spare * len(lens)
+        k, v = (torch.zeros(1, pool, *s.k.shape[2:], dtype=dtype, device="cuda") for _ in "kv")
+        k[:, :s.k.shape[1]], v[:, :s.k.shape[1]] = s.k, s.v
+        s.cache = PagedCache(k, v, s.cache.tables, s.cache.lens,
+                             torch.zeros(pool, dtype=torch.int32, device="cuda"), s.cache.free_count)
+        s.k, s.v = k, v
+    s.attend()
+    s.check()
