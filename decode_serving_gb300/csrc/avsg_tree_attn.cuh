@@ -235,6 +235,14 @@ struct Piece {
   }
 };
 
+// Where a CTA's share begins, found by one of its threads.
+template <int KT>
+struct Begin {
+  Req<KT> q;
+  int r;
+  long long before;                        // list position of the request's first place
+};
+
 // The CTA's share of the list: every thread walks it alike.
 template <int KT>
 struct Walk {
@@ -243,8 +251,10 @@ struct Walk {
   int C;                                   // CTAs with a share
   int r, h, mt, ta;                        // ta: the next place of the unit
 
-  // Finds the share (all threads of the block; a barrier inside).  False: no work.
-  __device__ bool begin(const TreeArgs& a, long long* s_warp, long long* s_base, int* s_r) {
+  // Finds the share (all threads of the block; barriers inside).  False: no work, or an
+  // error latched before (its word and the lengths are read side by side).
+  __device__ bool begin(const TreeArgs& a, long long* s_warp, Begin<KT>* s_begin) {
+    const bool latched = load_err(a.err) != 0;
     const int per = (a.R + blockDim.x - 1) / blockDim.x;
     const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
     long long mine = 0;
@@ -253,23 +263,25 @@ struct Walk {
     const long long fit = W / a.min_tiles;
     C = fit < 1 ? 1 : fit < a.ctas ? (int)fit : a.ctas;
     const int cta = blockIdx.x;
-    if (W == 0 || cta >= C) return false;  // (the same for the whole block)
+    if (__syncthreads_or(latched) || W == 0 || cta >= C) return false;  // (alike in the whole block)
     at = cta * W / C;
     end = (cta + 1) * W / C;
     if (before <= at && at < before + mine)
       for (int i = r0; i < r1; ++i) {
-        const long long w = load_req<KT>(a, i).per_head(a.tpm) * a.H;
+        const Req<KT> req = load_req<KT>(a, i);
+        const long long w = req.per_head(a.tpm) * a.H;
         if (at < before + w) {
-          *s_r = i;
-          *s_base = before;
+          s_begin->q = req;
+          s_begin->r = i;
+          s_begin->before = before;
           break;
         }
         before += w;
       }
     __syncthreads();
-    r = *s_r;
-    q = load_req<KT>(a, r);
-    const long long head = q.per_head(a.tpm), off = at - *s_base;
+    r = s_begin->r;
+    q = s_begin->q;
+    const long long head = q.per_head(a.tpm), off = at - s_begin->before;
     h = (int)(off / head);
     const long long rest = off - h * head;
     int lo = 0, hi = q.mts;                // before(lo) <= rest < before(hi)
@@ -357,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
   constexpr bool HALF = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_warp[kThreads / 32];
-  __shared__ long long s_base;                       // list position of request s_r's first tile
-  __shared__ int s_r;
+  __shared__ Begin<KT> s_begin;
   __shared__ float s_m[WK][MT], s_l[WK][MT];
   __shared__ int s_depth[kMaxDrafts];
   long long* s_row = reinterpret_cast<long long*>(smem + S * 2 * SH::TILE);
@@ -371,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
 
   griddep_wait();
   Walk<KT> walk;
-  if (__syncthreads_or(load_err(a.err) != 0) || !walk.begin(a, s_warp, &s_base, &s_r)) {
+  if (!walk.begin(a, s_warp, &s_begin)) {
     if (tid == 0) a.head[cta] = head;
     return;
   }
@@ -722,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(Tr
 // Joins the partials of the units that cross CTAs: blockIdx.x is the CTA in
 // whose share a unit begins, blockIdx.y a group of its rows.  WPR warps work
 // on one row, each on every WPR-th piece.
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a, int MT) {
   constexpr int RPC = kMergeWarps / WPR;             // rows per CTA
@@ -749,7 +760,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a
 #pragma unroll
     for (int x = 0; x < VPL; ++x) o[x] = 0.f;
     if (have)
-#pragma unroll 4
+#pragma unroll 8
       for (int i = part; i < head.x; i += WPR) {
         const float2 ml = *reinterpret_cast<const float2*>(a.ml + slot(i) * 2);
         const float f = ex2(ml.x - use);
@@ -805,7 +816,7 @@ template <typename T, int D>
 cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
   const int most = a.max_new < a.tpm ? a.max_new : a.tpm;
   const int rows = most * a.G;
-  // Many units: few pieces each, a warp per row; few units: many pieces, four.
+  // Many units: few pieces each, a warp per row; few units: many pieces, eight.
   // (CTAs without a unit to join only cost their launch; looping over rows costs 1.5 us a round.)
   const int groups = a.R * a.H >= 16 ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
   const dim3 grid(a.ctas, groups < 64 ? groups : 64);

@@ -323,8 +323,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   constexpr int COLS = D / 64;             // blocks of 64 columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ long long s_warp[kUmmaThreads / 32];
-  __shared__ long long s_base;
-  __shared__ int s_r, s_give_up, s_bad[2];
+  __shared__ Begin<UT> s_begin;
+  __shared__ int s_give_up, s_bad[2];
   __shared__ uint32_t s_tmem;
   __shared__ unsigned char s_depth[2][kMaxDrafts];
   // The softmax warps' walk: its state would cost registers that the scores need.
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   }
   griddep_wait();
   Walk<UT> walk;
-  const bool idle = __syncthreads_or(load_err(a.err) != 0) || !walk.begin(a, s_warp, &s_base, &s_r);
+  const bool idle = !walk.begin(a, s_warp, &s_begin);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   if (idle) {
