@@ -137,7 +137,7 @@ def test_caps_windows_and_slopes(dim, dtype, kw, tree):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("groups,most", [(1, 8), (4, 8), (8, 16)])
+@pytest.mark.parametrize("groups,most", [(1, 8), (4, 8), (8, 16), (16, 16)])
 def test_what_a_row_does_not_see_does_not_reach_it(dtype, groups, most):
     """NaN and infinities behind the last token, in drafts of other branches and outside the window;
     rows that see nothing."""
@@ -396,3 +396,82 @@ def test_few_rows_with_a_small_and_a_large_pool(lens, new, groups, dim, dtype, s
         s.k, s.v = k, v
     s.attend()
     s.check()
+
+
+@pytest.mark.parametrize("groups,dim", [(2, 64), (6, 128), (3, 256)])
+def test_rows_aligned_to_four_bytes_only(groups, dim):
+    """q rows whose start and stride are even counts of values, and no more."""
+    s = Step([70, 3], [4, 5], 8, 2, groups, dim, F16, True)
+    width = 2 * groups * dim
+    wide = torch.zeros(s.total, width + 6, dtype=F16, device="cuda")
+    wide[:, 2:2 + width] = s.q.reshape(s.total, -1)
+    s.attend(q=wide[:, 2:2 + width])
+    s.check()
+
+
+@pytest.mark.parametrize("groups", [2, 9])
+def test_thousands_of_requests(groups):
+    lens = [(i * 37) % 150 for i in range(3000)]
+    s = Step(lens, [(i * 5) % 4 for i in range(3000)], 16, 1, groups, 64, BF16, True)
+    s.attend()
+    s.check(only=set(range(0, 3000, 97)) | {2999})
+
+
+def test_two_streams_with_a_workspace_each():
+    """Two caches' attention at the same time gives what each gives alone."""
+    steps = [Step([4000, 17], [5, 8], 16, 2, 4, 128, BF16, True, seed=k) for k in (1, 2)]
+    alone = []
+    for s in steps:
+        s.attend()
+        alone.append(s.out.clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    works = [s.cache.attention_workspace(4, 8) for s in steps]
+    for s in steps:
+        s.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, st, w in zip(steps, streams, works):
+            s.attend(work=w, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for s, a in zip(steps, alone):
+        assert s.cache.error()[0] == 0 and torch.equal(s.out, a)
+
+
+def test_two_graphs_share_a_workspace_in_turn():
+    s = Step([2000, 40], [6, 8], 16, 2, 4, 128, F16, True)
+    few = Step([900], [1], 16, 2, 4, 128, F16, False)
+    work = s.cache.attention_workspace(4, 8)
+    graphs = []
+    s.attend(work=work)
+    few.attend(work=work, most=8)
+    torch.cuda.synchronize()
+    want = s.out.clone(), few.out.clone()
+    side = torch.cuda.Stream()
+    for x in (s, few):
+        with torch.cuda.stream(side):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                x.attend(work=work, most=8, stream=torch.cuda.current_stream().cuda_stream)
+        graphs.append(g)
+    s.out.zero_(), few.out.zero_()
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s.out, want[0]) and torch.equal(few.out, want[1])
+
+
+@pytest.mark.parametrize("dim,dtype,window", [(128, BF16, 0), (64, F16, 0), (128, F16, 300)])
+def test_a_late_maximum(dim, dtype, window):
+    """Scores that grow along the keys, so that the output is scaled again and again; and keys of
+    large scores at the very end and the very beginning."""
+    s = Step([900, 640], [40, 3], 16, 1, 6, dim, dtype, True)
+    first, tables = host(s.first), host(s.cache.tables)
+    for r, (length, n) in enumerate(zip(s.lens.tolist(), s.new)):
+        q = s.q[first[r], 0].float()
+        for p in range(0, length + n, 3):
+            at = (0, int(tables[r, p // 16]), 0, p % 16)
+            s.k[at] = (q * (8.0 * p / (length + n)) / q.norm() * dim ** 0.25).to(dtype)
+    s.attend(window=window, scale=1.0)
+    s.check(window=window, scale=1.0)
