@@ -30,6 +30,9 @@
 // and V are read once for 256 rows).  Up to 128 rows: the streams take the
 // even and the odd tiles, with an output each, joined at the end of the unit.
 //
+// Tiles are taken from the last key backwards: where scores carry a distance
+// bias, the largest come first and the output is hardly ever scaled.
+//
 // Tensor memory (512 columns): S/P of stream x at 128 x + 64 (half & 1), O at
 // 256 + 128 x.
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
@@ -201,6 +204,7 @@ __device__ __forceinline__ float reciprocal(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float at_most_60(float x) { return x > 60.f ? 60.f : x; }  // (NaN stays)
 // Two fp32 values at once.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t x;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     // tells its phase.
     auto clean_v = [&](const Piece& s, bool two, int t) {
       const int n = idx + v_place(two, t, s.count), b = n % kRing;
-      const int j = s.j0 + t * UT, rows = min(UT, s.limit - j);
+      const int j = s.j0 + (s.count - 1 - t) * UT, rows = min(UT, s.limit - j);
       const int from = a.window > 0 ? 0 : max(0, s.all_see - j);
       bar_wait(full(b), (n / kRing) & 1, give_up, a.err);
       unsigned char* v = smem_raw + M::RING + b * M::TILE;
@@ -512,6 +516,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         __syncwarp();                      // (tensor-memory accesses are the whole warp's)
         tc_fence_after();
       };
+      const int last = s.count - 1;
       const uint32_t ts0 = tmem + lanes + 128 * x;
       uint32_t w[2][32];
       if (halves > 0 && warp_live) {
@@ -521,7 +526,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       }
       for (int i = 0; i < halves; ++i, ++hh) {
         const int t = two ? i >> 1 : (i & ~1) + x;
-        const bool edge = t < e0 || t >= e1;
+        const int kt = last - t;           // place among the piece's keys
+        const bool edge = kt < e0 || kt >= e1;
         const uint32_t ts = ts0 + 64 * (hh & 1);
         if (!warp_live) {                  // only padding: nobody reads what these rows give
           wait_scores(hh);
@@ -530,6 +536,26 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           warp_arrive(p_full(x, hh & 1), lane);
           continue;
         }
+        // keys that the row does not see
+        auto hide = [&]() {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            // committed tokens (a chain: up to this one) below, the window's begin above
+            const int j = s.j0 + kt * UT + (hh & 1) * UH + c * 32;
+            const int below = s.len + (s.chain ? tok + 1 : 0) - j;
+            uint32_t see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
+            if (a.window > 0) {
+              const int from = q_pos - a.window + 1 - j;
+              see &= from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+            }
+            const int d = j - s.len;       // draft of the chunk's first key
+            if (!s.chain && d > -32 && d < 64)
+              see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!((see >> y) & 1)) w[c][y] = 0xff800000u;
+          }
+        };
         // The weights are taken relative to the maximum so far while this half's is found: neither
         // waits for the other.  Where it turns out to have grown too far, once per piece and
         // seldom after, the scores are read again.
@@ -542,13 +568,20 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           if constexpr (EXTRA) {
             // capped, in units of log 2: cap tanh(x / cap) = cap (1 - 2 / (exp(2 x / cap) + 1))
             scale = 1.f;
+            // (Two share a reciprocal, so that a NaN reaches its neighbour: only the row's own, once
+            // unseen keys are hidden.  Beyond 2^60 the quotient is below the last bit anyway.)
+            if (__builtin_expect(edge, 0)) hide();
             if (a.cap_in != 0.f) {
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int y = 0; y < 32; ++y)
-                  w[c][y] = __float_as_uint(
-                      fmaf(reciprocal(ex2(__uint_as_float(w[c][y]) * a.cap_in) + 1.f), -2.f * a.cap_out, a.cap_out));
+                for (int y = 0; y < 32; y += 2) {
+                  const float e0 = ex2(at_most_60(__uint_as_float(w[c][y]) * a.cap_in)) + 1.f;
+                  const float e1 = ex2(at_most_60(__uint_as_float(w[c][y + 1]) * a.cap_in)) + 1.f;
+                  const float r = reciprocal(e0 * e1) * (-2.f * a.cap_out);
+                  w[c][y] = __float_as_uint(fmaf(r, e1, a.cap_out));
+                  w[c][y + 1] = __float_as_uint(fmaf(r, e0, a.cap_out));
+                }
             } else {
 #pragma unroll
               for (int c = 0; c < 2; ++c)
@@ -557,7 +590,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
             if (a.slopes) {
               // slope (pos_q - pos_k), less what is the same for the half's keys
-              const int j = s.j0 + t * UT + (hh & 1) * UH;
+              const int j = s.j0 + kt * UT + (hh & 1) * UH;
               away = slope * (float)(q_pos - j);
               if (s.chain || j + UH <= s.len) {
 #pragma unroll
@@ -577,25 +610,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               }
             }
           }
-          if (__builtin_expect(edge, 0)) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              // committed tokens (a chain: up to this one) below, the window's begin above
-              const int j = s.j0 + t * UT + (hh & 1) * UH + c * 32;
-              const int below = s.len + (s.chain ? tok + 1 : 0) - j;
-              uint32_t see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
-              if (a.window > 0) {
-                const int from = q_pos - a.window + 1 - j;
-                see &= from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
-              }
-              const int d = j - s.len;       // draft of the chunk's first key
-              if (!s.chain && d > -32 && d < 64)
-                see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
-#pragma unroll
-              for (int y = 0; y < 32; ++y)
-                if (!((see >> y) & 1)) w[c][y] = 0xff800000u;
-            }
-          }
+          if (__builtin_expect(edge, 0)) hide();
           float tops[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
@@ -789,7 +804,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         is_v = z >= pairs || !(z & 1);
         t = z >= pairs ? s.count - 2 + z - pairs : (z >> 1) + ((z & 1) ? 2 : 0);
       }
-      const int j = s.j0 + t * UT + lane * ua.box_rows;
+      const int j = s.j0 + (s.count - 1 - t) * UT + lane * ua.box_rows;
       page = -1;
       if (lane < boxes && j < s.limit) {
         page = __ldg(a.tables + (size_t)s.r * a.max_pages + (j >> a.shift));

@@ -137,8 +137,9 @@ def test_caps_windows_and_slopes(dim, dtype, kw, tree):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
 @pytest.mark.parametrize("groups,most", [(1, 8), (4, 8), (8, 16), (16, 16)])
-def test_what_a_row_does_not_see_does_not_reach_it(dtype, groups, most):
+def test_what_a_row_does_not_see_does_not_reach_it(dtype, groups, most, cap):
     """NaN and infinities behind the last token, in drafts of other branches and outside the window;
     rows that see nothing."""
     s = Step([40, 0, 75], [most, 7, 3], 16, 2, groups, 64, dtype, True)
@@ -155,8 +156,8 @@ def test_what_a_row_does_not_see_does_not_reach_it(dtype, groups, most):
     s.k[page(0, 43)] = math.nan                        # draft 3
     s.v[page(2, 3)] = math.nan                         # outside the window
     s.k[page(2, 4)] = math.inf
-    s.attend(window=50)
-    s.check(window=50)
+    s.attend(window=50, softcap=cap)
+    s.check(window=50, cap=cap)
 
 
 def test_rows_of_any_stride_and_reused_workspace():
