@@ -88,12 +88,55 @@ __device__ __forceinline__ void store_vec(TO* p, const float* x) {
 // T: type of q, k, v and the cache; TQ: type of q_out; VEC: values per chunk;
 // TOK: tokens per CTA.
 template <typename T, typename TQ, int VEC, int TOK>
-__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
   extern __shared__ float2 s_cs[];            // [TOK][rot / 2] cos, sin
   const int tid = threadIdx.x, half = a.rot >> 1;
   const int t0 = blockIdx.x * TOK;
+  const int groups = half / VEC, units = a.unit_heads * a.per_head;
   griddep_wait();
-  if (__syncthreads_or(load_err(a.err) != 0)) return;
+  const bool latched = load_err(a.err) != 0;
+
+  // One place of one head: values d0 .. and d1 .. of it (d1 < 0: one chunk alone; d0 < 0: none).
+  const T* src;
+  long long stride;
+  int hh, w, d0, d1;
+  bool is_q, is_v, turns;
+  Vec<T, VEC> x0[TOK], x1[TOK];
+  auto load = [&](int u) {
+    const int head = u / a.per_head;
+    w = u - head * a.per_head;
+    is_v = head >= a.Hq + a.H;
+    is_q = head < a.Hq;
+    hh = is_q ? head : is_v ? head - a.Hq - a.H : head - a.Hq;
+    src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
+    stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+    turns = !is_v && w < groups;
+    if (turns) {
+      d0 = a.offset + (a.interleaved ? 2 * w * VEC : w * VEC);
+      d1 = a.interleaved ? d0 + VEC : d0 + half;
+    } else {
+      // neighbouring chunks of what keeps its values
+      const int rot = is_v ? 0 : a.rot, c = 2 * (is_v ? w : w - groups);
+      d0 = c * VEC;
+      d1 = d0 + VEC < a.D - rot ? d0 + VEC : -1;
+      if (d0 >= a.D - rot) d0 = -1;
+      if (rot && d0 >= a.offset) d0 += rot;
+      if (rot && d1 >= a.offset) d1 += rot;
+    }
+    if (u >= units) d0 = -1;
+    if (d0 < 0) return;
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+      if (t0 + j >= a.T) continue;
+      const T* p = src + (t0 + j) * stride + (long long)hh * a.D;
+      x0[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d0));
+      if (d1 >= 0) x1[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d1));
+    }
+  };
+  // The first place's rows are on their way while slots are read and angles computed (rows of
+  // padding are read too, but go nowhere).
+  int u = blockIdx.y * blockDim.x + tid;
+  load(u);
   int slot[TOK];
 #pragma unroll
   for (int j = 0; j < TOK; ++j) {
@@ -112,103 +155,77 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotArgs a) {
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
     s_cs[x] = make_float2(cs * a.magnitude, sn * a.magnitude);
   }
-  __syncthreads();
+  if (__syncthreads_or(latched)) return;
   griddep_launch();
 
-  const int groups = half / VEC;
-  const int units = a.unit_heads * a.per_head;
-  for (int u = blockIdx.y * blockDim.x + tid; u < units; u += gridDim.y * blockDim.x) {
-    const int head = u / a.per_head, w = u - head * a.per_head;
-    const bool is_v = head >= a.Hq + a.H, is_q = head < a.Hq;
-    const int hh = is_q ? head : is_v ? head - a.Hq - a.H : head - a.Hq;
-    const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
-    const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-    // values d0 .. and d1 .. of the head (d1 < 0: one chunk alone)
-    const bool turns = !is_v && w < groups;
-    int d0, d1;
-    if (turns) {
-      d0 = a.offset + (a.interleaved ? 2 * w * VEC : w * VEC);
-      d1 = a.interleaved ? d0 + VEC : d0 + half;
-    } else {
-      // neighbouring chunks of what keeps its values
-      const int rot = is_v ? 0 : a.rot, c = 2 * (is_v ? w : w - groups);
-      d0 = c * VEC;
-      d1 = d0 + VEC;
-      if (d0 >= a.D - rot) continue;
-      if (d1 >= a.D - rot) d1 = -1;
-      if (rot && d0 >= a.offset) d0 += rot;
-      if (rot && d1 >= a.offset) d1 += rot;
-    }
-    Vec<T, VEC> x0[TOK], x1[TOK];
+  for (;;) {
+    if (d0 >= 0) {
 #pragma unroll
-    for (int j = 0; j < TOK; ++j) {
-      if (slot[j] < 0) continue;
-      const T* p = src + (t0 + j) * stride + (long long)hh * a.D;
-      x0[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d0));
-      if (d1 >= 0) x1[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d1));
-    }
+      for (int j = 0; j < TOK; ++j) {
+        if (slot[j] < 0) continue;
+        const int t = t0 + j;
+        float y0[VEC], y1[VEC];
 #pragma unroll
-    for (int j = 0; j < TOK; ++j) {
-      if (slot[j] < 0) continue;
-      const int t = t0 + j;
-      float y0[VEC], y1[VEC];
+        for (int i = 0; i < VEC; ++i) {
+          y0[i] = to_f(x0[j].x[i]);
+          y1[i] = to_f(x1[j].x[i]);
+        }
+        if (turns) {
+          const float2* cs = s_cs + j * half + w * VEC;
+          if (a.interleaved) {
+            float z[2 * VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        y0[i] = to_f(x0[j].x[i]);
-        y1[i] = to_f(x1[j].x[i]);
-      }
-      if (turns) {
-        const float2* cs = s_cs + j * half + w * VEC;
-        if (a.interleaved) {
-          float z[2 * VEC];
+            for (int i = 0; i < VEC; ++i) {
+              z[i] = y0[i];
+              z[VEC + i] = y1[i];
+            }
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            z[i] = y0[i];
-            z[VEC + i] = y1[i];
+            for (int i = 0; i < VEC; ++i) {
+              const float2 c = cs[i];
+              const float p = z[2 * i], q = z[2 * i + 1];
+              z[2 * i] = p * c.x - q * c.y;
+              z[2 * i + 1] = p * c.y + q * c.x;
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              y0[i] = z[i];
+              y1[i] = z[VEC + i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const float2 c = cs[i];
+              const float p = y0[i], q = y1[i];
+              y0[i] = p * c.x - q * c.y;
+              y1[i] = p * c.y + q * c.x;
+            }
           }
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float2 c = cs[i];
-            const float p = z[2 * i], q = z[2 * i + 1];
-            z[2 * i] = p * c.x - q * c.y;
-            z[2 * i + 1] = p * c.y + q * c.x;
-          }
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            y0[i] = z[i];
-            y1[i] = z[VEC + i];
-          }
+        }
+        if (is_q) {
+          long long row;                        // of the [.., G][D] block this head belongs to
+          if (a.n_tok == 1) row = (long long)t * a.Hq + hh;
+          else row = (((long long)(t / a.n_tok) * a.H + hh / a.G) * a.n_tok + t % a.n_tok) * a.G +
+                     hh % a.G;
+          TQ* o = static_cast<TQ*>(a.q_out) + row * a.D;
+          store_vec<TQ, VEC>(o + d0, y0);
+          if (d1 >= 0) store_vec<TQ, VEC>(o + d1, y1);
         } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float2 c = cs[i];
-            const float p = y0[i], q = y1[i];
-            y0[i] = p * c.x - q * c.y;
-            y1[i] = p * c.y + q * c.x;
+          const long long row =
+              ((((long long)(slot[j] >> a.shift) * a.H + hh) << a.shift) + (slot[j] & ((1 << a.shift) - 1)));
+          T* o = static_cast<T*>(is_v ? a.vp : a.kp) + row * a.D;
+          if (!turns) {                         // unchanged bits
+            *reinterpret_cast<typename Chunk<2 * VEC>::type*>(o + d0) = x0[j].raw;
+            if (d1 >= 0) *reinterpret_cast<typename Chunk<2 * VEC>::type*>(o + d1) = x1[j].raw;
+          } else {
+            store_vec<T, VEC>(o + d0, y0);
+            store_vec<T, VEC>(o + d1, y1);
           }
         }
       }
-      if (is_q) {
-        long long row;                        // of the [.., G][D] block this head belongs to
-        if (a.n_tok == 1) row = (long long)t * a.Hq + hh;
-        else row = (((long long)(t / a.n_tok) * a.H + hh / a.G) * a.n_tok + t % a.n_tok) * a.G +
-                   hh % a.G;
-        TQ* o = static_cast<TQ*>(a.q_out) + row * a.D;
-        store_vec<TQ, VEC>(o + d0, y0);
-        if (d1 >= 0) store_vec<TQ, VEC>(o + d1, y1);
-      } else {
-        const long long row =
-            ((((long long)(slot[j] >> a.shift) * a.H + hh) << a.shift) + (slot[j] & ((1 << a.shift) - 1)));
-        T* o = static_cast<T*>(is_v ? a.vp : a.kp) + row * a.D;
-        if (!turns) {                         // unchanged bits
-          *reinterpret_cast<typename Chunk<2 * VEC>::type*>(o + d0) = x0[j].raw;
-          if (d1 >= 0) *reinterpret_cast<typename Chunk<2 * VEC>::type*>(o + d1) = x1[j].raw;
-        } else {
-          store_vec<T, VEC>(o + d0, y0);
-          store_vec<T, VEC>(o + d1, y1);
-        }
-      }
     }
+    u += gridDim.y * blockDim.x;
+    if (u >= units) break;
+    load(u);
   }
 }
 
