@@ -818,10 +818,10 @@ cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
   const int rows = most * a.G;
   // Many units: few pieces each, a warp per row; few units: many pieces, eight.
   // (CTAs without a unit to join only cost their launch; looping over rows costs 1.5 us a round.)
-  const int groups = a.R * a.H >= 16 ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
+  const bool many = (long long)a.R * a.H * ((a.max_new + a.tpm - 1) / a.tpm) >= 16;
+  const int groups = many ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
   const dim3 grid(a.ctas, groups < 64 ? groups : 64);
-  if (a.R * a.H >= 16)
-    return launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
+  if (many) return launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
   return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
 }
 
