@@ -70,7 +70,6 @@ cudaError_t launch_tree_umma(const TreeArgs& a, int dtype, int D, int dev, cudaS
 namespace tree {
 
 constexpr int KT = 64;           // keys per tile
-constexpr int kThreads = 128;
 // fp16 weights are held times 2^6: the smallest normal one is then 2^-20 of
 // the largest, not 2^-14; with the 2^8 that a weight may reach relative to a
 // maximum not yet followed (avsg_tree_umma.cu) it is far from the type's end.
@@ -348,7 +347,9 @@ struct Walk {
 template <typename T_, int D_, int WM_>
 struct Shape {
   using T = T_;
-  static constexpr int D = D_, WM = WM_, WK = 4 / WM_, MT = 16 * WM_;
+  // Heads of 256 values leave room for one CTA per SM: eight warps, where each can have 16 keys.
+  static constexpr int D = D_, WM = WM_, WARPS = D_ == 256 && WM_ > 1 ? 8 : 4, WK = WARPS / WM_, MT = 16 * WM_;
+  static constexpr int THREADS = 32 * WARPS;
   static constexpr int NK = KT / WK;                 // keys of a tile per warp
   static constexpr int STAGES = D == 64 ? 4 : 3;
   static constexpr int CTAS_PER_SM = D == 256 ? 1 : 2;
@@ -362,8 +363,9 @@ struct Shape {
 };
 
 template <class SH>
-__global__ void __launch_bounds__(kThreads, SH::CTAS_PER_SM) tree_attn_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel(TreeArgs a) {
   using T = typename SH::T;
+  constexpr int kThreads = SH::THREADS;
   constexpr int D = SH::D, WM = SH::WM, WK = SH::WK, MT = SH::MT, NK = SH::NK, S = SH::STAGES;
   constexpr int CPR = D / 8;                         // 16-byte chunks per row
   constexpr bool HALF = std::is_same<T, __half>::value;
@@ -831,7 +833,7 @@ cudaError_t launch_one(const TreeArgs& a, int dev, cudaStream_t st) {
   static SmemLimit limit;
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(tree_attn_kernel<SH>), SH::SMEM, dev);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_attn_kernel<SH>, dim3(a.ctas), dim3(kThreads), SH::SMEM, st, a);
+    e = launch_pdl(tree_attn_kernel<SH>, dim3(a.ctas), dim3(SH::THREADS), SH::SMEM, st, a);
   return e != cudaSuccess ? e : launch_merge<T, D>(a, SH::MT, st);
 }
 
