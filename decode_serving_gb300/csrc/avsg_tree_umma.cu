@@ -35,6 +35,16 @@
 //
 // Tensor memory (512 columns): S/P of stream x at 128 x + 64 (half & 1), O at
 // 256 + 128 x.
+// What bounds it.  Up to 128 rows: HBM (16 x 8 units of 32768 tokens, 16-token
+// pages, heads of 128: 322 us, 6.65 of 6.78 TB/s).  256 rows: the tensor cores
+// (64 drafts of 4 heads over the same: 415 to 435 us, 1.3 PFLOP/s; a causal
+// 4096-token chunk after 4096: 333 us, 1.65 PFLOP/s).  A product of 128 rows
+// and 64 keys reads both operands from shared memory and takes 55 cycles, not
+// 32: the price of two places for scores.  One place of 128 keys (64 cycles a
+// product) made the streams wait for one another (533 us), and so did weights
+// in shared memory, which free the place early but cost a proxy fence a half
+// (554 us).  Short units pay about 10 us each for their beginning and end, a
+// third of it hidden by the loads that run ahead (256 x 8 units of 1000: 211 us).
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
 // the waits after it return at once.
 #include <cuda.h>
