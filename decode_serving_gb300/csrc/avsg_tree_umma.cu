@@ -12,7 +12,7 @@
 //                   output there when the maximum has grown by more than 2^8
 //                   (until then weights up to 2^8 stand in for it: the same
 //                   quotient, no pass over the output);
-//   warps 8, 10     K and V tiles by TMA in turn, one box per page, a lane each, into a
+//   warps 8, 10     K and V tiles by TMA, one box per page, a lane each, into a
 //                   ring of 160 KB that runs on into the next unit;
 //   warps 9, 11     issue the products of stream 0 and 1: S = Q K^T (both in
 //                   shared memory), O += P V (P in tensor memory).  An issuing
@@ -413,9 +413,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     int hh = 0, seg = 0, idx = 0;  // hh: halves of this stream since the start
     // V of tile t, made safe to multiply: see above.  Rows that every query sees are left alone
     // (what they hold reaches every query anyway), which without a window are all but the new
-    // tokens'.  Both streams may do the same tile: they write the same values.  Its load's number
-    // follows those of loads that this tile's scores needed by less than the ring's length, so the parity
-    // tells its phase.
+    // tokens'.  Both streams may do the same tile: they write the same values.  The load before
+    // it in its buffer came before this tile's K, which has been seen, so the parity tells.
     auto clean_v = [&](const Piece& s, bool two, int t) {
       const int n = idx + v_place(two, t, s.count), b = n % kRing;
       const int j = s.j0 + (s.count - 1 - t) * UT, rows = min(UT, s.limit - j);
@@ -790,16 +789,26 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     }
     if (tid == 0) a.head[cta] = head;
   } else if (warp == 8 || warp == 10) {
-    // ---- loads, taken in turn by two warps.  Order of a segment: two streams over all tiles:
-    // K0 V0 K1 V1 ...; one tile each in turn: K0 K1 V0 K2 V1 K3 ... -- the order in which the
-    // products use and release them.  Page ids are looked up one load ahead.
+    // ---- loads.  Order of a segment: two streams over all tiles: K0 V0 K1 V1 ...; one tile each
+    // in turn: K0 K1 V0 K2 V1 K3 ... -- the order in which the products use them.  Warp 8 fills
+    // the buffers of even number, warp 10 the others: a warp has then seen every phase of its
+    // buffers' barriers, which their parity alone does not tell apart.  Page ids are looked up
+    // one load ahead.
     Piece s;
     const int part = warp == 8 ? 0 : 1;
     const int boxes = UT / ua.box_rows;
-    int idx = part;
-    int page = -1, group = 0, is_v = 0;    // the next load's box of this lane
+    int idx = 0, buf = 0, x = 0;           // the next load: its number, its buffer, its place
     bool more = walk.next(a, s);
-    int x = part;
+    auto step = [&]() {
+      ++idx;
+      if (++buf == kRing) buf = 0;
+      if (++x == 2 * s.count) {
+        x = 0;
+        more = walk.next(a, s);
+      }
+    };
+    while (more && (buf & 1) != part) step();
+    int page = -1, group = 0, is_v = 0, to = 0, use = 0;  // this warp's next load, this lane's box
     auto look_up = [&]() {
       const bool two = s.ntok * a.G > UM;
       int t;
@@ -824,29 +833,28 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           page = -1;
         }
       }
-      if ((x += 2) >= 2 * s.count) {
-        x = part;
-        more = walk.next(a, s);
-      }
+      to = buf;
+      use = idx / kRing;
+      do step();
+      while (more && (buf & 1) != part);
     };
-    if (more) look_up();
-    bool last = false;
-    while (!last) {
-      const int now = page, now_group = group, now_v = is_v, b = idx % kRing;
-      last = !more;
+    bool have = more;
+    if (have) look_up();
+    while (have) {
+      const int now = page, now_group = group, now_v = is_v, b = to, phase = use;
+      have = more;
       if (more) look_up();
       const int n = __popc(__ballot_sync(0xffffffffu, now >= 0));
-      bar_wait(empty(b), ((idx / kRing) & 1) ^ 1, give_up, a.err);
+      bar_wait(empty(b), (phase & 1) ^ 1, give_up, a.err);
       if (lane == 0) bar_expect(full(b), n * ua.box_rows * D * 2);
       __syncwarp();
       if (now >= 0)
         tma_box(smem + M::RING + b * M::TILE + lane * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
                 now_group, now);
-      idx += 2;
     }
-    // every copy of this warp has landed before the CTA may end
-    for (int n = max(part, idx - 2 * kRing); n < idx; n += 2)
-      if (n + kRing >= idx) bar_wait(full(n % kRing), (n / kRing) & 1, give_up, a.err);
+    // every copy of this warp has landed before the CTA may end (idx: loads in all)
+    for (int b = part; b < kRing && b < idx; b += 2)
+      bar_wait(full(b), ((idx - 1 - b) / kRing) & 1, give_up, a.err);
   } else {
       // ---- products.  Up to 128 rows, both warps follow every load, in order: a tile that is the
       // other stream's is passed on, so that a buffer is filled again only when both have seen it

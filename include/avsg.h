@@ -358,7 +358,8 @@ int avsg_read_rows(const void* src, int64_t num_rows, int64_t row_bytes, const i
  * device can see (a page id outside the pool, too few free pages, a path that
  * is not increasing) is latched in d_error = {code, request, position}; the
  * first error stays, and every later call on the same d_error does nothing on
- * the device until the caller zeroes it.  All memory is the caller's, on the
+ * the device until the caller zeroes it.  avsg_page_plan calls on one d_error
+ * must not run at the same time.  All memory is the caller's, on the
  * current device (INVALID_ARG for pages of another one), and must stay valid
  * until the enqueued work is done.  Calls on several streams are independent
  * as long as nothing that one of them writes is used by another at a time.
@@ -440,8 +441,8 @@ typedef struct avsg_rotary {
  * avsg_rotary_write -- rotates q and k by their tokens' positions, writes q to
  * d_q_out and k, v to their slots of the given layer.  Angles are exact at any
  * int32 position; arithmetic is fp32, rounded once.  A token with slot -1 is
- * skipped whole (padding); a slot past the pool is skipped and latched
- * (BAD_SELECTION).  Slots must be distinct.  d_q_out may be d_q when the types
+ * skipped whole (padding); a slot past the pool is latched (BAD_SELECTION), its
+ * token not written, the call's others written or not.  Slots must be distinct.  d_q_out may be d_q when the types
  * agree, tokens_per_request is 1 and q_stride is num_q_heads * D; otherwise
  * outputs must not overlap inputs.  With page_tokens 1, num_pages T and no
  * slots, d_k and d_v are the [R][H][D] rows avsg_append takes, and with q_f32

@@ -347,7 +347,9 @@ def test_rotary_skips_and_latches_a_slot_past_the_pool():
     out = torch.zeros(3, 64, dtype=BF16, device="cuda")
     cache.rotary(x, x, x, dev(np.arange(3)), dev(np.array([1, 8, 2])), freq, out)
     assert cache.error() == (-4, -1, 1)
-    assert (out[1] == 0).all() and (out[0] == x[0]).all() and (cache.v[0, 0, 0, 2] == x[2]).all()
+    assert (out[1] == 0).all()                                 # the others: written or not
+    rows = cache.v[0, :, 0].reshape(8, 64)
+    assert all((rows[i] == 0).all() for i in (0, 3, 4, 5, 6, 7))
     out.zero_()
     cache.rotary(x, x, x, dev(np.arange(3)), dev(np.array([1, 3, 2])), freq, out)
     assert (out == 0).all()                                    # latched
