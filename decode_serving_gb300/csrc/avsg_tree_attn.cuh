@@ -738,83 +738,92 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
   if (tid == 0) a.head[cta] = head;
 }
 
-// Joins the partials of the units that cross CTAs: blockIdx.x is the CTA in
-// whose share a unit begins, blockIdx.y a group of its rows.  WPR warps work
-// on one row, each on every WPR-th piece.
+// Joins the partials of the units that cross CTAs.  WPR warps work on one row,
+// each on every WPR-th piece.  blockIdx.x is the CTA in whose share a unit
+// begins (32 of them where up to kFewUnits units are looked for), blockIdx.y a
+// group of its rows.
 constexpr int kMergeWarps = 8;
+constexpr int kFewUnits = 4;
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a, int MT) {
   constexpr int RPC = kMergeWarps / WPR;             // rows per CTA
   constexpr int VPL = D / 32;                        // values per lane
   __shared__ float s_o[kMergeWarps][D], s_sum[kMergeWarps];
   griddep_wait();
-  const int cta = blockIdx.x;
-  const int4 head = a.head[cta];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int part = warp % WPR;
-  if (head.x == 0) return;
-  for (int r0 = blockIdx.y * RPC; r0 < head.w; r0 += gridDim.y * RPC) {
-    const int row = r0 + warp / WPR;
-    const bool have = row < head.w;
-    // piece 0 is the second partial of its CTA (the unit begins there), the others the first
-    auto slot = [&](int i) { return (long long)(2 * (cta + i) + (i == 0 ? 1 : 0)) * MT + row; };
-    float top = -INFINITY;
-    if (have)
-      for (int i = lane; i < head.x; i += 32) top = fmaxf(top, a.ml[slot(i) * 2]);
+  unsigned begins = 1;
+  if constexpr (WPR > 1) {
+    const int look = blockIdx.x * 32 + lane;
+    begins = __ballot_sync(0xffffffffu, look < a.ctas && a.head[min(look, a.ctas - 1)].x != 0);
+  }
+  for (; begins; begins &= begins - 1) {
+    const int cta = WPR > 1 ? blockIdx.x * 32 + __ffs(begins) - 1 : blockIdx.x;
+    const int4 head = a.head[cta];
+    if (head.x == 0) continue;
+    for (int r0 = blockIdx.y * RPC; r0 < head.w; r0 += gridDim.y * RPC) {
+      const int row = r0 + warp / WPR;
+      const bool have = row < head.w;
+      // piece 0 is the second partial of its CTA (the unit begins there), the others the first
+      auto slot = [&](int i) { return (long long)(2 * (cta + i) + (i == 0 ? 1 : 0)) * MT + row; };
+      float top = -INFINITY;
+      if (have)
+        for (int i = lane; i < head.x; i += 32) top = fmaxf(top, a.ml[slot(i) * 2]);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float use = top == -INFINITY ? 0.f : top;
-    float o[VPL], sum = 0.f;
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float use = top == -INFINITY ? 0.f : top;
+      float o[VPL], sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < VPL; ++x) o[x] = 0.f;
-    if (have)
+      for (int x = 0; x < VPL; ++x) o[x] = 0.f;
+      if (have)
 #pragma unroll 8
-      for (int i = part; i < head.x; i += WPR) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.ml + slot(i) * 2);
-        const float f = ex2(ml.x - use);
-        sum += ml.y * f;
-        const float* p = a.part + slot(i) * D + lane * VPL;
-        if constexpr (VPL >= 4) {
+        for (int i = part; i < head.x; i += WPR) {
+          const float2 ml = *reinterpret_cast<const float2*>(a.ml + slot(i) * 2);
+          const float f = ex2(ml.x - use);
+          sum += ml.y * f;
+          const float* p = a.part + slot(i) * D + lane * VPL;
+          if constexpr (VPL >= 4) {
 #pragma unroll
-          for (int x = 0; x < VPL; x += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(p + x);
-            o[x] += y.x * f;
-            o[x + 1] += y.y * f;
-            o[x + 2] += y.z * f;
-            o[x + 3] += y.w * f;
+            for (int x = 0; x < VPL; x += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(p + x);
+              o[x] += y.x * f;
+              o[x + 1] += y.y * f;
+              o[x + 2] += y.z * f;
+              o[x + 3] += y.w * f;
+            }
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            o[0] += y.x * f;
+            o[1] += y.y * f;
           }
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(p);
-          o[0] += y.x * f;
-          o[1] += y.y * f;
         }
-      }
-    if constexpr (WPR > 1) {
+      if constexpr (WPR > 1) {
 #pragma unroll
-      for (int x = 0; x < VPL; ++x) s_o[warp][lane * VPL + x] = o[x];
-      if (lane == 0) s_sum[warp] = sum;
-      __syncthreads();
-      if (part == 0) {
+        for (int x = 0; x < VPL; ++x) s_o[warp][lane * VPL + x] = o[x];
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (part == 0) {
 #pragma unroll
-        for (int w = 1; w < WPR; ++w) {
-          sum += s_sum[warp + w];
+          for (int w = 1; w < WPR; ++w) {
+            sum += s_sum[warp + w];
 #pragma unroll
-          for (int x = 0; x < VPL; ++x) o[x] += s_o[warp + w][lane * VPL + x];
+            for (int x = 0; x < VPL; ++x) o[x] += s_o[warp + w][lane * VPL + x];
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
-    }
-    if (!have || part != 0) continue;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int lt = row / a.G, gg = row - lt * a.G;
-    const long long at = (long long)(head.y + lt) * a.H * a.G + head.z * a.G + gg;
-    unsigned char* dst = a.out + (at * D + lane * VPL) * 2;
+      if (!have || part != 0) continue;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int lt = row / a.G, gg = row - lt * a.G;
+      const long long at = (long long)(head.y + lt) * a.H * a.G + head.z * a.G + gg;
+      unsigned char* dst = a.out + (at * D + lane * VPL) * 2;
 #pragma unroll
-    for (int x = 0; x < VPL; x += 2)
-      *reinterpret_cast<uint32_t*>(dst + x * 2) = pack<T>(o[x] * inv, o[x + 1] * inv);
-    if (a.lse && lane == 0) {
-      constexpr float shift = std::is_same<T, __half>::value ? kHalfShift : 0.f;
-      a.lse[at] = sum == 0.f ? -INFINITY : (top - shift) * 0.6931471805599453f + logf(sum);
+      for (int x = 0; x < VPL; x += 2)
+        *reinterpret_cast<uint32_t*>(dst + x * 2) = pack<T>(o[x] * inv, o[x + 1] * inv);
+      if (a.lse && lane == 0) {
+        constexpr float shift = std::is_same<T, __half>::value ? kHalfShift : 0.f;
+        a.lse[at] = sum == 0.f ? -INFINITY : (top - shift) * 0.6931471805599453f + logf(sum);
+      }
     }
   }
 }
@@ -824,13 +833,16 @@ template <typename T, int D>
 cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
   const int most = a.max_new < a.tpm ? a.max_new : a.tpm;
   const int rows = most * a.G;
-  // Many units: few pieces each, a warp per row; few units: many pieces, eight.
-  // (CTAs without a unit to join only cost their launch; looping over rows costs 1.5 us a round.)
-  const bool many = (long long)a.R * a.H * ((a.max_new + a.tpm - 1) / a.tpm) >= 16;
-  const int groups = many ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
-  const dim3 grid(a.ctas, groups < 64 ? groups : 64);
-  if (many) return launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
-  return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, grid, dim3(kMergeWarps * 32), 0, st, a, MT);
+  // A few units lie in up to 304 CTAs' shares: eight warps on a row (one: 16 us for 304
+  // pieces), a block for 32 shares (one unit of 256 rows, 32768 tokens: 31 us the call, 80 with
+  // a block for each share).
+  if ((long long)a.R * a.H * ((a.max_new + a.tpm - 1) / a.tpm) <= kFewUnits)
+    return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, dim3((a.ctas + 31) / 32, rows),
+                      dim3(kMergeWarps * 32), 0, st, a, MT);
+  // Else a warp per row, in few groups: every CTA of the grid without a unit to join costs its
+  // launch (304 x 32 of them 5 us), a further round of rows 1.5 us.
+  const int groups = (rows + kMergeWarps - 1) / kMergeWarps;
+  return launch_pdl(tree_merge_kernel<T, D, 1>, dim3(a.ctas, groups), dim3(kMergeWarps * 32), 0, st, a, MT);
 }
 
 template <typename T, int D, int WM>

@@ -383,9 +383,10 @@ def test_a_step_gives_the_definition():
 @pytest.mark.parametrize("lens,new,groups,dim,dtype", [
     ([0, 1, 127, 128, 129, 700], [1, 1, 1, 1, 1, 1], 4, 128, BF16),
     ([513, 0, 64], [2, 3, 1], 5, 64, F16),
+    ([300, 31, 64, 1], [4, 8, 5, 1], 4, 128, F16),
 ])
 def test_few_rows_with_a_small_and_a_large_pool(lens, new, groups, dim, dtype, spare):
-    """Up to 16 rows per kv-head run on either kernel, by the pool's tokens per request."""
+    """Up to 32 rows per kv-head run on either kernel, by the pool's tokens per request."""
     s = Step(lens, new, 16, 2, groups, dim, dtype, False)
     if spare:
         from decode_serving_gb300.paged import PagedCache
