@@ -25,11 +25,10 @@ Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   // 4000 tokens up to 16 rows, 2000 up to 32; with 64 rows it is never far behind.  Lengths are
   // not known here; the pool's tokens per request are.
   const int64_t room = (int64_t)p->num_pages * p->page_tokens / p->num_requests;
-  x.umma = p->page_tokens >= 8 && p->head_dim <= 128 &&
-           (rows > 32 || room >= (rows > 16 ? 4096 : 8192));
+  x.umma = p->page_tokens >= 8 && (rows > 32 || room >= (rows > 16 ? 4096 : 8192));
   // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
   x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  x.MT = x.umma ? 256 : 16 * x.wm;
+  x.MT = !x.umma ? 16 * x.wm : p->head_dim == 256 ? 128 : 256;
   x.ctas = x.umma || p->head_dim == 256 ? sms : 2 * sms;
   return x;
 }

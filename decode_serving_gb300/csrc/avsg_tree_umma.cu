@@ -55,7 +55,6 @@ namespace avsg {
 namespace tree {
 namespace {
 
-constexpr int UT = 128;                    // keys per tile
 constexpr int UM = 128;                    // rows per stream
 constexpr int kUmmaThreads = 384;
 constexpr int UH = 64;                     // keys per half tile
@@ -70,10 +69,13 @@ struct UmmaArgs {
 
 template <int D>
 struct Mem {
+  static constexpr bool SOLO = D > 128;    // one stream
+  static constexpr int UT = SOLO ? UH : 2 * UH;  // keys per tile
+  static constexpr int ROWS = SOLO ? UM : 2 * UM;  // rows of a unit
   static constexpr int Q = UM * D * 2;     // bytes of one stream's rows
   static constexpr int TILE = UT * D * 2;
-  static constexpr int BUFS = D == 128 ? 5 : 10;  // 160 KB either way
-  static constexpr int RING = 2 * Q;
+  static constexpr int BUFS = D == 64 ? 10 : 5;  // 160 KB either way
+  static constexpr int RING = SOLO ? Q + 2 * UM * 4 : 2 * Q;  // (m and l of the rows, see s_m)
   static constexpr int BARS = RING + BUFS * TILE;
   static constexpr int SMEM = BARS + 8 * (2 * BUFS + 16);
 };
@@ -284,8 +286,9 @@ template <typename T, typename TO, int D>
 __device__ __noinline__ void add_bad_values(const TreeArgs& a, const Piece& s, const unsigned char* q, int tok,
                                             int q_pos, unsigned long long bits, float slope, float ref,
                                             float inv, TO* row) {
+  constexpr int UT = Mem<D>::UT;
   for (int t = 0; t < s.count; ++t) {
-    if (!s.edge<UT>(t, a.window)) continue;
+    if (!s.edge<Mem<D>::UT>(t, a.window)) continue;
     const int end = min(s.j0 + (t + 1) * UT, s.limit);
     for (int j = a.window > 0 ? s.j0 + t * UT : max(s.j0 + t * UT, s.all_see); j < end; ++j) {
       const int page = a.tables[(size_t)s.r * a.max_pages + (j >> a.shift)];
@@ -336,7 +339,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     tree_umma_kernel(UmmaArgs ua, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
   using M = Mem<D>;
-  constexpr int kRing = M::BUFS;
+  constexpr int kRing = M::BUFS, UT = M::UT;
+  constexpr bool SOLO = M::SOLO;
   constexpr bool HALF = std::is_same<T, __half>::value;
   constexpr float SHIFT = HALF ? kHalfShift : 0.f;
   constexpr int COLS = D / 64;             // blocks of 64 columns
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   const int cta = blockIdx.x;
   const uint32_t smem = smem_u32(smem_raw);
   float* s_m = reinterpret_cast<float*>(smem_raw + M::Q);  // (where up to 128 rows leave stream 1's q free)
-  float* s_l = s_m + 2 * UM;
+  float* s_l = s_m + (SOLO ? UM : 2 * UM);
   const uint32_t bars = smem + M::BARS;
   auto full = [&](int b) { return bars + 8 * b; };
   auto empty = [&](int b) { return bars + 8 * (kRing + b); };
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     };
     for (; s_more[seg & 1]; ++seg) {
       const Piece& s = s_piece[seg & 1];
-      const bool two = s.ntok * a.G > UM;
+      const bool two = !SOLO && s.ntok * a.G > UM;
       const int rl = two ? x * UM + row : row;
       const bool mine = rl < s.ntok * a.G;
       const int lt = rl / a.G, gg = rl - lt * a.G;
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         s_more[(seg + 1) & 1] = s_walk.next(a, s_piece[(seg + 1) & 1]);
       }
       float m = -INFINITY, l = 0.f;
-      const int halves = 2 * (two ? s.count : (s.count - x + 1) >> 1);
+      const int halves = SOLO ? (x == 0 ? s.count : 0) : 2 * (two ? s.count : (s.count - x + 1) >> 1);
       // tiles e0 .. e1 - 1 of the piece are seen whole by every row (Piece::edge)
       const int e1 = min(s.count, max(0, s.all_see - s.j0) / UT);
       const int e0 = a.window > 0 ? max(0, (s.far_pos - a.window - s.j0 + UT) / UT) : 0;
@@ -539,13 +543,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         tm_ld32(ts0 + 64 * (hh & 1) + 32, w[1]);
       }
       for (int i = 0; i < halves; ++i, ++hh) {
-        const int t = two ? i >> 1 : (i & ~1) + x;
+        const int t = SOLO ? i : two ? i >> 1 : (i & ~1) + x, half = SOLO ? 0 : hh & 1;  // tile, its half
         const int kt = last - t;           // place among the piece's keys
         const bool edge = kt < e0 || kt >= e1;
         const uint32_t ts = ts0 + 64 * (hh & 1);
         if (!warp_live) {                  // only padding: nobody reads what these rows give
           wait_scores(hh);
-          if (__builtin_expect(edge && !(hh & 1), 0)) clean_v(s, two, t);
+          if (__builtin_expect(edge && half == 0, 0)) clean_v(s, two, t);
           tc_fence_before();
           warp_arrive(p_full(x, hh & 1), lane);
           continue;
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             // committed tokens (a chain: up to this one) below, the window's begin above
-            const int j = s.j0 + kt * UT + (hh & 1) * UH + c * 32;
+            const int j = s.j0 + kt * UT + half * UH + c * 32;
             const int below = s.len + (s.chain ? tok + 1 : 0) - j;
             uint32_t see = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
             if (a.window > 0) {
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
             if (a.slopes) {
               // slope (pos_q - pos_k), less what is the same for the half's keys
-              const int j = s.j0 + kt * UT + (hh & 1) * UH;
+              const int j = s.j0 + kt * UT + half * UH;
               away = slope * (float)(q_pos - j);
               if (s.chain || j + UH <= s.len) {
 #pragma unroll
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         tm_st16(ts, w[0]);                 // over scores that have been read
         tm_st16(ts + 16, w[1]);
         l += sum;
-        if (__builtin_expect(edge && !(hh & 1), 0)) clean_v(s, two, t);
+        if (__builtin_expect(edge && half == 0, 0)) clean_v(s, two, t);
         __syncwarp();
         // the next half's scores come while P is stored, where they are there already
         const bool more = i + 1 < halves;
@@ -738,9 +742,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       // ---- the end of the piece
       // Up to 128 rows the two streams' outputs are joined here (stream 1 has none in a piece of
       // one tile), half of the columns by either stream's warps.
-      const bool join = !two && s.count > 1;
+      const bool join = !SOLO && !two && s.count > 1;
       bar_wait(o_last(x), seg & 1, give_up, a.err);
-      if (!two) {
+      if (!two && (!SOLO || x == 0)) {
         s_m[UM * x + row] = m;
         s_l[UM * x + row] = l;
       }
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const float sum = l * f0 + l1 * f1;
       const float inv = s.whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
       const long long at = (long long)(s.f + max(tok, 0)) * a.H * a.G + s.h * a.G + gg;
-      const long long slot = ((long long)(2 * cta + (s.begins ? 1 : 0)) * (2 * UM) + rl);
+      const long long slot = ((long long)(2 * cta + (s.begins ? 1 : 0)) * M::ROWS + rl);
       if (warp_live) {
         const uint32_t from = two ? to : tmem + lanes + 256;
         const float g0 = f0 * inv, g1 = f1 * inv;  // (inv is 1 where the output is not divided yet)
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     while (more && (buf & 1) != part) step();
     int page = -1, group = 0, is_v = 0, to = 0, use = 0;  // this warp's next load, this lane's box
     auto look_up = [&]() {
-      const bool two = s.ntok * a.G > UM;
+      const bool two = !SOLO && s.ntok * a.G > UM;
       int t;
       if (two) {
         t = x >> 1;
@@ -909,7 +913,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       auto scores = [&](int x, int q, uint32_t k, int hh) {
         __syncwarp();
         const uint32_t qa = uniform(operand_low(smem + q * M::Q)), to = uniform(tmem + 128 * x + 64 * (hh & 1));
-        const uint32_t ka = uniform(operand_low(k + (hh & 1) * HALF_TILE)), bar = uniform(s_full(x, hh & 1));
+        const uint32_t ka = uniform(operand_low(k + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(s_full(x, hh & 1));
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -924,7 +928,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         bar_wait(p_full(x, hh & 1), (hh >> 1) & 1, give_up, a.err);
         tc_fence_after();
         __syncwarp();
-        const uint32_t va = uniform(operand_low(v + (hh & 1) * HALF_TILE)), bar = uniform(o_done(x));
+        const uint32_t va = uniform(operand_low(v + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(o_done(x));
         const uint32_t from = uniform(tmem + 128 * x + 64 * (hh & 1)), to = uniform(tmem + 256 + 128 * x);
         const uint32_t add = uniform(first ? 0 : 1);
         if (elect_one()) {
@@ -946,9 +950,31 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         if (elect_one()) mma_commit(bar);
       };
       while (walk.next(a, s)) {
-        const bool two = s.ntok * a.G > UM;
+        const bool two = !SOLO && s.ntok * a.G > UM;
         const int x = me;
-        if (two) {
+        if (SOLO && me == 1) {
+          for (int i = 0; i < 2 * s.count; ++i) {
+            wait_load(i);
+            pass_on(i);
+          }
+        } else if (SOLO) {
+          bar_wait(q_one, q1 & 1, give_up, a.err);
+          ++q1;
+          tc_fence_after();
+          for (int t = 0; t < 2 && t < s.count; ++t) {
+            scores(0, 0, wait_load(t), ps + t);
+            release(t);
+          }
+          for (int t = 0; t < s.count; ++t) {
+            const int place = v_place(false, t, s.count);
+            output(0, wait_load(place), ps + t, t == 0);
+            release(place);
+            if (t + 2 < s.count) {
+              scores(0, 0, wait_load(place + 1), ps + t + 2);
+              release(place + 1);
+            }
+          }
+        } else if (two) {
           const int hh = ps;
           bar_wait(q_full(x), qs & 1, give_up, a.err);
           ++qs;
@@ -1011,7 +1037,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         }
         // (also where stream 1 has no tile: its softmax warps wait for this warp to have come by)
         finish(x);
-        ps += 2 * (two ? s.count : (s.count + 1 - me) >> 1);
+        ps += SOLO ? s.count : 2 * (two ? s.count : (s.count + 1 - me) >> 1);
         idx += 2 * s.count;
         __syncwarp();
       }
@@ -1062,13 +1088,13 @@ cudaError_t launch_umma_one(const TreeArgs& a, int dtype, int dev, cudaStream_t 
   if (e != cudaSuccess) return e;
   UmmaArgs u{};
   u.t = a;
-  u.box_rows = (1 << a.shift) < UT ? 1 << a.shift : UT;
+  u.box_rows = (1 << a.shift) < Mem<D>::UT ? 1 << a.shift : Mem<D>::UT;
   u.q_vec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_stride % 8 == 0;
   CUtensorMap k_map, v_map;
   if (!encode_pages(&k_map, a.k, a, dtype, D, u.box_rows) || !encode_pages(&v_map, a.v, a, dtype, D, u.box_rows))
     return cudaErrorInvalidValue;
   e = launch_pdl(kernel, dim3(a.ctas), dim3(kUmmaThreads), Mem<D>::SMEM, st, u, k_map, v_map);
-  return e != cudaSuccess ? e : launch_merge<T, D>(a, 2 * UM, st);
+  return e != cudaSuccess ? e : launch_merge<T, D>(a, Mem<D>::ROWS, st);
 }
 
 template <typename T, int D>
@@ -1082,9 +1108,11 @@ cudaError_t launch_umma(const TreeArgs& a, int dtype, int dev, cudaStream_t st) 
 
 cudaError_t launch_tree_umma(const TreeArgs& a, int dtype, int D, int dev, cudaStream_t st) {
   if (dtype == AVSG_BF16)
-    return D == 64 ? tree::launch_umma<__nv_bfloat16, 64>(a, dtype, dev, st)
-                   : tree::launch_umma<__nv_bfloat16, 128>(a, dtype, dev, st);
-  return D == 64 ? tree::launch_umma<__half, 64>(a, dtype, dev, st)
-                 : tree::launch_umma<__half, 128>(a, dtype, dev, st);
+    return D == 64    ? tree::launch_umma<__nv_bfloat16, 64>(a, dtype, dev, st)
+           : D == 128 ? tree::launch_umma<__nv_bfloat16, 128>(a, dtype, dev, st)
+                      : tree::launch_umma<__nv_bfloat16, 256>(a, dtype, dev, st);
+  return D == 64    ? tree::launch_umma<__half, 64>(a, dtype, dev, st)
+         : D == 128 ? tree::launch_umma<__half, 128>(a, dtype, dev, st)
+                    : tree::launch_umma<__half, 256>(a, dtype, dev, st);
 }
 }  // namespace avsg

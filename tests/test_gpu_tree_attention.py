@@ -384,6 +384,8 @@ def test_a_step_gives_the_definition():
     ([0, 1, 127, 128, 129, 700], [1, 1, 1, 1, 1, 1], 4, 128, BF16),
     ([513, 0, 64], [2, 3, 1], 5, 64, F16),
     ([300, 31, 64, 1], [4, 8, 5, 1], 4, 128, F16),
+    ([0, 63, 64, 65, 1500], [1, 2, 3, 1, 2], 3, 256, BF16),
+    ([700, 0, 129], [8, 5, 1], 4, 256, F16),
 ])
 def test_few_rows_with_a_small_and_a_large_pool(lens, new, groups, dim, dtype, spare):
     """Up to 32 rows per kv-head run on either kernel, by the pool's tokens per request."""
