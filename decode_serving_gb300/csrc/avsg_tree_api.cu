@@ -17,15 +17,17 @@ struct Plan {
 Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   const int64_t rows = (int64_t)G * max_new;
   Plan x;
-  // tcgen05 (avsg_tree_umma.cu): boxes of whole 8-row groups, an output that fits the tensor
-  // memory twice.  It always works on 128 rows; with few rows it pays where contexts are long
-  // (8 x 8 units, one token, 16000 tokens: 91 us against 99; 32 x 8 units, 32 rows, 3000 tokens:
-  // 80 against 89) and costs 4 to 10 us a call where they are short (8 x 8 units, one token, 300
-  // tokens: 17.4 against 11.6; 32 x 8 units, 32 rows, 50 tokens: 22 against 12).  Equal at about
-  // 4000 tokens up to 16 rows, 2000 up to 32; with 64 rows it is never far behind.  Lengths are
-  // not known here; the pool's tokens per request are.
+  // tcgen05 (avsg_tree_umma.cu): boxes of whole 8-row groups.  It always works on 128 rows; with
+  // few rows it pays where contexts are long (8 x 8 units, one token, 16000 tokens: 91 us against
+  // 99; 32 x 8 units, 32 rows, 3000 tokens: 80 against 89) and costs 4 to 10 us a call where they
+  // are short (8 x 8 units, one token, 300 tokens: 17.4 against 11.6; 32 x 8 units, 32 rows, 50
+  // tokens: 22 against 12).  Equal at about 4000 tokens up to 16 rows, 2000 up to 32; with 64 rows
+  // it is never far behind.  Heads of 256: equal at 1000 (32 x 8 units, one token, 2000 tokens: 94
+  // against 122; 50 tokens: 21 against 17).  Lengths are not known here; the pool's tokens per
+  // request are.
   const int64_t room = (int64_t)p->num_pages * p->page_tokens / p->num_requests;
-  x.umma = p->page_tokens >= 8 && (rows > 32 || room >= (rows > 16 ? 4096 : 8192));
+  const int64_t enough = p->head_dim == 256 ? 1024 : rows > 16 ? 4096 : 8192;
+  x.umma = p->page_tokens >= 8 && (rows > 32 || room >= enough);
   // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
   x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   x.MT = !x.umma ? 16 * x.wm : p->head_dim == 256 ? 128 : 256;

@@ -952,15 +952,17 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       while (walk.next(a, s)) {
         const bool two = !SOLO && s.ntok * a.G > UM;
         const int x = me;
+        if (SOLO) {
+          bar_wait(q_one, q1 & 1, give_up, a.err);  // (both warps: the end of the unit before)
+          ++q1;
+          tc_fence_after();
+        }
         if (SOLO && me == 1) {
           for (int i = 0; i < 2 * s.count; ++i) {
             wait_load(i);
             pass_on(i);
           }
         } else if (SOLO) {
-          bar_wait(q_one, q1 & 1, give_up, a.err);
-          ++q1;
-          tc_fence_after();
           for (int t = 0; t < 2 && t < s.count; ++t) {
             scores(0, 0, wait_load(t), ps + t);
             release(t);

@@ -421,6 +421,17 @@ def test_thousands_of_requests(groups):
     s.check(only=set(range(0, 3000, 97)) | {2999})
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF16), (256, BF16)])
+@pytest.mark.parametrize("most", [9, 150])
+def test_many_short_units(dim, dtype, most):
+    """Several units in a CTA's share, of one tile and of a few (of 40 rows and more: on tcgen05)."""
+    lens = [(i * 37) % 200 for i in range(600 if most < 64 else 60)]
+    s = Step(lens, [5 + i % 5 if most < 64 else most - i for i in range(len(lens))], 16, 1, 8, dim, dtype,
+             most < 64)
+    s.attend()
+    s.check(only=set(range(0, len(lens), 31)) | {len(lens) - 1})
+
+
 def test_two_streams_with_a_workspace_each():
     """Two caches' attention at the same time gives what each gives alone."""
     steps = [Step([4000, 17], [5, 8], 16, 2, 4, 128, BF16, True, seed=k) for k in (1, 2)]
@@ -466,7 +477,8 @@ def test_two_graphs_share_a_workspace_in_turn():
     assert torch.equal(s.out, want[0]) and torch.equal(few.out, want[1])
 
 
-@pytest.mark.parametrize("dim,dtype,window", [(128, BF16, 0), (64, F16, 0), (128, F16, 300)])
+@pytest.mark.parametrize("dim,dtype,window", [(128, BF16, 0), (64, F16, 0), (128, F16, 300),
+                                              (256, BF16, 0), (256, F16, 300)])
 def test_a_late_maximum(dim, dtype, window):
     """Scores that grow along the keys, so that the output is scaled again and again; and keys of
     large scores at the very end and the very beginning."""
