@@ -13,6 +13,7 @@ struct Plan {
   int wm;      // the other kernel's warps along the rows
   int MT;      // rows per m-tile
   int ctas;
+  int begin;   // see TreeArgs
 };
 Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   const int64_t rows = (int64_t)G * max_new;
@@ -31,6 +32,12 @@ Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
   x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   x.MT = !x.umma ? 16 * x.wm : p->head_dim == 256 ? 128 : 256;
+  // Eight units of one tile take 6 us each on tcgen05, where 64 KB of K and V take 1.5 us, and
+  // longer with many rows; about 2 us with mma.sync, where a tile does.  8 against 4 for eight
+  // requests of 1 to 20000 tokens with 64 drafts each: 55 us against 61 (2: 79, 16: 59); heads of
+  // 256: 72 against 78 for 256 chunks of 300.  6 against 4 for 32 x 8 units of 300 tokens, one
+  // token, heads of 256: 30 us against 33.
+  x.begin = !x.umma ? 1 : rows > 32 ? 8 : p->head_dim == 256 ? 6 : 4;
   x.ctas = x.umma || p->head_dim == 256 ? sms : 2 * sms;
   return x;
 }
@@ -126,6 +133,7 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   a.window = t->window;
   a.ctas = x.ctas;
   a.min_tiles = 2;
+  a.begin = x.begin;
   a.score_log2 = scale * log2e;
   if (t->softcap > 0.f) {
     a.cap_in = 2.f * log2e * scale / t->softcap;

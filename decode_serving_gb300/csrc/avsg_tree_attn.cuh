@@ -62,6 +62,9 @@ struct TreeArgs {
   int tpm;                       // tokens per m-tile
   int window;
   int ctas, min_tiles;
+  // What the beginning and the end of a unit cost a CTA (its q rows, the first scores, the
+  // output), in tiles: the shares count it, or a CTA with many short units would finish late.
+  int begin;
   float score_log2;              // scale * log2(e)
   float cap_in, cap_out;         // 2 log2(e) scale / cap, cap * log2(e); cap_in 0: no cap
 };
@@ -70,7 +73,7 @@ struct TreeArgs {
 cudaError_t launch_tree_d64(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 cudaError_t launch_tree_d128(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 cudaError_t launch_tree_d256(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
-// D of 64 or 128, pages of at least 8 tokens, up to 256 rows per m-tile (avsg_tree_umma.cu).
+// Pages of at least 8 tokens, 256 rows per m-tile, 128 for D of 256 (avsg_tree_umma.cu).
 cudaError_t launch_tree_umma(const TreeArgs& a, int dtype, int D, int dev, cudaStream_t st);
 
 namespace tree {
@@ -169,31 +172,23 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
   return sum;
 }
 
-// What the beginning and the end of a unit cost a CTA (its q rows, the first
-// scores, the output), in tiles of its kernel: the shares count it, or a CTA
-// with many short units would finish late.  Measured on eight units of one
-// tile: 6 us each where a tile of 128 keys takes 1.5 us, about 2 us with the
-// tiles of 64 keys.
-template <int KT>
-__host__ __device__ constexpr int kBegin() { return KT == 128 ? 4 : 1; }
-
 // One request as the kernels see it.  A request with a bad length is latched
 // and has no work.  Its rows are cut into mts units of tpm tokens per kv-head.
 template <int KT>
 struct Req {
-  int len, n, f, lo, mts;
+  int len, n, f, lo, mts, begin;
   bool chain;
 
-  // Places of unit mt in the list: kBegin<KT>() for its beginning, then its
+  // Places of unit mt in the list: `begin` for its beginning, then its
   // tiles, counted from key lo, up to the last key that a row may see.
   __device__ int places(int mt, int tpm) const {
-    return kBegin<KT>() + (len - lo + (chain ? min(n, (mt + 1) * tpm) : n) + KT - 1) / KT;
+    return begin + (len - lo + (chain ? min(n, (mt + 1) * tpm) : n) + KT - 1) / KT;
   }
   // Places of the units before mt.
   __device__ long long before(int mt, int tpm) const {
     if (mt == 0) return 0;
     if (!chain) return (long long)mt * places(0, tpm);
-    return (long long)mt * kBegin<KT>() + floor_sum(mt, KT, tpm, (long long)(len - lo) + tpm + KT - 1);
+    return (long long)mt * begin + floor_sum(mt, KT, tpm, (long long)(len - lo) + tpm + KT - 1);
   }
   __device__ long long per_head(int tpm) const {
     return n ? before(mts - 1, tpm) + places(mts - 1, tpm) : 0;
@@ -206,6 +201,7 @@ __device__ __forceinline__ Req<KT> load_req(const TreeArgs& a, int r) {
   const int end = a.first[r + 1];
   q.len = a.len[r];
   q.n = end - q.f;
+  q.begin = a.begin;
   int code = 0;
   if (q.f < 0 || end < q.f || end > a.T || q.len < 0) code = AVSG_ERR_BAD_SELECTION;
   else if (q.n > a.max_new ||
@@ -319,7 +315,7 @@ struct Walk {
       p.all_see = q.len + (q.chain ? p.tok0 + 1 : 0);
       p.far_pos = q.len + (q.chain ? p.tok0 + p.ntok : q.n) - 1;
       // tiles that lie before the window of every row have no work
-      int skip = kBegin<KT>();
+      int skip = a.begin;
       if (a.window > 0 && q.chain)
         skip += max(0, (q.len + p.tok0 - a.window + 1 - q.lo) / KT);
       at += t1 - t0;
@@ -339,7 +335,7 @@ struct Walk {
       }
       const int from = max(t0, skip);
       if (from >= t1) continue;
-      p.j0 = lo + (from - kBegin<KT>()) * KT;
+      p.j0 = lo + (from - a.begin) * KT;
       p.count = t1 - from;
       p.begins = t0 <= skip;
       p.whole = p.begins && t1 == all;

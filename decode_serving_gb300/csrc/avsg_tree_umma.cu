@@ -1,4 +1,4 @@
-// Tree attention for heads of 64 or 128 values on the 5th-generation tensor
+// Tree attention on the 5th-generation tensor
 // cores (tcgen05, accumulators in tensor memory), K and V fetched by TMA.
 //
 // The same operation and the same equal shares of one list of tiles as in
@@ -29,12 +29,17 @@
 // More than 128 rows: stream x holds rows 128x .. and both use every tile (K
 // and V are read once for 256 rows).  Up to 128 rows: the streams take the
 // even and the odd tiles, with an output each, joined at the end of the unit.
+// Heads of 256: two outputs would leave no tensor memory for scores, so there
+// is stream 0 alone, of 128 rows, with tiles of 64 keys (a tile is its half):
+// the products of one half hide the softmax of the next.  Stream 1's softmax
+// warps write half of the output, its issuing warp passes every tile on.
 //
 // Tiles are taken from the last key backwards: where scores carry a distance
 // bias, the largest come first and the output is hardly ever scaled.
 //
 // Tensor memory (512 columns): S/P of stream x at 128 x + 64 (half & 1), O at
 // 256 + 128 x.
+//
 // What bounds it.  Up to 128 rows: HBM (16 x 8 units of 32768 tokens, 16-token
 // pages, heads of 128: 322 us, 6.65 of 6.78 TB/s).  256 rows: the tensor cores
 // (64 drafts of 4 heads over the same: 415 to 435 us, 1.3 PFLOP/s; a causal
@@ -43,8 +48,10 @@
 // 32: the price of two places for scores.  One place of 128 keys (64 cycles a
 // product) made the streams wait for one another (533 us), and so did weights
 // in shared memory, which free the place early but cost a proxy fence a half
-// (554 us).  Short units pay about 10 us each for their beginning and end, a
-// third of it hidden by the loads that run ahead (256 x 8 units of 1000: 211 us).
+// (554 us).  Heads of 256: 605 us for 16 x 8 units of 32768 tokens (7.1 TB/s), 710 us for
+// 4096 after 4096 (1.55 PFLOP/s).  Short units pay 6 to 10 us each for their beginning and
+// end, a third of it hidden by the loads that run ahead (256 x 8 units of 1000 tokens, 64
+// rows: 233 us, 256 rows: 384 us).
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
 // the waits after it return at once.
 #include <cuda.h>
