@@ -32,7 +32,11 @@
 // Heads of 256: two outputs would leave no tensor memory for scores, so there
 // is stream 0 alone, of 128 rows, with tiles of 64 keys (a tile is its half):
 // the products of one half hide the softmax of the next.  Stream 1's softmax
-// warps write half of the output, its issuing warp passes every tile on.
+// warps write half of the output, its issuing warp passes every tile on.  Q lies
+// in tensor memory, where stream 1's scores would be: a product of 64 keys then
+// takes 32 cycles (4096 after 4096: 621 us, 710 with both operands in shared
+// memory).  The ring has 128 KB there; with 192 or 224 HBM gives less (16 x 8
+// units of 32768 tokens: 626 and 632 us, 605 so).
 //
 // Tiles are taken from the last key backwards: where scores carry a distance
 // bias, the largest come first and the output is hardly ever scaled.
@@ -48,8 +52,8 @@
 // 32: the price of two places for scores.  One place of 128 keys (64 cycles a
 // product) made the streams wait for one another (533 us), and so did weights
 // in shared memory, which free the place early but cost a proxy fence a half
-// (554 us).  Heads of 256: 605 us for 16 x 8 units of 32768 tokens (7.1 TB/s), 710 us for
-// 4096 after 4096 (1.55 PFLOP/s).  Short units pay 6 to 10 us each for their beginning and
+// (554 us).  Heads of 256: 605 us for 16 x 8 units of 32768 tokens (7.1 TB/s), 621 us for
+// 4096 after 4096 (1.77 PFLOP/s).  Short units pay 6 to 10 us each for their beginning and
 // end, a third of it hidden by the loads that run ahead (256 x 8 units of 1000 tokens, 64
 // rows: 233 us, 256 rows: 384 us).
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
@@ -79,10 +83,12 @@ struct Mem {
   static constexpr bool SOLO = D > 128;    // one stream
   static constexpr int UT = SOLO ? UH : 2 * UH;  // keys per tile
   static constexpr int ROWS = SOLO ? UM : 2 * UM;  // rows of a unit
-  static constexpr int Q = UM * D * 2;     // bytes of one stream's rows
+  static constexpr int Q = SOLO ? 0 : UM * D * 2;  // bytes of one stream's rows
   static constexpr int TILE = UT * D * 2;
-  static constexpr int BUFS = D == 64 ? 10 : 5;  // 160 KB either way
-  static constexpr int RING = SOLO ? Q + 2 * UM * 4 : 2 * Q;  // (m and l of the rows, see s_m)
+  static constexpr int BUFS = D == 64 ? 10 : D == 128 ? 5 : 4;  // 160 KB, 128 KB for D of 256
+  // Heads of 256: m and l of the rows (see s_m), then q on its way to tensor memory in padded rows.
+  static constexpr int STAGE = 2 * UM * 4, STAGE_ROW = D * 2 + 16;
+  static constexpr int RING = SOLO ? (STAGE + UM * STAGE_ROW + 1023) / 1024 * 1024 : 2 * Q;
   static constexpr int BARS = RING + BUFS * TILE;
   static constexpr int SMEM = BARS + 8 * (2 * BUFS + 16);
 };
@@ -485,7 +491,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           for (int it = 0; it < 32 / RPI; ++it) {
             const bool ok = r < rows;
             const unsigned char* src = ok ? base + (t * a.q_stride + g * D) * 2 : a.q;
-            const uint32_t dst = to + (at / 8) * (1024 * COLS) + (at & 7) * 128 + (((ch & 7) ^ (at & 7)) << 4);
+            const uint32_t dst =
+                SOLO ? smem + M::STAGE + at * M::STAGE_ROW + ch * 16
+                     : to + (at / 8) * (1024 * COLS) + (at & 7) * 128 + (((ch & 7) ^ (at & 7)) << 4);
             if (ua.q_vec) {
               cp_async16(dst, src, ok ? 16 : 0);
             } else {
@@ -523,7 +531,27 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       }
       if (q_loading) {
         cp_wait<0>();
-        async_fence();
+        if constexpr (SOLO) {              // on to tensor memory, a row by the thread that owns it
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t r[32];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const uint4 z =
+                  *reinterpret_cast<const uint4*>(smem_raw + M::STAGE + row * M::STAGE_ROW + c * 128 + y * 16);
+              r[4 * y] = z.x;
+              r[4 * y + 1] = z.y;
+              r[4 * y + 2] = z.z;
+              r[4 * y + 3] = z.w;
+            }
+            tm_st32(tmem + lanes + 128 + c * 32, r);
+          }
+          tm_wait_st();
+          tc_fence_before();
+        } else {
+          async_fence();
+        }
       }
       if (two || x == 0) warp_arrive(two ? q_full(x) : q_one, lane);
 
@@ -920,12 +948,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       auto scores = [&](int x, int q, uint32_t k, int hh) {
         __syncwarp();
         const uint32_t qa = uniform(operand_low(smem + q * M::Q)), to = uniform(tmem + 128 * x + 64 * (hh & 1));
+        const uint32_t to_q = uniform(tmem + 128);   // (heads of 256)
         const uint32_t ka = uniform(operand_low(k + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(s_full(x, hh & 1));
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * 1024 + (ks % 4) * 32) >> 4;
-            mma_ss(to, operand<COLS>(qa + off), operand<COLS>(ka + off), id_s, ks > 0);
+            if constexpr (SOLO) mma_ts(to, to_q + ks * 8, operand<COLS>(ka + off), id_s, ks > 0);
+            else mma_ss(to, operand<COLS>(qa + off), operand<COLS>(ka + off), id_s, ks > 0);
           }
           mma_commit(bar);
         }
