@@ -32,12 +32,12 @@ Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
   x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   x.MT = !x.umma ? 16 * x.wm : p->head_dim == 256 ? 128 : 256;
-  // Eight units of one tile take 6 us each on tcgen05, where 64 KB of K and V take 1.5 us, and
-  // longer with many rows; about 2 us with mma.sync, where a tile does.  8 against 4 for eight
-  // requests of 1 to 20000 tokens with 64 drafts each: 55 us against 61 (2: 79, 16: 59); heads of
-  // 256: 72 against 78 for 256 chunks of 300.  6 against 4 for 32 x 8 units of 300 tokens, one
-  // token, heads of 256: 30 us against 33.
-  x.begin = !x.umma ? 1 : rows > 32 ? 8 : p->head_dim == 256 ? 6 : 4;
+  // Eight units of one tile take 6 us each on tcgen05, where 64 KB of K and V take 1.5 us; longer
+  // with more of q and out.  About 2 us with mma.sync, where a tile does.  Eight requests of 1 to
+  // 20000 tokens, 64 drafts each, heads of 128: 57 us, with 4 61, with 2 79, with 16 59; heads of
+  // 256 and 1 to 32768: 113 us with 8, 129 with 6; 32 x 8 units of 300, one token: 29 us with 6, 33
+  // with 4.
+  x.begin = !x.umma ? 1 : (rows > 32 ? 6 : 4) + (p->head_dim == 256 ? 2 : 0);
   x.ctas = x.umma || p->head_dim == 256 ? sms : 2 * sms;
   return x;
 }
@@ -86,7 +86,7 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   if (rc != AVSG_OK) return rc;
   if (t->num_tokens < 0 || t->layer < 0 || t->layer >= p->num_layers || t->window < 0 ||
       !(t->softmax_scale >= 0.f) || isinf(t->softmax_scale) || !(t->softcap >= 0.f) ||
-      isinf(t->softcap) || t->reserved0 != 0)
+      isinf(t->softcap * 1.4426950408889634f) || t->reserved0 != 0)
     return AVSG_ERR_INVALID_ARG;
   if (t->num_tokens == 0) return AVSG_OK;
   const int64_t row = (int64_t)p->num_kv_heads * t->q_per_kv * p->head_dim;

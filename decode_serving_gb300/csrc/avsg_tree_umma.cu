@@ -291,6 +291,13 @@ __device__ __forceinline__ int v_place(bool two, int t, int count) {
   return two ? 2 * t + 1 : count == 1 ? 1 : 2 + t + min(t, count - 2);
 }
 
+// One capped score, in units of log 2.
+__device__ __forceinline__ float capped(const TreeArgs& a, float x) {
+  const float t = x * a.cap_in * kCapUnit, u = t * t;
+  if (fabsf(t) <= kCapNear) return t * a.cap_out * fmaf(fmaf(fmaf(kCap3, u, kCap2), u, kCap1), u, 1.f);
+  return a.cap_out * (1.f - __fdividef(2.f, ex2(x * a.cap_in) + 1.f));
+}
+
 // Adds what the products left out: values of V that are not finite, in tiles
 // that some rows see only in part, times this row's weights (rows that do not
 // see them are thus not reached).  `row` is the row's written output, `ref`
@@ -330,7 +337,7 @@ __device__ __noinline__ void add_bad_values(const TreeArgs& a, const Piece& s, c
         const float2 y = unpack<T>(reinterpret_cast<const uint32_t*>(q)[d]), z = unpack<T>(k[d]);
         x += y.x * z.x + y.y * z.y;
       }
-      if (a.cap_in != 0.f) x = a.cap_out * (1.f - __fdividef(2.f, ex2(x * a.cap_in) + 1.f));
+      if (a.cap_in != 0.f) x = capped(a, x);
       else x *= a.score_log2;
       const float p = unpack<T>(pack<T>(ex2(x - slope * (float)(q_pos - k_pos) - ref), 0.f)).x;
       if (p == 0.f) continue;
@@ -629,16 +636,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 for (int y = 0; y < 32; y += 2)
                   far = max3(far, fabsf(__uint_as_float(w[c][y])), fabsf(__uint_as_float(w[c][y + 1])));
             }
-            // x / cap within a half, for all of the warp's scores: tanh(t) = t (1 + c1 t^2 + c2 t^4 +
-            // c3 t^6), fitted to the least largest error (2e-7, below that of the quotient).  It
-            // leaves the special functions to the weights (16 x 8 units of 32768 tokens, 256 rows,
-            // D 128: 655 us, with the quotient 723, without a cap 444).
-            const float k = a.cap_in * 0.34657359028f;
-            if (a.cap_in != 0.f && __all_sync(0xffffffffu, far * k <= 0.5f)) {
+            // Near 0 a polynomial: it leaves the special functions to the weights (16 x 8 units of
+            // 32768 tokens, 256 rows, D 128: 655 us, with the quotient 723, without a cap 444).
+            const float k = a.cap_in * kCapUnit;
+            if (a.cap_in != 0.f && __all_sync(0xffffffffu, far * k <= kCapNear)) {
               const float co = a.cap_out;
-              const uint64_t k2 = pair(k, k), one = pair(co, co), c1 = pair(-0.33326461f * co, -0.33326461f * co),
-                             c2 = pair(0.13185862f * co, 0.13185862f * co),
-                             c3 = pair(-0.04422929f * co, -0.04422929f * co);
+              const uint64_t k2 = pair(k, k), one = pair(co, co), c1 = pair(kCap1 * co, kCap1 * co),
+                             c2 = pair(kCap2 * co, kCap2 * co), c3 = pair(kCap3 * co, kCap3 * co);
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll

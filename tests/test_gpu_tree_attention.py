@@ -136,6 +136,17 @@ def test_caps_windows_and_slopes(dim, dtype, kw, tree):
     s.check(slopes=slopes, **kw)
 
 
+@pytest.mark.parametrize("dim,page,new", [(64, 4, 12), (128, 16, 12), (256, 4, 12), (256, 16, 12), (128, 16, 2)])
+def test_a_cap_far_above_the_scores(dim, page, new):
+    """It changes a score s by s (s / cap)^2 / 3: here, below 50, by less than 2^-24 of itself, so the
+    result is held to the one without a cap."""
+    s = Step([300, 40], [new, new], page, 2, 4, dim, F16, True)
+    s.attend(softcap=1e6)
+    s.check()
+    s.attend(softcap=3.0, slopes=dev(np.full(8, 0.25, np.float32), torch.float32))
+    s.check(cap=3.0, slopes=np.full(8, 0.25, np.float32))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("cap", [0.0, 20.0])
 @pytest.mark.parametrize("groups,most", [(1, 8), (4, 8), (8, 16), (16, 16)])
