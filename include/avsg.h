@@ -475,7 +475,7 @@ typedef struct avsg_tree {
   int32_t layer;
   int32_t window;       /* 0: none */
   float softmax_scale;  /* 0 selects 1/sqrt(D) */
-  float softcap;        /* 0: none */
+  float softcap;        /* 0: none; below 2^127 */
   int32_t reserved0;    /* must be 0 */
   int64_t q_stride;     /* values between tokens of d_q, even */
   const void* d_q;      /* rows of [H][G][D], the cache's type, 4-byte aligned */

@@ -85,6 +85,7 @@ def test_bad_rotary(lib, kw, code):
     (dict(num_tokens=-1), -1), (dict(q_per_kv=0), -1), (dict(q_per_kv=65), -7), (dict(max_new=0), -1),
     (dict(layer=2), -1), (dict(layer=-1), -1), (dict(window=-1), -1), (dict(softmax_scale=-1.0), -1),
     (dict(softmax_scale=math.inf), -1), (dict(softcap=-1.0), -1), (dict(softcap=math.nan), -1),
+    (dict(softcap=3e38), -1),
     (dict(reserved0=1), -1), (dict(q_stride=255), -1), (dict(q_stride=257), -1), (dict(d_q=None), -1),
     (dict(d_q=2), -1), (dict(d_first=None), -1), (dict(d_out=None), -1), (dict(d_out=8), -1),
     (dict(d_work=None), -1), (dict(d_work=128), -1),
