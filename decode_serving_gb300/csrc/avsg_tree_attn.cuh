@@ -174,10 +174,18 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 
 // cap tanh(t) for t = x / cap within a half: t (1 + c1 t^2 + c2 t^4 + c3 t^6), fitted to the least
 // largest error (2e-7; near 0 the relative error vanishes, so that a cap far above the scores
-// leaves them as they are).  Both kernels take it where all of a warp's scores are that small, and
-// cap (1 - 2 / (exp(2 t) + 1)) elsewhere, whose error is a rounding of the cap.
+// leaves them as they are).  Elsewhere cap (1 - 2 / (exp(2 t) + 1)), whose error is a rounding of the
+// cap.
 constexpr float kCapNear = 0.5f, kCap1 = -0.33326461f, kCap2 = 0.13185862f, kCap3 = -0.04422929f;
 constexpr float kCapUnit = 0.34657359028f;  // t = x cap_in log(2) / 2
+// The largest |t| of a row's scores that takes the polynomial; far: the largest |t| that the row sees
+// among the keys at hand.  All of them or none: a row then depends on nothing but what it sees, and
+// where a warp's rows agree one of the two is all that is computed.  A cap so large that its rounding
+// (cap 2^-22, in units of log 2) would show beside that of a 16-bit weight (2^-9) decides score by score.
+constexpr float kCapLarge = 512.f;
+__device__ __forceinline__ float cap_polynomial_reach(float far, float cap_out) {
+  return far <= kCapNear || cap_out > kCapLarge ? kCapNear : -1.f;
+}
 
 // One request as the kernels see it.  A request with a bad length is latched
 // and has no work.  Its rows are cut into mts units of tpm tokens per kv-head.
@@ -550,27 +558,75 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         }
         bad_v = __syncthreads_or(mine);              // (also: K has been read by every warp)
       }
+      // Whether key (x, y) is seen by its row; how far away it is.
+      auto sees = [&](int x, int y, int& far) {
+        const int j = j0 + wk * NK + x * 8 + 2 * c + (y & 1), row = y >> 1;
+        const int jd = j - pc.len;
+        bool see = true;
+        int k_pos = j;
+        if (jd >= 0) {
+          if (pc.chain) {
+            see = jd <= tok[row];
+          } else {
+            see = jd < pc.n && ((bits[row] >> (jd & 63)) & 1);
+            k_pos = pc.len + s_depth[jd & 63];
+          }
+        }
+        far = q_pos[row] - k_pos;
+        return see && !(a.window > 0 && far >= a.window);
+      };
       if (a.cap_in != 0.f) {
         // (in units of log 2)
         const float k = a.cap_in * kCapUnit, co = a.cap_out;
-        float far = 0.f;
-#pragma unroll
-        for (int x = 0; x < NK / 8; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) far = fmaxf(far, fabsf(s[x][y]));
-        if (__all_sync(0xffffffffu, far * k <= kCapNear)) {
+        if (edge) {
+          // what a row does not see must not choose how its scores are capped
 #pragma unroll
           for (int x = 0; x < NK / 8; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const float t = s[x][y] * k, u = t * t;
-              s[x][y] = t * fmaf(fmaf(fmaf(kCap3 * co, u, kCap2 * co), u, kCap1 * co), u, co);
+              int far;
+              if (!sees(x, y, far)) s[x][y] = 0.f;
             }
-        } else {
+        }
+        float far[2] = {0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < NK / 8; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) far[y >> 1] = fmaxf(far[y >> 1], fabsf(s[x][y]));
+        auto near = [&](float t) {
+          const float u = t * t;
+          return t * fmaf(fmaf(fmaf(kCap3 * co, u, kCap2 * co), u, kCap1 * co), u, co);
+        };
+        auto quotient = [&](float x) { return co * (1.f - __fdividef(2.f, ex2(x * a.cap_in) + 1.f)); };
+        if (__all_sync(0xffffffffu, fmaxf(far[0], far[1]) * k <= kCapNear)) {
 #pragma unroll
           for (int x = 0; x < NK / 8; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) s[x][y] = co * (1.f - __fdividef(2.f, ex2(s[x][y] * a.cap_in) + 1.f));
+            for (int y = 0; y < 4; ++y) s[x][y] = near(s[x][y] * k);
+        } else {
+          float reach[2];
+          bool none = true;                          // no row near (padding rows have no say)
+#pragma unroll
+          for (int row = 0; row < 2; ++row) {
+            far[row] = fmaxf(far[row], __shfl_xor_sync(0xffffffffu, far[row], 1));
+            far[row] = fmaxf(far[row], __shfl_xor_sync(0xffffffffu, far[row], 2));
+            reach[row] = cap_polynomial_reach(far[row] * k, co);
+            none = none && (tok[row] < 0 || reach[row] < 0.f);
+          }
+          if (__all_sync(0xffffffffu, none)) {
+#pragma unroll
+            for (int x = 0; x < NK / 8; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) s[x][y] = quotient(s[x][y]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < NK / 8; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float t = s[x][y] * k;
+                s[x][y] = fabsf(t) <= reach[y >> 1] ? near(t) : quotient(s[x][y]);
+              }
+          }
         }
       } else {
 #pragma unroll
@@ -583,21 +639,9 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         for (int x = 0; x < NK / 8; ++x)
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int j = j0 + wk * NK + x * 8 + 2 * c + (y & 1), row = y >> 1;
-            const int jd = j - pc.len;
-            bool see = true;
-            int k_pos = j;
-            if (jd >= 0) {
-              if (pc.chain) {
-                see = jd <= tok[row];
-              } else {
-                see = jd < pc.n && ((bits[row] >> (jd & 63)) & 1);
-                k_pos = pc.len + s_depth[jd & 63];
-              }
-            }
-            const int far = q_pos[row] - k_pos;
-            if (a.window > 0 && far >= a.window) see = false;
-            s[x][y] = see ? s[x][y] - slope[row] * (float)far : -INFINITY;
+            int far;
+            const bool see = sees(x, y, far);
+            s[x][y] = see ? s[x][y] - slope[y >> 1] * (float)far : -INFINITY;
           }
       }
       float corr[2];

@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           warp_arrive(p_full(x, hh & 1), lane);
           continue;
         }
-        // keys that the row does not see
-        auto hide = [&]() {
+        // gives the keys that the row does not see this value
+        auto hide = [&](uint32_t with) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             // committed tokens (a chain: up to this one) below, the window's begin above
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               see |= d >= 0 ? (uint32_t)(bits >> d) : (uint32_t)(bits << -d);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              if (!((see >> y) & 1)) w[c][y] = 0xff800000u;
+              if (!((see >> y) & 1)) w[c][y] = with;
           }
         };
         // The weights are taken relative to the maximum so far while this half's is found: neither
@@ -630,44 +630,70 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             scale = 1.f;
             float far = 0.f;
             if (a.cap_in != 0.f) {
+              // What a row does not see must not choose how its scores are capped, nor reach, as
+              // a NaN, the score that it shares a reciprocal with.
+              if (__builtin_expect(edge, 0)) hide(0u);
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int y = 0; y < 32; y += 2)
                   far = max3(far, fabsf(__uint_as_float(w[c][y])), fabsf(__uint_as_float(w[c][y + 1])));
             }
-            // Near 0 a polynomial: it leaves the special functions to the weights (16 x 8 units of
-            // 32768 tokens, 256 rows, D 128: 655 us, with the quotient 723, without a cap 444).
-            const float k = a.cap_in * kCapUnit;
-            if (a.cap_in != 0.f && __all_sync(0xffffffffu, far * k <= kCapNear)) {
-              const float co = a.cap_out;
-              const uint64_t k2 = pair(k, k), one = pair(co, co), c1 = pair(kCap1 * co, kCap1 * co),
-                             c2 = pair(kCap2 * co, kCap2 * co), c3 = pair(kCap3 * co, kCap3 * co);
+            // The polynomial for a row whose scores of this half are all near 0, the quotient for the
+            // others (see cap_polynomial_reach).  Where all rows are near, the special functions are
+            // left to the weights (16 x 8 units of 16384 tokens, 256 rows, D 128: 367 us; the
+            // quotient alone 431, both of them 532; without a cap 227).
+            const float k = a.cap_in * kCapUnit, co = a.cap_out;
+            const uint64_t k2 = pair(k, k), one = pair(co, co), c1 = pair(kCap1 * co, kCap1 * co),
+                           c2 = pair(kCap2 * co, kCap2 * co), c3 = pair(kCap3 * co, kCap3 * co);
+            auto near = [&](uint64_t t) {
+              const uint64_t u = mul2(t, t);
+              return mul2(t, fma2(fma2(fma2(c3, u, c2), u, c1), u, one));
+            };
+            // cap tanh(x / cap) = cap (1 - 2 / (exp(2 x / cap) + 1)); two scores share a reciprocal.
+            // Beyond 2^60 the quotient is below the last bit anyway.
+            auto quotient = [&](float s0, float s1, float& x0, float& x1) {
+              const float e0 = ex2(at_most_60(s0 * a.cap_in)) + 1.f;
+              const float e1 = ex2(at_most_60(s1 * a.cap_in)) + 1.f;
+              const float r = reciprocal(e0 * e1) * (-2.f * co);
+              x0 = fmaf(r, e1, co);
+              x1 = fmaf(r, e0, co);
+            };
+            // (padding rows, whose scores are 0, have no say)
+            if (a.cap_in != 0.f && __all_sync(0xffffffffu, !mine || far * k <= kCapNear)) {
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int y = 0; y < 32; y += 2) {
-                  const uint64_t t = mul2(pair(__uint_as_float(w[c][y]), __uint_as_float(w[c][y + 1])), k2);
-                  const uint64_t u = mul2(t, t);
                   float x0, x1;
-                  unpair(mul2(t, fma2(fma2(fma2(c3, u, c2), u, c1), u, one)), x0, x1);
+                  unpair(near(mul2(pair(__uint_as_float(w[c][y]), __uint_as_float(w[c][y + 1])), k2)), x0, x1);
+                  w[c][y] = __float_as_uint(x0);
+                  w[c][y + 1] = __float_as_uint(x1);
+                }
+            } else if (a.cap_in != 0.f && __all_sync(0xffffffffu, !mine || cap_polynomial_reach(far * k, co) < 0.f)) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int y = 0; y < 32; y += 2) {
+                  float x0, x1;
+                  quotient(__uint_as_float(w[c][y]), __uint_as_float(w[c][y + 1]), x0, x1);
                   w[c][y] = __float_as_uint(x0);
                   w[c][y + 1] = __float_as_uint(x1);
                 }
             } else if (a.cap_in != 0.f) {
-              // cap tanh(x / cap) = cap (1 - 2 / (exp(2 x / cap) + 1)).  Two share a reciprocal, so
-              // that a NaN reaches its neighbour: only the row's own, once unseen keys are hidden.
-              // Beyond 2^60 the quotient is below the last bit anyway.
-              if (__builtin_expect(edge, 0)) hide();
+              const float reach = cap_polynomial_reach(far * k, co);
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int y = 0; y < 32; y += 2) {
-                  const float e0 = ex2(at_most_60(__uint_as_float(w[c][y]) * a.cap_in)) + 1.f;
-                  const float e1 = ex2(at_most_60(__uint_as_float(w[c][y + 1]) * a.cap_in)) + 1.f;
-                  const float r = reciprocal(e0 * e1) * (-2.f * a.cap_out);
-                  w[c][y] = __float_as_uint(fmaf(r, e1, a.cap_out));
-                  w[c][y + 1] = __float_as_uint(fmaf(r, e0, a.cap_out));
+                  const float s0 = __uint_as_float(w[c][y]), s1 = __uint_as_float(w[c][y + 1]);
+                  const uint64_t t = mul2(pair(s0, s1), k2);
+                  float t0, t1, n0, n1, x0, x1;
+                  unpair(t, t0, t1);
+                  unpair(near(t), n0, n1);
+                  quotient(s0, s1, x0, x1);
+                  w[c][y] = __float_as_uint(fabsf(t0) <= reach ? n0 : x0);
+                  w[c][y + 1] = __float_as_uint(fabsf(t1) <= reach ? n1 : x1);
                 }
             } else {
 #pragma unroll
@@ -697,7 +723,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               }
             }
           }
-          if (__builtin_expect(edge, 0)) hide();
+          if (__builtin_expect(edge, 0)) hide(0xff800000u);
           float tops[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {

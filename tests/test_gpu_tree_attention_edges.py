@@ -1,0 +1,82 @@
+"""Tree attention where a result may depend on what it must not: values that a row does not see, the
+place of a tile's border, words and bits that stand for nothing, the stream of a call."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_paged import BF16, F16, dev, host
+from test_gpu_tree_attention import Step
+
+pytestmark = pytest.mark.gpu
+
+# (groups, dim, page): few rows and pages of fewer than 8 tokens run on mma.sync, the others on tcgen05;
+# 12 drafts of 4 heads are one stream's rows, of 16 heads two streams'.
+KERNELS = [(1, 64, 16), (4, 64, 4), (4, 256, 4), (4, 64, 16), (16, 64, 16), (4, 128, 16), (16, 128, 16), (4, 256, 16)]
+
+
+def unseen_places(s, window):
+    """(page, row) of keys that no row sees: behind the last token, outside every window."""
+    out = []
+    for r, (length, n) in enumerate(zip(s.lens.tolist(), s.new)):
+        out += [(r, p) for p in range(max(0, length - window + 1))]
+        out += [(r, p) for p in range(length + n, -(-(length + n) // s.page) * s.page)]
+    return [s.row(r, p) for r, p in out]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+def test_unseen_keys_leave_a_large_cap_alone(groups, dim, page, dtype):
+    """A cap of 1e6 changes scores below 50 by less than 2^-24 of themselves, whatever the keys hold
+    that a row does not see: no bit of the result may depend on them."""
+    window, draft = 50, 2
+    s = Step([40, 0, 75], [12, 7, 3], page, 2, groups, dim, dtype, True)
+    s.htables = host(s.cache.tables)
+    at = unseen_places(s, window)
+    a, b = s.row(0, 40 + draft)                        # seen by its branch only
+    blind = torch.from_numpy(np.array([not (int(m) >> draft) & 1 or t >= 12 for t, m in enumerate(s.mask)])).cuda()
+    results = []
+    for value in (0.0, math.inf, -3e4, math.nan):
+        for x, y in at + [(a, b)]:
+            s.k[0, x, :, y] = 0.0
+            s.k[0, x, :, y, 3] = value                 # (its scores: infinities, large ones, NaN)
+        s.attend(window=window, softcap=1e6)
+        results.append((s.out[blind].clone(), s.lse[blind].clone()))
+        if value == 0.0:
+            s.check(window=window)                     # the definition without a cap
+    assert s.cache.error()[0] == 0
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+
+
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+def test_a_row_is_capped_by_what_it_sees(groups, dim, page):
+    """Scores beyond half of the cap, of one row or of all: the same bits whatever the other rows see,
+    and for a large cap as near the definition as small scores are."""
+    s = Step([200, 9], [12, 5], page, 2, groups, dim, BF16, True)
+    s.htables = host(s.cache.tables)
+    blind = torch.from_numpy(np.array([not (int(m) >> 2) & 1 or t >= 12 for t, m in enumerate(s.mask)])).cuda()
+    for cap in (2.0, 30.0, 1e5):
+        results = []
+        for value in (0.0, 2.0**50):
+            a, b = s.row(0, 202)                       # draft 2, seen by its branch only
+            s.k[0, a, :, b] = 0.0
+            s.k[0, a, :, b, 3] = value
+            s.attend(softcap=cap)
+            results.append((s.out[blind].clone(), s.lse[blind].clone()))
+            if cap < 1e5 or value == 0.0:
+                s.check(cap=cap)
+        assert all(torch.equal(x, y) for x, y in zip(*results))
+    # a seen score of -cap, which has no weight, leaves the small ones beside it as exact as one of
+    # -512 / sqrt(dim) does, whose weight is below 1e-13
+    a, b = s.row(0, 30)
+    s.q[:, :, 3] = 1.0
+    s.k[0, a, :, b] = 0.0
+    results = []
+    for value in (-512.0, -2.0**50):
+        s.k[0, a, :, b, 3] = value
+        s.attend(softcap=1e5)
+        results.append((s.out.clone(), s.lse.clone()))
+        s.check(cap=1e5)
+    assert all(torch.equal(x, y) for x, y in zip(*results))
