@@ -250,8 +250,9 @@ __global__ void __launch_bounds__(kPlanThreads) keep_lengths_kernel(KeepArgs a) 
   }
   __syncthreads();
   // This CTA's share of the kept paths (strictly increasing, inside the
-  // request) and of the pages that go back; a failure reaches the other CTAs
-  // through the error word, read after the barrier.
+  // request), of the pages that stay and whose rows move, and of those that go
+  // back (which rows may come from); a failure reaches the other CTAs through
+  // the error word, read after the barrier.
   if (ok) {
     const int warp = rank * (kPlanThreads / 32) + (tid >> 5), warps = ctas * (kPlanThreads / 32);
     if (a.path)
@@ -261,6 +262,11 @@ __global__ void __launch_bounds__(kPlanThreads) keep_lengths_kernel(KeepArgs a) 
           const int x = a.path[f + i], before = i ? a.path[f + i - 1] : -1;
           if (x <= before || x < 0 || x >= n) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, i);
         }
+        if (k > 0 && a.path[f + k - 1] != k - 1)
+          for (int x = (a.len[r] >> a.shift) + (tid & 31); x < s_from[r]; x += 32) {
+            const int32_t id = a.tables[(size_t)r * a.max_pages + x];
+            if (id < 0 || id >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
+          }
       }
     for (int e = rank * kPlanThreads + tid; e < (int)total; e += ctas * kPlanThreads) {
       const int r = find_request(s_back, a.R, e);
@@ -336,6 +342,7 @@ __global__ void __launch_bounds__(kMoveThreads) keep_rows_kernel(MoveArgs a) {
   const int columns = a.H * 2 * a.chunks;
   auto offset = [&](int p, int h, int c) -> long long {
     const int32_t page = row[p >> a.shift];
+    // (checked before by keep_lengths_kernel: a table that was changed since is not followed)
     if (page < 0 || page >= a.num_pages) {
       raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, p);
       return -1;

@@ -389,3 +389,32 @@ def test_refusals_of_the_cache():
         c.rotary(x, x, x, i(2), i(2), f, x, rot_offset=2)
     with pytest.raises(ValueError):
         PagedCache(c.k, c.v, c.tables, c.lens, c.free[:4], c.free_count)
+
+
+@pytest.mark.parametrize("page_of,path", [
+    (2, [0, 2, 5, 7]),                                 # the page of both the rows and their places
+    (2, [0, 1, 8, 11]),                                # of the places alone: the rows lie in the next one
+    (3, [0, 1, 8, 11, 12, 13, 14, 15, 16, 17]),        # of rows and, in part, places; a page is returned behind it
+])
+def test_keep_checks_the_pages_that_stay_before_it_changes_anything(page_of, path):
+    b = Batch([3, 40], 16, room=3, spare=9, layers=2)
+    b.plan([20, 26], 46)
+    paths = np.zeros(46, np.int32)
+    paths[:3] = [0, 5, 9]                              # request 0 moves rows of its own
+    paths[20:20 + len(path)] = path
+    b.cache.tables[1, page_of] = 1 << 20
+    state = (b.cache.lens, b.cache.free, b.cache.free_count, b.k.view(torch.int16), b.v.view(torch.int16))
+    before = [host(x).copy() for x in state]
+    b.cache.keep(b.first, dev(paths), dev(np.array([3, len(path)])))
+    assert b.cache.error()[:2] == (-4, 1)
+    for x, y in zip(state, before):
+        assert (host(x) == y).all()
+
+
+def test_keep_reads_no_page_whose_rows_stay():
+    """A path that keeps its rows where they are asks nothing of the pages that stay."""
+    b = Batch([3, 40], 16, room=3, spare=9)
+    b.plan([20, 8], 28)
+    b.cache.tables[1, 2] = 1 << 20
+    b.cache.keep(b.first, dev(np.concatenate([np.arange(20), np.arange(8)])), dev(np.array([3, 4])))
+    assert b.cache.error()[0] == 0 and host(b.cache.lens).tolist() == [6, 44]
