@@ -226,7 +226,8 @@ class PagedCache:
 
     def error(self):
         """(code, request, position) of the first latched device error, code 0
-        for none; waits for the device."""
+        for none; waits for the device (all of its streams)."""
+        torch.cuda.synchronize(self.device)
         return tuple(self._error.tolist()[:3])
 
     def clear_error(self):

@@ -418,3 +418,22 @@ def test_keep_reads_no_page_whose_rows_stay():
     b.cache.tables[1, 2] = 1 << 20
     b.cache.keep(b.first, dev(np.concatenate([np.arange(20), np.arange(8)])), dev(np.array([3, 4])))
     assert b.cache.error()[0] == 0 and host(b.cache.lens).tolist() == [6, 44]
+
+
+def test_error_waits_for_every_stream():
+    from decode_serving_gb300.paged import PagedCache, rotary_frequencies
+    cache = PagedCache.allocate(1, 1, 2, 1, 4, 64)
+    freq = rotary_frequencies(64).cuda()
+    x = torch.randn(3, 64, device="cuda").to(BF16)
+    out = torch.zeros(3, 64, dtype=BF16, device="cuda")
+    pos, slots = dev(np.arange(3)), dev(np.array([1, 8, 2]))      # slot 8 is past the pool
+    side = torch.cuda.Stream()
+    cache.rotary(x, x, x, pos, dev(np.arange(3)), freq, out)      # (the first launch loads the kernel)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    assert cache.error()[0] == 0
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                            # about 0.1 s
+    cache.rotary(x, x, x, pos, slots, freq, out, stream=side.cuda_stream)
+    assert cache.error() == (-4, -1, 1)
