@@ -51,6 +51,10 @@ class PagedCache:
     tables [requests][max_pages], lens [requests], free [num_pages] and
     free_count [1] int32.  New tokens are ragged rows: request r owns rows
     first[r] .. first[r + 1] of every per-token tensor.
+
+    Calls are enqueued on torch's current stream, so that they follow the
+    tensors' own work and are captured with it; ``stream`` names another one by
+    its handle (0: the default stream).
     """
 
     def __init__(self, k, v, tables, lens, free, free_count):
@@ -116,11 +120,15 @@ class PagedCache:
                              f"{list(shape)} with strides {list(stride)}")
         return stride[0] if shape[0] > 1 else width
 
+    def _stream(self, stream):
+        """The handle to launch on (the raw form of torch.cuda.current_stream, without its object)."""
+        return (torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream) or None
+
     def _heads(self, t):
         """Heads of a row tensor [T][heads * head_dim] or [T][heads][head_dim]."""
         return t.shape[1] if t.dim() == 3 else t.shape[1] // self.head_dim
 
-    def plan(self, new, first, slots, positions, mask=None, free_count_out=None, stream=0):
+    def plan(self, new, first, slots, positions, mask=None, free_count_out=None, stream=None):
         """Tables, slots and positions of the step's new tokens.  new [requests],
         first [requests + 1], slots and positions [capacity] int32; mask
         [tokens] int64 words of ancestor bits; free_count_out defaults to the
@@ -137,12 +145,13 @@ class PagedCache:
             masks = mask.numel()
             self._check("mask", mask, torch.int64, masks)
         rc = self._plan(self._at, new.data_ptr(), None if mask is None else mask.data_ptr(), masks, capacity,
-                        first.data_ptr(), slots.data_ptr(), positions.data_ptr(), out.data_ptr(), stream or None)
+                        first.data_ptr(), slots.data_ptr(), positions.data_ptr(), out.data_ptr(),
+                        self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_page_plan")
 
     def rotary(self, q, k, v, positions, slots, freq, q_out, layer=0, rot_offset=0,
-               interleaved=False, magnitude=1.0, tokens_per_request=1, stream=0):
+               interleaved=False, magnitude=1.0, tokens_per_request=1, stream=None):
         """Rotates q into q_out and k into the pages, stores v beside it.
 
         q [T][q_heads * head_dim] (or [T][q_heads][head_dim]), k and v like it
@@ -164,7 +173,7 @@ class PagedCache:
         rc = self._rotary(self._at, _ROTARY.pack(
             tokens, heads, 2 * pairs, rot_offset, interleaved, f32, tokens_per_request, layer, qs, ks, vs,
             magnitude, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
-            0 if slots is None else slots.data_ptr(), q_out.data_ptr()), stream or None)
+            0 if slots is None else slots.data_ptr(), q_out.data_ptr()), self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_rotary_write")
 
@@ -174,7 +183,7 @@ class PagedCache:
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def attend(self, q, first, out, max_new, work, mask=None, lse=None, layer=0, scale=0.0,
-               softcap=0.0, window=0, slopes=None, stream=0):
+               softcap=0.0, window=0, slopes=None, stream=None):
         """Attention of the step's new tokens over their requests' pages.
 
         q [T][q_heads][head_dim] (any stride between tokens), out like it and
@@ -200,11 +209,11 @@ class PagedCache:
         rc = self._attend(self._at, _TREE.pack(
             tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
             first.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if slopes is None else slopes.data_ptr(),
-            out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size), stream or None)
+            out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size), self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_tree_attention")
 
-    def keep(self, first, path, keep, lens_out=None, free_count_out=None, stream=0):
+    def keep(self, first, path, keep, lens_out=None, free_count_out=None, stream=None):
         """Keeps the accepted drafts of every layer and frees the pages past the
         new lengths.  keep [requests] int32: kept tokens, or -1: the request
         ends; path [tokens] int32 or None: the first keep[r] ones."""
@@ -220,7 +229,7 @@ class PagedCache:
             paths = path.numel()
             self._check("path", path, torch.int32, paths)
         rc = self._keep(self._at, first.data_ptr(), None if path is None else path.data_ptr(), paths,
-                        keep.data_ptr(), lens.data_ptr(), count.data_ptr(), stream or None)
+                        keep.data_ptr(), lens.data_ptr(), count.data_ptr(), self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_tree_keep")
 

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from test_gpu_paged import BF16, F16, dev, host
-from test_gpu_tree_attention import Step
+from test_gpu_tree_attention import Decoder, Step
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,47 @@ def test_a_row_is_capped_by_what_it_sees(groups, dim, page):
         results.append((s.out.clone(), s.lse.clone()))
         s.check(cap=1e5)
     assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+def step_without_streams(d):
+    """A step's calls as the README prints them."""
+    c = d.cache
+    c.plan(d.new, d.first, d.slots, d.pos, mask=d.mask)
+    for layer in range(2):
+        a, b = d.H * d.G * d.D, d.H * d.D
+        q, k, v = d.qkv[layer].split((a, b, b), 1)
+        c.rotary(q, k, v, d.pos, d.slots, d.freq, d.q[layer], layer=layer)
+        c.attend(d.q[layer], d.first, d.out[layer], 8, d.work, mask=d.mask, layer=layer)
+    c.keep(d.first, d.path, d.kept)
+
+
+@pytest.mark.parametrize("how", ["side stream", "graph"])
+def test_calls_without_a_stream_follow_the_current_one(how):
+    runs = []
+    for where in ("default", how):
+        d = Decoder(BF16)
+        d.cache.free_count.fill_(40)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if where == "graph":
+            d.inputs(0)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step_without_streams(d)
+        for t in range(3):
+            if where == "side stream":
+                d.inputs(50 + t)
+                late = d.qkv.clone()
+                d.qkv.zero_()
+                torch.cuda.synchronize()
+                with torch.cuda.stream(side):
+                    torch.cuda._sleep(20_000_000)
+                    d.qkv.copy_(late)
+                    step_without_streams(d)
+                side.synchronize()
+            else:
+                d.inputs(50 + t)
+                g.replay() if where == "graph" else step_without_streams(d)
+        assert d.cache.error()[0] == 0
+        runs.append([x.clone() for x in (d.out, d.cache.lens, d.cache.tables, d.cache.free_count, d.cache.k)])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
