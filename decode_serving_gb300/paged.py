@@ -4,7 +4,7 @@ avsg_page_plan, avsg_rotary_write, avsg_tree_attention and avsg_tree_keep
 
 All tensors are the caller's, contiguous and on one CUDA device; shapes, types
 and devices are checked here (``ValueError``), the rest by the library
-(``AvsgError``).  Nothing synchronises except ``error`` and ``clear_error``.
+(``AvsgError``).  Nothing synchronises except ``error``, ``clear_error`` and the making of a cache.
 """
 from __future__ import annotations
 
@@ -77,6 +77,7 @@ class PagedCache:
         self._check("free", free, torch.int32, pages)
         self._check("free_count", free_count, torch.int32, 1)
         self._error = torch.zeros(4, dtype=torch.int32, device=k.device)
+        torch.cuda.current_stream(k.device).synchronize()  # (any stream may read it from here on)
         self._pages = C.avsg_pages(len(lens), layers, pages, heads, page, dim, tables.shape[1],
                                    _TYPES[k.dtype], k.data_ptr(), v.data_ptr(), tables.data_ptr(),
                                    lens.data_ptr(), free.data_ptr(), free_count.data_ptr(),

@@ -437,3 +437,21 @@ def test_error_waits_for_every_stream():
         torch.cuda._sleep(200_000_000)                            # about 0.1 s
     cache.rotary(x, x, x, pos, slots, freq, out, stream=side.cuda_stream)
     assert cache.error() == (-4, -1, 1)
+
+
+def test_a_new_cache_serves_any_stream():
+    """Its error word is zero for calls on every stream, not only behind the stream it was made on."""
+    from decode_serving_gb300.paged import PagedCache
+    old = PagedCache.allocate(1, 2, 2, 1, 16, 64)
+    i32 = lambda n: torch.full((n,), -7, dtype=torch.int32, device="cuda")  # noqa: E731
+    new, first, slots, pos = dev(np.array([3])), i32(2), i32(3), i32(3)
+    old.plan(new, first, slots, pos)                   # (loads the kernel)
+    side = torch.cuda.Stream()
+    keep = [torch.full((4,), 7, dtype=torch.int32, device="cuda") for _ in range(64)]
+    slots.fill_(-7)
+    torch.cuda.synchronize()
+    del keep                                           # (memory of such words is given out again)
+    torch.cuda._sleep(200_000_000)
+    cache = PagedCache(old.k, old.v, old.tables, old.lens, old.free, old.free_count)
+    cache.plan(new, first, slots, pos, stream=side.cuda_stream)
+    assert cache.error()[0] == 0 and host(slots).tolist() == [16, 17, 18]
