@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
       }
       slot[x] = (page << a.shift) + (p & page_mask);
       pos[x] = p;
-      if (a.mask) {
+      if (a.mask && s_first[r + 1] - s_first[r] <= kMaxDrafts) {  // (longer requests are chains)
         const unsigned long long m = a.mask[t];
         if (m) pos[x] = len + __popcll(m) - 1;
       }

@@ -390,7 +390,8 @@ typedef struct avsg_pages {
  *   d_new   : int32 [R], new tokens per request (0 is allowed).
  *   d_mask  : uint64 [num_mask] or NULL: ancestors of each draft (see
  *             avsg_tree_attention); position = len + depth, with depth the
- *             number of bits - 1.  NULL or a zero word: len + index.
+ *             number of bits - 1.  NULL, a zero word, or a request with more
+ *             than 64 new tokens, whose words are not looked at: len + index.
  *   capacity: entries of d_slot and d_pos.
  *   d_first : int32 [R + 1], receives the exclusive sum of d_new.
  *   d_slot  : int32 [capacity], receives each token's slot, -1 behind the last.
@@ -458,7 +459,8 @@ int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream);
  * New token i of a request sees every committed token and, of its new ones,
  * those in its mask word (bit j: new token j of the same request; an ancestor
  * mask holds the token's own bit).  d_mask NULL, or a request with more than
- * 64 new tokens: the new tokens up to itself (a chain, or a prompt chunk).
+ * 64 new tokens, whose words are not looked at: the new tokens up to itself (a
+ * chain, or a prompt chunk).
  * Positions: a committed token's index; a new token's len + number of mask
  * bits - 1, len + i for a chain or a zero word.  window > 0: only keys with
  * position of q - position of k < window.  The new tokens' own K and V must

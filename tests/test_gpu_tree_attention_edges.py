@@ -124,3 +124,16 @@ def test_calls_without_a_stream_follow_the_current_one(how):
         assert d.cache.error()[0] == 0
         runs.append([x.clone() for x in (d.out, d.cache.lens, d.cache.tables, d.cache.free_count, d.cache.k)])
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("groups,dim,page", [(1, 64, 4), (4, 128, 16), (2, 256, 16)])
+def test_long_requests_are_chains_whatever_their_words_hold(groups, dim, page):
+    """More than 64 new tokens: the plan's positions and the attention's are those of a chain."""
+    s = Step([10, 33], [70, 9], page, 2, groups, dim, BF16, True)
+    s.mask[:70] = 5                                    # (Step made zeros; two bits for every token)
+    s.dmask = dev(s.mask, torch.int64)
+    s.cache.free_count.fill_(s.count)                  # the same pages again
+    s.plan(s.new, s.total, s.mask)
+    assert host(s.pos)[:70].tolist() == list(range(10, 80))
+    s.attend(window=25)
+    s.check(window=25)
