@@ -328,7 +328,8 @@ struct Walk {
       p.ntok = min(a.tpm, q.n - p.tok0);
       p.limit = q.len + (q.chain ? p.tok0 + p.ntok : q.n);
       p.all_see = q.len + (q.chain ? p.tok0 + 1 : 0);
-      p.far_pos = q.len + (q.chain ? p.tok0 + p.ntok : q.n) - 1;
+      // (a position is the number of a word's bits, those past the request's tokens too)
+      p.far_pos = q.len + (q.chain ? p.tok0 + p.ntok : kMaxDrafts) - 1;
       // tiles that lie before the window of every row have no work
       int skip = a.begin;
       if (a.window > 0 && q.chain)

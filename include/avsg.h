@@ -462,7 +462,8 @@ int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream);
  * 64 new tokens, whose words are not looked at: the new tokens up to itself (a
  * chain, or a prompt chunk).
  * Positions: a committed token's index; a new token's len + number of mask
- * bits - 1, len + i for a chain or a zero word.  window > 0: only keys with
+ * bits - 1 (bits past the request's tokens stand for no key, but count), len + i
+ * for a chain or a zero word.  window > 0: only keys with
  * position of q - position of k < window.  The new tokens' own K and V must
  * be in the pages (avsg_rotary_write).  A row without a visible key gives
  * zeros and -infinity.  What a row does not see does not reach it, whatever

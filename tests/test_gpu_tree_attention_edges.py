@@ -137,3 +137,21 @@ def test_long_requests_are_chains_whatever_their_words_hold(groups, dim, page):
     assert host(s.pos)[:70].tolist() == list(range(10, 80))
     s.attend(window=25)
     s.check(window=25)
+
+
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+def test_bits_past_the_new_tokens_count_for_the_position(groups, dim, page):
+    """A mask word's bits past the request's tokens stand for no key, but a position is the number
+    of bits: the window lies before that position."""
+    s = Step([532, 70, 0], [3, 12, 5], page, 2, groups, dim, BF16, True)
+    words = s.mask.view(np.uint64).copy()
+    words[:3] |= np.uint64(2**64 - 8)
+    words[3:15] |= np.uint64(2**64 - 2**40)
+    s.mask = words.view(np.int64)
+    s.dmask = dev(s.mask, torch.int64)
+    slopes = np.full(2 * groups, 0.02, np.float32)
+    for window in (200, 66, 30):
+        s.attend(window=window)
+        s.check(window=window)
+    s.attend(window=200, slopes=dev(slopes, torch.float32))
+    s.check(window=200, slopes=slopes)
