@@ -1,5 +1,7 @@
 // avsg_tree_attention: host checks, the workspace's layout and the choice of
 // the rows per m-tile.
+#include <float.h>
+
 #include "avsg_tree_attn.cuh"
 
 namespace avsg {
@@ -85,9 +87,17 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   int rc = check_attention(p, t->q_per_kv, t->max_new);
   if (rc != AVSG_OK) return rc;
   if (t->num_tokens < 0 || t->layer < 0 || t->layer >= p->num_layers || t->window < 0 ||
-      !(t->softmax_scale >= 0.f) || isinf(t->softmax_scale) || !(t->softcap >= 0.f) ||
-      isinf(t->softcap * 1.4426950408889634f) || t->reserved0 != 0)
+      !(t->softmax_scale >= 0.f) || !(t->softcap >= 0.f) || t->reserved0 != 0)
     return AVSG_ERR_INVALID_ARG;
+  // The factors that scores and capped scores are multiplied by: an infinite one would make a score
+  // of 0 a NaN.
+  const float scale = t->softmax_scale > 0.f ? t->softmax_scale : 1.0f / sqrtf((float)p->head_dim);
+  const float log2e = 1.4426950408889634f;
+  const float score_log2 = scale * log2e, cap_out = t->softcap * log2e;
+  float cap_in = t->softcap > 0.f ? 2.f * log2e * scale / t->softcap : 0.f;
+  if (isinf(score_log2) || isinf(cap_out) || isinf(cap_in)) return AVSG_ERR_INVALID_ARG;
+  // A factor below the normal range has few bits left; only products q.k beyond 2^126 come near such a cap.
+  if (cap_in < FLT_MIN) cap_in = 0.f;
   if (t->num_tokens == 0) return AVSG_OK;
   const int64_t row = (int64_t)p->num_kv_heads * t->q_per_kv * p->head_dim;
   if (!t->d_q || !t->d_first || !t->d_out || !t->d_work || t->q_stride < row || t->q_stride % 2 ||
@@ -103,8 +113,6 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   if (t->work_bytes < w.bytes) return AVSG_ERR_CAPACITY;
   const size_t layer = (size_t)p->num_pages * p->num_kv_heads * p->page_tokens * D * 2;
   unsigned char* work = static_cast<unsigned char*>(t->d_work);
-  const float scale = t->softmax_scale > 0.f ? t->softmax_scale : 1.0f / sqrtf((float)D);
-  const float log2e = 1.4426950408889634f;
   TreeArgs a{};
   a.k = static_cast<const unsigned char*>(p->d_k) + t->layer * layer;
   a.v = static_cast<const unsigned char*>(p->d_v) + t->layer * layer;
@@ -134,10 +142,10 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   a.ctas = x.ctas;
   a.min_tiles = 2;
   a.begin = x.begin;
-  a.score_log2 = scale * log2e;
-  if (t->softcap > 0.f) {
-    a.cap_in = 2.f * log2e * scale / t->softcap;
-    a.cap_out = t->softcap * log2e;
+  a.score_log2 = score_log2;
+  if (cap_in != 0.f) {
+    a.cap_in = cap_in;
+    a.cap_out = cap_out;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = x.umma     ? launch_tree_umma(a, p->dtype, D, dev, st)

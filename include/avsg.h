@@ -477,8 +477,8 @@ typedef struct avsg_tree {
   int32_t max_new;      /* no request has more new tokens (else CAPACITY is latched) */
   int32_t layer;
   int32_t window;       /* 0: none */
-  float softmax_scale;  /* 0 selects 1/sqrt(D) */
-  float softcap;        /* 0: none; below 2^127 */
+  float softmax_scale;  /* 0 selects 1/sqrt(D); below 2^126 */
+  float softcap;        /* 0: none; below 2^127; softmax_scale / softcap below 2^126 */
   int32_t reserved0;    /* must be 0 */
   int64_t q_stride;     /* values between tokens of d_q, even */
   const void* d_q;      /* rows of [H][G][D], the cache's type, 4-byte aligned */

@@ -155,3 +155,12 @@ def test_bits_past_the_new_tokens_count_for_the_position(groups, dim, page):
         s.check(window=window)
     s.attend(window=200, slopes=dev(slopes, torch.float32))
     s.check(window=200, slopes=slopes)
+
+
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+def test_a_cap_far_below_the_scores(groups, dim, page):
+    """Every score is the cap's value or its negative, next to nothing: all visible keys weigh the same."""
+    s = Step([300, 40], [12, 5], page, 2, groups, dim, F16, True)
+    for cap in (1e-30, 1e-37):
+        s.attend(softcap=cap)
+        s.check(cap=cap)

@@ -99,6 +99,18 @@ def test_bad_attention(lib, kw, code):
     assert lib.avsg_tree_attention(p, avsg.avsg_tree(**f), None) == code
 
 
+@pytest.mark.parametrize("scale,cap,code", [
+    (3e38, 0.0, -1), (0.0, 1e-40, -1), (1.0, 1e-39, -1), (1e30, 1e-9, -1), (1e38, 1e30, 0), (1e-38, 1e38, 0),
+    (0.0, 1e-37, 0), (2e38, 0.0, 0),
+])
+def test_factors_of_scores_are_finite(lib, scale, cap, code):
+    """What scores are multiplied by: the scale, and twice the scale by the cap, times log2(e)."""
+    from decode_serving_gb300 import avsg
+    p, at = pages()
+    t = avsg.avsg_tree(num_tokens=0, q_per_kv=2, max_new=4, layer=1, softmax_scale=scale, softcap=cap)
+    assert lib.avsg_tree_attention(p, t, None) == code
+
+
 def test_attention_shapes(lib):
     from decode_serving_gb300 import avsg
     n = ctypes.c_size_t()
