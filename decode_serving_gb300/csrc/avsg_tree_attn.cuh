@@ -559,9 +559,8 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         }
         bad_v = __syncthreads_or(mine);              // (also: K has been read by every warp)
       }
-      // Whether key (x, y) is seen by its row; how far away it is.
-      auto sees = [&](int x, int y, int& far) {
-        const int j = j0 + wk * NK + x * 8 + 2 * c + (y & 1), row = y >> 1;
+      // Whether this thread's row sees key j; how far away it is.
+      auto sees_key = [&](int j, int row, int& far) {
         const int jd = j - pc.len;
         bool see = true;
         int k_pos = j;
@@ -575,6 +574,9 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         }
         far = q_pos[row] - k_pos;
         return see && !(a.window > 0 && far >= a.window);
+      };
+      auto sees = [&](int x, int y, int& far) {      // the key of score (x, y)
+        return sees_key(j0 + wk * NK + x * 8 + 2 * c + (y & 1), y >> 1, far);
       };
       if (a.cap_in != 0.f) {
         // (in units of log 2)
@@ -696,8 +698,8 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         }
       } else {
         // Some value of V is not finite, and 0 times it would be NaN in rows
-        // that do not see it: this tile's products one by one, leaving out the
-        // weights that are 0.  P lies over the K tile, which is done with.
+        // that do not see it: this tile's products one by one, for the keys
+        // that the row sees.  P lies over the K tile, which is done with.
         uint32_t* pp = reinterpret_cast<uint32_t*>(kst);  // [MT][KT / 2]
 #pragma unroll
         for (int x = 0; x < NK / 8; ++x)
@@ -708,8 +710,11 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         __syncwarp();                                 // a warp reads what it wrote itself
         for (int j = wk * NK; j < (wk + 1) * NK; ++j) {
           float p[2];
+          bool see[2];
 #pragma unroll
           for (int row = 0; row < 2; ++row) {
+            int far;
+            see[row] = sees_key(j0 + j, row, far);
             const float2 w = unpack<T>(pp[(wm * 16 + g + 8 * row) * (KT / 2) + j / 2]);
             p[row] = j & 1 ? w.y : w.x;
           }
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
                 kst + SH::TILE + j * (D * 2) + ((x ^ (j & 7)) << 4) + c * 4));
 #pragma unroll
             for (int row = 0; row < 2; ++row)
-              if (p[row] != 0.f) {
+              if (see[row]) {
                 acc[x][2 * row] += p[row] * w.x;
                 acc[x][2 * row + 1] += p[row] * w.y;
               }

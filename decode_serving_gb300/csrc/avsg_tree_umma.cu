@@ -339,8 +339,8 @@ __device__ __noinline__ void add_bad_values(const TreeArgs& a, const Piece& s, c
       }
       if (a.cap_in != 0.f) x = capped(a, x);
       else x *= a.score_log2;
+      // (a weight that rounds to 0 gives NaN, as it does in the products of tiles seen whole)
       const float p = unpack<T>(pack<T>(ex2(x - slope * (float)(q_pos - k_pos) - ref), 0.f)).x;
-      if (p == 0.f) continue;
       for (int d = 0; d < D; ++d) {
         const uint32_t pair = v[d / 2];
         if (!not_finite<T>(d & 1 ? pair & 0xffff0000u : pair & 0xffffu)) continue;
@@ -843,11 +843,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           if (join) tm_ld32(from + 128 + c * 32, w1);
           tm_wait_ld(w0);
           tm_wait_ld(w1);
-          // (a factor of 0 stands for a stream that saw nothing, whatever its output holds)
+          // (the output of a stream that saw nothing is 0; one that is not finite stays so)
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
-            float o = g0 == 0.f ? 0.f : __uint_as_float(w0[y]) * g0;
-            if (join) o += g1 == 0.f ? 0.f : __uint_as_float(w1[y]) * g1;
+            float o = __uint_as_float(w0[y]) * g0;
+            if (join) o += __uint_as_float(w1[y]) * g1;
             w0[y] = __float_as_uint(o);
           }
           auto o = [&](int y) { return __uint_as_float(w0[y]); };

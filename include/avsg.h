@@ -468,7 +468,8 @@ int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream);
  * be in the pages (avsg_rotary_write).  A row without a visible key gives
  * zeros and -infinity.  What a row does not see does not reach it, whatever
  * it holds; neither does what lies in the pages behind the last new token.
- * A weight that rounds to 0 in the cache's type counts as 0.
+ * A value of V that is not finite makes the results that see it not finite: an
+ * infinity, or NaN where its weight rounds to 0 in the cache's type.
  */
 typedef struct avsg_tree {
   int32_t num_tokens;   /* rows of d_q, d_out and d_lse (at least d_first[R]; the

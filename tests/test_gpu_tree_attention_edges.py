@@ -164,3 +164,31 @@ def test_a_cap_far_below_the_scores(groups, dim, page):
     for cap in (1e-30, 1e-37):
         s.attend(softcap=cap)
         s.check(cap=cap)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+@pytest.mark.parametrize("length", [128, 150, 700, 1500])
+def test_values_that_are_not_finite_reach_every_row_that_sees_them(groups, dim, page, dtype, length):
+    """One key takes all of the weight, that of the others rounds to 0: wherever a tile's border lies, a
+    row that sees an infinity or a NaN of V has a result that is not finite, and no other row has."""
+    s = Step([length], [12], page, 1, groups, dim, dtype, True)
+    s.htables = host(s.cache.tables)
+    q = s.q[:, 0].float()
+    s.q[:] = (q.mean(0) + 0.1 * q)[:, None].to(dtype)  # rows that agree on the largest key
+    s.k *= 0.1
+    a, b = s.row(0, length - 40)
+    s.k[0, a, :, b] = (q.mean(0) * 30).to(dtype)
+    for place, value in ((5, math.inf), (length - 33, math.nan), (length + 2, -math.inf), (length + 7, math.inf)):
+        a, b = s.row(0, place)
+        old = s.v[0, a, :, b, 3].clone()
+        s.v[0, a, :, b, 3] = value
+        s.attend(scale=40.0)
+        sees = place < length or torch.from_numpy((s.mask >> (place - length)) & 1).bool().cuda()
+        finite = torch.isfinite(s.out.float())
+        assert torch.equal(~finite[..., 3], (torch.zeros_like(s.lse) > 1) | (
+            sees if place < length else sees[:, None])), f"place {place}"
+        assert finite[..., :3].all() and finite[..., 4:].all()
+        s.v[0, a, :, b, 3] = old
+    s.attend(scale=40.0)
+    s.check(scale=40.0)
