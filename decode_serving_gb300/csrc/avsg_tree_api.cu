@@ -17,31 +17,36 @@ struct Plan {
   int ctas;
   int begin;   // see TreeArgs
 };
+Plan plan_kernel(bool umma, int D, int64_t rows, int sms) {
+  Plan x;
+  x.umma = umma;
+  // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
+  x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  x.MT = !umma ? 16 * x.wm : D == 256 ? 128 : 256;
+  // Eight units of one tile take 6 us each on tcgen05, where 64 KB of K and V take 1.5 us; longer
+  // with more of q and out.  About 2 us with mma.sync, where a tile does.  Eight requests of 1 to
+  // 20000 tokens, 64 drafts each, heads of 128: 57 us, with 4 61, with 2 79, with 16 59; heads of
+  // 256 and 1 to 32768: 113 us with 8, 129 with 6; 32 x 8 units of 300, one token: 29 us with 6, 33
+  // with 4.
+  x.begin = !umma ? 1 : (rows > 32 ? 6 : 4) + (D == 256 ? 2 : 0);
+  x.ctas = umma || D == 256 ? sms : 2 * sms;
+  return x;
+}
 Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   const int64_t rows = (int64_t)G * max_new;
-  Plan x;
   // tcgen05 (avsg_tree_umma.cu): boxes of whole 8-row groups.  It always works on 128 rows; with
   // few rows it pays where contexts are long (8 x 8 units, one token, 16000 tokens: 91 us against
   // 99; 32 x 8 units, 32 rows, 3000 tokens: 80 against 89) and costs 4 to 10 us a call where they
   // are short (8 x 8 units, one token, 300 tokens: 17.4 against 11.6; 32 x 8 units, 32 rows, 50
   // tokens: 22 against 12).  Equal at about 4000 tokens up to 16 rows, 2000 up to 32; with 64 rows
   // it is never far behind.  Heads of 256: equal at 1000 (32 x 8 units, one token, 2000 tokens: 94
-  // against 122; 50 tokens: 21 against 17).  Lengths are not known here; the pool's tokens per
-  // request are.
+  // against 122; 50 tokens: 21 against 17).  Lengths are not known here; the pool's room per place
+  // of a request stands for them, so that a large pool with few or short requests in it takes
+  // tcgen05 at the cost just given.
   const int64_t room = (int64_t)p->num_pages * p->page_tokens / p->num_requests;
   const int64_t enough = p->head_dim == 256 ? 1024 : rows > 16 ? 4096 : 8192;
-  x.umma = p->page_tokens >= 8 && (rows > 32 || room >= enough);
-  // 16 rows a warp, the fewest that hold all rows (up to 64); the other warps split the keys
-  x.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  x.MT = !x.umma ? 16 * x.wm : p->head_dim == 256 ? 128 : 256;
-  // Eight units of one tile take 6 us each on tcgen05, where 64 KB of K and V take 1.5 us; longer
-  // with more of q and out.  About 2 us with mma.sync, where a tile does.  Eight requests of 1 to
-  // 20000 tokens, 64 drafts each, heads of 128: 57 us, with 4 61, with 2 79, with 16 59; heads of
-  // 256 and 1 to 32768: 113 us with 8, 129 with 6; 32 x 8 units of 300, one token: 29 us with 6, 33
-  // with 4.
-  x.begin = !x.umma ? 1 : (rows > 32 ? 6 : 4) + (p->head_dim == 256 ? 2 : 0);
-  x.ctas = x.umma || p->head_dim == 256 ? sms : 2 * sms;
-  return x;
+  const bool umma = p->page_tokens >= 8 && (rows > 32 || room >= enough);
+  return plan_kernel(umma, p->head_dim, rows, sms);
 }
 
 struct Workspace {
@@ -54,6 +59,14 @@ Workspace layout(const Plan& x, int D) {
   w.part = w.ml + up((size_t)2 * x.ctas * x.MT * 2 * sizeof(float));
   w.bytes = w.part + up((size_t)2 * x.ctas * x.MT * D * sizeof(float));
   return w;
+}
+
+// Enough for either kernel: a workspace then serves every pool of these heads.
+size_t workspace_bytes(int D, int G, int max_new, int sms) {
+  const int64_t rows = (int64_t)G * max_new;
+  const size_t a = layout(plan_kernel(false, D, rows, sms), D).bytes;
+  const size_t b = layout(plan_kernel(true, D, rows, sms), D).bytes;
+  return a > b ? a : b;
 }
 
 int check_attention(const avsg_pages* p, int q_per_kv, int max_new) {
@@ -78,7 +91,7 @@ extern "C" int avsg_tree_attention_workspace(const avsg_pages* p, int32_t q_per_
   int dev = 0, sms = 0;
   const int rd = paged_device(p->d_k, &dev, &sms);
   if (rd != AVSG_OK) return rd;
-  *bytes = layout(plan_attention(p, q_per_kv, max_new, sms), p->head_dim).bytes;
+  *bytes = workspace_bytes(p->head_dim, q_per_kv, max_new, sms);
   return AVSG_OK;
 }
 
@@ -110,7 +123,7 @@ extern "C" int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void
   const int D = p->head_dim;
   const Plan x = plan_attention(p, t->q_per_kv, t->max_new, sms);
   const Workspace w = layout(x, D);
-  if (t->work_bytes < w.bytes) return AVSG_ERR_CAPACITY;
+  if (t->work_bytes < workspace_bytes(D, t->q_per_kv, t->max_new, sms)) return AVSG_ERR_CAPACITY;
   const size_t layer = (size_t)p->num_pages * p->num_kv_heads * p->page_tokens * D * 2;
   unsigned char* work = static_cast<unsigned char*>(t->d_work);
   TreeArgs a{};

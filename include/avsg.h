@@ -494,7 +494,7 @@ typedef struct avsg_tree {
 
 /*
  * Bytes of d_work for the device of p->d_k.  The size depends on D, q_per_kv
- * and max_new, not on lengths.  Calls that may run at the same time (two
+ * and max_new, not on lengths or the pool.  Calls that may run at the same time (two
  * streams, two graphs) need a workspace each.
  */
 int avsg_tree_attention_workspace(const avsg_pages* p, int32_t q_per_kv, int32_t max_new,

@@ -192,3 +192,19 @@ def test_values_that_are_not_finite_reach_every_row_that_sees_them(groups, dim, 
         s.v[0, a, :, b, 3] = old
     s.attend(scale=40.0)
     s.check(scale=40.0)
+
+
+@pytest.mark.parametrize("groups,most,dim", [(4, 1, 128), (4, 8, 64), (2, 5, 256), (16, 9, 128)])
+def test_a_workspace_fits_every_pool(groups, most, dim):
+    """Its size depends on the heads and max_new alone: a small pool's serves a large one."""
+    from decode_serving_gb300.paged import PagedCache
+    caches = [PagedCache.allocate(2, 4, pages, 1, page, dim) for pages, page in ((8, 16), (2048, 16), (64, 4))]
+    sizes = [c.attention_workspace(groups, most).numel() for c in caches]
+    assert sizes[0] == sizes[1] == sizes[2]
+    work = caches[0].attention_workspace(groups, most)
+    q = torch.randn(2, groups, dim, device="cuda").to(BF16)
+    for c in caches:
+        out, first = torch.full_like(q, 3.0), dev(np.array([0, 1, 2]))
+        c.plan(dev(np.array([1, 1])), first, dev(np.zeros(2)), dev(np.zeros(2)))
+        c.attend(q, first, out, most, work)
+        assert c.error()[0] == 0 and (out == 0).all()  # (V is zero)
