@@ -57,8 +57,12 @@
 // end, a third of it hidden by the loads that run ahead (256 x 8 units of 1000 tokens, 64
 // rows: 233 us, 256 rows: 384 us).
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
-// the waits after it return at once.
+// the waits after it return at once.  A warp whose wait failed issues no copy
+// and no product after it, and passes no buffer on; the others go on with what
+// their barriers still give them.  Copies and products that were issued are
+// awaited all the same before the CTA ends or frees its tensor memory.
 #include <cuda.h>
+#include <stdlib.h>
 
 #include "avsg_tree_attn.cuh"
 
@@ -70,12 +74,15 @@ constexpr int UM = 128;                    // rows per stream
 constexpr int kUmmaThreads = 384;
 constexpr int UH = 64;                     // keys per half tile
 constexpr float kLazy = 8.f;               // growth of the maximum (log2) that O is scaled for
-constexpr long long kWaitClocks = 4000000000LL;
+constexpr long long kWaitClocks = 4000000000LL;  // about two seconds
 
 struct UmmaArgs {
   TreeArgs t;
   int box_rows;                            // tokens per TMA box: min(page, 128)
   int q_vec;                               // rows of q are 16-byte aligned
+#ifdef AVSG_DEBUG_BOUNDS
+  long long wait_clocks;                   // what a wait may take
+#endif
 };
 
 template <int D>
@@ -126,18 +133,37 @@ __device__ __forceinline__ void warp_arrive(uint32_t b, int lane) {
   __syncwarp();
   if (lane == 0) bar_arrive(b);
 }
-// Waits for the phase of the given parity, a few seconds at most.
-__device__ __forceinline__ void bar_wait(uint32_t b, uint32_t parity, volatile int* gave_up, DevErr* err) {
-  if (bar_try(b, parity)) return;
+// Waits for the phase of the given parity.  False: it did not come in time, or another wait has given
+// up and this one would have had to wait.  In the bounds-checked build a call may set the limit, and
+// a try does not wait in the hardware, so that a test can let waits run out.
+struct Waits {
+  long long clocks;
+  volatile int* gave_up;
+  DevErr* err;
+};
+__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, const Waits& w) {
+#ifdef AVSG_DEBUG_BOUNDS
+  auto come = [&] { return bar_test(b, parity); };
+#else
+  auto come = [&] { return bar_try(b, parity); };
+#endif
+  if (come()) return true;
   const long long t0 = clock64();
-  while (!bar_try(b, parity)) {
-    if (*gave_up) return;
-    if (clock64() - t0 > kWaitClocks) {
-      *gave_up = 1;
-      raise_error(err, AVSG_ERR_TIMEOUT, -1, -1);
-      return;
+  while (!come()) {
+    if (*w.gave_up) return false;
+    if (clock64() - t0 > w.clocks) {
+      *w.gave_up = 1;
+      raise_error(w.err, AVSG_ERR_TIMEOUT, -1, -1);
+      return false;
     }
   }
+  return true;
+}
+// Waits for copies or products that were issued: their end comes whatever became of other waits.
+__device__ __forceinline__ void bar_drain(uint32_t b, uint32_t parity) {
+  if (bar_try(b, parity)) return;
+  const long long t0 = clock64();
+  while (!bar_try(b, parity) && clock64() - t0 <= kWaitClocks) {}
 }
 // One lane of a converged warp, always the same one.  (Code under it keeps the operands of
 // the tensor and copy instructions in uniform registers; under `lane == 0` each of them cost
@@ -389,6 +415,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   auto o_last = [&](int x) { return bars + 8 * (2 * kRing + 10 + x); };
   auto q_full = [&](int x) { return bars + 8 * (2 * kRing + 12 + x); };  // 129 to 256 rows
   const uint32_t q_one = bars + 8 * (2 * kRing + 14);                     // up to 128
+  const uint32_t drained = bars + 8 * (2 * kRing + 15);  // every product has ended
 
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
@@ -410,6 +437,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       bar_init(q_full(x), UM / 32);
     }
     bar_init(q_one, UM / 32);
+    bar_init(drained, 2);
     s_give_up = s_bad[0] = s_bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -425,7 +453,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     return;
   }
   griddep_launch();
-  volatile int* give_up = &s_give_up;
+#ifdef AVSG_DEBUG_BOUNDS
+  const Waits waits{ua.wait_clocks, &s_give_up, a.err};
+#else
+  const Waits waits{kWaitClocks, &s_give_up, a.err};
+#endif
   if (tid == 0) {
     if (smem & 1023) raise_error(a.err, AVSG_ERR_INTERNAL, -1, -1);  // (atoms are 1024-byte aligned)
     s_walk = walk;
@@ -448,7 +480,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int n = idx + v_place(two, t, s.count), b = n % kRing;
       const int j = s.j0 + (s.count - 1 - t) * UT, rows = min(UT, s.limit - j);
       const int from = a.window > 0 ? 0 : max(0, s.all_see - j);
-      bar_wait(full(b), (n / kRing) & 1, give_up, a.err);
+      bar_wait(full(b), (n / kRing) & 1, waits);
       unsigned char* v = smem_raw + M::RING + b * M::TILE;
       bool bad = false;
       for (int y = from * (D / 8) + row; y < UT * (D / 8); y += UM) {
@@ -572,7 +604,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int e1 = min(s.count, max(0, s.all_see - s.j0) / UT);
       const int e0 = a.window > 0 ? max(0, (s.far_pos - a.window - s.j0 + UT) / UT) : 0;
       auto wait_scores = [&](int n) {
-        bar_wait(s_full(x, n & 1), (n >> 1) & 1, give_up, a.err);
+        bar_wait(s_full(x, n & 1), (n >> 1) & 1, waits);
         __syncwarp();                      // (tensor-memory accesses are the whole warp's)
         tc_fence_after();
       };
@@ -763,7 +795,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (i > 0) {
               // the product before this one has to be done (the one before it is: these scores
               // came after it)
-              bar_wait(o_done(x), (hh - 1) & 1, give_up, a.err);
+              bar_wait(o_done(x), (hh - 1) & 1, waits);
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -808,7 +840,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       // Up to 128 rows the two streams' outputs are joined here (stream 1 has none in a piece of
       // one tile), half of the columns by either stream's warps.
       const bool join = !SOLO && !two && s.count > 1;
-      bar_wait(o_last(x), seg & 1, give_up, a.err);
+      bar_wait(o_last(x), seg & 1, waits);
       if (!two && (!SOLO || x == 0)) {
         s_m[UM * x + row] = m;
         s_l[UM * x + row] = l;
@@ -913,6 +945,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     };
     while (more && (buf & 1) != part) step();
     int page = -1, group = 0, is_v = 0, to = 0, use = 0;  // this warp's next load, this lane's box
+    int end = 0;                           // the loads before this one were issued
     auto look_up = [&]() {
       const bool two = !SOLO && s.ntok * a.G > UM;
       int t;
@@ -949,16 +982,16 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       have = more;
       if (more) look_up();
       const int n = __popc(__ballot_sync(0xffffffffu, now >= 0));
-      bar_wait(empty(b), (phase & 1) ^ 1, give_up, a.err);
+      if (!__all_sync(0xffffffffu, bar_wait(empty(b), (phase & 1) ^ 1, waits))) break;
+      end = phase * kRing + b + 1;
       if (lane == 0) bar_expect(full(b), n * ua.box_rows * D * 2);
       __syncwarp();
       if (now >= 0)
         tma_box(smem + M::RING + b * M::TILE + lane * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
                 now_group, now);
     }
-    // every copy of this warp has landed before the CTA may end (idx: loads in all)
-    for (int b = part; b < kRing && b < idx; b += 2)
-      bar_wait(full(b), ((idx - 1 - b) / kRing) & 1, give_up, a.err);
+    // every copy of this warp has landed before the CTA may end
+    for (int b = part; b < kRing && b < end; b += 2) bar_drain(full(b), ((end - 1 - b) / kRing) & 1);
   } else {
       // ---- products.  Up to 128 rows, both warps follow every load, in order: a tile that is the
       // other stream's is passed on, so that a buffer is filled again only when both have seen it
@@ -969,9 +1002,15 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       int ps = 0;                          // halves of this stream since the start
       const uint32_t id_s = instruction<T>(UH, false), id_o = instruction<T>(D, true);
       constexpr uint32_t HALF_TILE = UH / 8 * 1024 * COLS;
+      // A wait of this lane has given up: it issues nothing more, and passes no buffer on.  (Each
+      // lane by itself, without a vote; those that issue are always the same.)
+      bool stop = false;
+      auto wait = [&](uint32_t bar, int phase) {
+        if (!stop) stop = !bar_wait(bar, phase & 1, waits);
+      };
       auto wait_load = [&](int place) -> uint32_t {
         const int i = idx + place, b = i % kRing;
-        bar_wait(full(b), (i / kRing) & 1, give_up, a.err);
+        wait(full(b), i / kRing);
         return smem + M::RING + b * M::TILE;
       };
       // Scores of half hh (of the stream's halves since the start) from rows q and the keys at k.
@@ -980,7 +1019,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         const uint32_t qa = uniform(operand_low(smem + q * M::Q)), to = uniform(tmem + 128 * x + 64 * (hh & 1));
         const uint32_t to_q = uniform(tmem + 128);   // (heads of 256)
         const uint32_t ka = uniform(operand_low(k + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(s_full(x, hh & 1));
-        if (elect_one()) {
+        if (elect_one() && !stop) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * 1024 + (ks % 4) * 32) >> 4;
@@ -992,13 +1031,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       };
       // P V of half hh of stream x; v: its tile.
       auto output = [&](int x, uint32_t v, int hh, bool first) {
-        bar_wait(p_full(x, hh & 1), (hh >> 1) & 1, give_up, a.err);
+        wait(p_full(x, hh & 1), hh >> 1);
         tc_fence_after();
         __syncwarp();
         const uint32_t va = uniform(operand_low(v + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(o_done(x));
         const uint32_t from = uniform(tmem + 128 * x + 64 * (hh & 1)), to = uniform(tmem + 256 + 128 * x);
         const uint32_t add = uniform(first ? 0 : 1);
-        if (elect_one()) {
+        if (elect_one() && !stop) {
 #pragma unroll
           for (int ks = 0; ks < UH / 16; ++ks)
             mma_ts(to, from + ks * 8, operand<COLS>(va + ks * (2048 * COLS >> 4)), id_o, ks > 0 ? 1 : add);
@@ -1006,21 +1045,21 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         }
       };
       auto finish = [&](int x) {
-        if (elect_one()) mma_commit(o_last(x));
+        if (elect_one() && !stop) mma_commit(o_last(x));
       };
       auto pass_on = [&](int place) {
         __syncwarp();
-        if (lane == 0) bar_arrive(empty((idx + place) % kRing));
+        if (lane == 0 && !stop) bar_arrive(empty((idx + place) % kRing));
       };
       auto release = [&](int place) {
         const uint32_t bar = uniform(empty((idx + place) % kRing));
-        if (elect_one()) mma_commit(bar);
+        if (elect_one() && !stop) mma_commit(bar);
       };
       while (walk.next(a, s)) {
         const bool two = !SOLO && s.ntok * a.G > UM;
         const int x = me;
         if (SOLO) {
-          bar_wait(q_one, q1 & 1, give_up, a.err);  // (both warps: the end of the unit before)
+          wait(q_one, q1);  // (both warps: the end of the unit before)
           ++q1;
           tc_fence_after();
         }
@@ -1045,7 +1084,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           }
         } else if (two) {
           const int hh = ps;
-          bar_wait(q_full(x), qs & 1, give_up, a.err);
+          wait(q_full(x), qs);
           ++qs;
           tc_fence_after();
           uint32_t k = wait_load(0);
@@ -1068,7 +1107,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
           }
         } else {
-          bar_wait(q_one, q1 & 1, give_up, a.err);
+          wait(q_one, q1);
           ++q1;
           tc_fence_after();
           for (int t = 0; t < 2 && t < s.count; ++t) {
@@ -1110,6 +1149,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         idx += 2 * s.count;
         __syncwarp();
       }
+      // every product of both warps has ended before tensor memory is given back
+      if (elect_one()) mma_commit(drained);
+      __syncwarp();
+      bar_drain(drained, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -1149,6 +1192,15 @@ bool encode_pages(CUtensorMap* map, const unsigned char* pages, const TreeArgs& 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+#ifdef AVSG_DEBUG_BOUNDS
+// AVSG_TREE_WAIT_CLOCKS in the environment: a shorter limit for the waits.
+long long wait_clocks() {
+  const char* v = getenv("AVSG_TREE_WAIT_CLOCKS");
+  const long long x = v && *v ? atoll(v) : kWaitClocks;
+  return x < 0 || x > kWaitClocks ? kWaitClocks : x;
+}
+#endif
+
 template <typename T, int D, bool EXTRA>
 cudaError_t launch_umma_one(const TreeArgs& a, int dtype, int dev, cudaStream_t st) {
   static SmemLimit limit;
@@ -1158,6 +1210,9 @@ cudaError_t launch_umma_one(const TreeArgs& a, int dtype, int dev, cudaStream_t 
   UmmaArgs u{};
   u.t = a;
   u.box_rows = (1 << a.shift) < Mem<D>::UT ? 1 << a.shift : Mem<D>::UT;
+#ifdef AVSG_DEBUG_BOUNDS
+  u.wait_clocks = wait_clocks();
+#endif
   u.q_vec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_stride % 8 == 0;
   CUtensorMap k_map, v_map;
   if (!encode_pages(&k_map, a.k, a, dtype, D, u.box_rows) || !encode_pages(&v_map, a.v, a, dtype, D, u.box_rows))
