@@ -673,8 +673,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
             // The polynomial for a row whose scores of this half are all near 0, the quotient for the
             // others (see cap_polynomial_reach).  Where all rows are near, the special functions are
-            // left to the weights (16 x 8 units of 16384 tokens, 256 rows, D 128: 367 us; the
-            // quotient alone 431, both of them 532; without a cap 227).
+            // left to the weights (16 x 8 units of 16384 tokens, 256 rows, D 128: 369 us; the
+            // quotient alone 432, both in one warp 555; without a cap 230).
             const float k = a.cap_in * kCapUnit, co = a.cap_out;
             const uint64_t k2 = pair(k, k), one = pair(co, co), c1 = pair(kCap1 * co, kCap1 * co),
                            c2 = pair(kCap2 * co, kCap2 * co), c3 = pair(kCap3 * co, kCap3 * co);
@@ -691,8 +691,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               x0 = fmaf(r, e1, co);
               x1 = fmaf(r, e0, co);
             };
-            // (padding rows, whose scores are 0, have no say)
-            if (a.cap_in != 0.f && __all_sync(0xffffffffu, !mine || far * k <= kCapNear)) {
+            if (a.cap_in != 0.f && __all_sync(0xffffffffu, far * k <= kCapNear)) {
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -703,6 +702,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                   w[c][y + 1] = __float_as_uint(x1);
                 }
             } else if (a.cap_in != 0.f && __all_sync(0xffffffffu, !mine || cap_polynomial_reach(far * k, co) < 0.f)) {
+              // (padding rows, whose scores are 0, have no say)
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
