@@ -208,3 +208,65 @@ def test_a_workspace_fits_every_pool(groups, most, dim):
         c.plan(dev(np.array([1, 1])), first, dev(np.zeros(2)), dev(np.zeros(2)))
         c.attend(q, first, out, most, work)
         assert c.error()[0] == 0 and (out == 0).all()  # (V is zero)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("groups,dim,page", [k for k in KERNELS if k[1] > 64])
+def test_unseen_values_with_wider_heads(groups, dim, page, dtype, cap):
+    s = Step([40, 0, 175], [12, 7, 3], page, 2, groups, dim, dtype, True)
+    s.mask[12] = 0                                     # request 1 has no context: its first row is empty
+    s.mask[15] = -2**63                                # a bit past its new tokens
+    s.dmask = dev(s.mask, torch.int64)
+    s.htables = host(s.cache.tables)
+    at = lambda r, p: (0, s.row(r, p)[0], slice(None), s.row(r, p)[1])  # noqa: E731
+    for r, p in ((r, p) for r, (length, n) in enumerate(zip(s.lens.tolist(), s.new))
+                 for p in range(length + n, -(-(length + n) // page) * page)):
+        s.k[at(r, p)] = s.v[at(r, p)] = math.nan
+    s.v[at(0, 42) + (dim - 1,)] = math.inf             # draft 2 of request 0: seen by its branch only
+    s.v[at(0, 42) + (63,)] = -math.inf
+    s.k[at(0, 43)] = math.nan                          # draft 3
+    s.v[at(2, 3)] = math.nan                           # outside the window
+    s.k[at(2, 4)] = math.inf
+    s.attend(window=150, softcap=cap)
+    s.check(window=150, cap=cap)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF16), (256, BF16), (256, F16)])
+@pytest.mark.parametrize("kw", [dict(slopes=True), dict(slopes=True, cap=6.0, window=90, scale=0.2),
+                                dict(window=33), dict(cap=30.0)])
+@pytest.mark.parametrize("tree", [True, False])
+def test_two_streams_with_caps_windows_and_slopes(dim, dtype, kw, tree):
+    """Units of more than 128 rows (two m-tiles for heads of 256)."""
+    heads, groups = 2, 12
+    s = Step([0, 500, 66, 129], [12, 19, 40, 1], 16, heads, groups, dim, dtype, tree)
+    kw = dict(kw)
+    slopes = (2.0 ** (-np.arange(1, heads * groups + 1) / 3.0)).astype(np.float32) if kw.pop("slopes", False) else None
+    s.attend(scale=kw.get("scale", 0.0), softcap=kw.get("cap", 0.0), window=kw.get("window", 0),
+             slopes=None if slopes is None else dev(slopes, torch.float32))
+    s.check(slopes=slopes, **kw)
+
+
+@pytest.mark.parametrize("dim,dtype,page", [(64, BF16, 16), (128, F16, 1), (256, BF16, 4)])
+@pytest.mark.parametrize("kw", [dict(window=70), dict(window=1), dict(slopes=True),
+                                dict(slopes=True, cap=5.0, window=100, scale=0.2)])
+def test_chains_on_mma_sync_with_windows_and_slopes(dim, dtype, page, kw):
+    heads, groups = 2, 3
+    new = [1, 5, 9, 2] if page == 16 else [70, 9, 30, 1]
+    s = Step([300, 0, 64, 1000], new, page, heads, groups, dim, dtype, False)
+    kw = dict(kw)
+    slopes = (2.0 ** (-np.arange(1, heads * groups + 1) / 2.0)).astype(np.float32) if kw.pop("slopes", False) else None
+    s.attend(scale=kw.get("scale", 0.0), softcap=kw.get("cap", 0.0), window=kw.get("window", 0),
+             slopes=None if slopes is None else dev(slopes, torch.float32))
+    s.check(slopes=slopes, **kw)
+
+
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+def test_the_same_bits_from_call_to_call(groups, dim, page):
+    s = Step([4000, 17, 900], [12, 1, 7], page, 2, groups, dim, BF16, True)
+    s.attend(softcap=30.0)
+    want = s.out.clone(), s.lse.clone()
+    for _ in range(5):
+        s.out.zero_(), s.lse.zero_()
+        s.attend(softcap=30.0)
+        assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1])
