@@ -455,3 +455,56 @@ def test_a_new_cache_serves_any_stream():
     cache = PagedCache(old.k, old.v, old.tables, old.lens, old.free, old.free_count)
     cache.plan(new, first, slots, pos, stream=side.cuda_stream)
     assert cache.error()[0] == 0 and host(slots).tolist() == [16, 17, 18]
+
+
+def test_the_binding_functions_make_the_same_calls():
+    """avsg.py's functions, which take structures and addresses, beside the cache's methods."""
+    from decode_serving_gb300 import avsg as C
+    from decode_serving_gb300.paged import PagedCache, rotary_frequencies
+    requests, heads, groups, dim = 3, 2, 4, 64
+    new, kept = dev(np.array([3, 1, 5])), dev(np.array([2, 0, 3]))
+    mask, path = dev(trees([3, 1, 5], 2), torch.int64), dev(np.array([0, 2, 0, 0, 0, 2, 4, 0, 0]))
+    gen = torch.Generator("cuda").manual_seed(4)
+    qkv = torch.randn(9, (groups + 2) * heads * dim, generator=gen, device="cuda").to(BF16)
+    freq = rotary_frequencies(dim).cuda()
+    a, b = groups * heads * dim, heads * dim
+    q, k, v = qkv.split((a, b, b), 1)
+    states = []
+    for how in ("methods", "functions"):
+        c = PagedCache.allocate(requests, 4, 8, heads, 8, dim)
+        first, slots, pos = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (4, 9, 9))
+        q_rot = torch.zeros(9, groups * heads, dim, dtype=BF16, device="cuda")
+        out, work = torch.zeros_like(q_rot), c.attention_workspace(groups, 5)
+        lse = torch.zeros(9, groups * heads, device="cuda")
+        if how == "methods":
+            c.plan(new, first, slots, pos, mask=mask)
+            c.rotary(q, k, v, pos, slots, freq, q_rot)
+            c.attend(q_rot, first, out, 5, work, mask=mask, lse=lse, softcap=20.0)
+            c.keep(first, path, kept)
+        else:
+            error = torch.zeros(4, dtype=torch.int32, device="cuda")
+            torch.cuda.synchronize()
+            p = C.avsg_pages(requests, 1, 8, heads, 8, dim, 4, C.AVSG_BF16, c.k.data_ptr(), c.v.data_ptr(),
+                             c.tables.data_ptr(), c.lens.data_ptr(), c.free.data_ptr(), c.free_count.data_ptr(),
+                             error.data_ptr())
+            C.avsg_page_plan(p, new.data_ptr(), mask.data_ptr(), 9, 9, first.data_ptr(), slots.data_ptr(),
+                             pos.data_ptr(), c.free_count.data_ptr())
+            width = qkv.shape[1]
+            C.avsg_rotary_write(p, C.avsg_rotary(
+                num_tokens=9, num_q_heads=groups * heads, rot_dim=dim, tokens_per_request=1, q_stride=width,
+                k_stride=width, v_stride=width, magnitude=1.0, d_q=q.data_ptr(), d_k=k.data_ptr(), d_v=v.data_ptr(),
+                d_freq=freq.data_ptr(), d_pos=pos.data_ptr(), d_slot=slots.data_ptr(), d_q_out=q_rot.data_ptr()))
+            assert C.avsg_tree_attention_workspace(p, groups, 5) == work.numel()
+            C.avsg_tree_attention(p, C.avsg_tree(
+                num_tokens=9, q_per_kv=groups, max_new=5, softcap=20.0, q_stride=a, d_q=q_rot.data_ptr(),
+                d_first=first.data_ptr(), d_mask=mask.data_ptr(), d_out=out.data_ptr(), d_lse=lse.data_ptr(),
+                d_work=work.data_ptr(), work_bytes=work.numel()))
+            C.avsg_tree_keep(p, first.data_ptr(), path.data_ptr(), 9, kept.data_ptr(), c.lens.data_ptr(),
+                             c.free_count.data_ptr())
+            with pytest.raises(C.AvsgError):
+                C.avsg_tree_keep(p, 0, path.data_ptr(), 9, kept.data_ptr(), c.lens.data_ptr(), c.free_count.data_ptr())
+            assert host(error)[0] == 0
+        states.append([x.clone() for x in (first, slots, pos, q_rot, out, lse, c.k, c.v, c.tables, c.lens, c.free,
+                                           c.free_count)])
+        assert host(c.lens).tolist() == [2, 0, 3]
+    assert all(torch.equal(x, y) for x, y in zip(*states))
