@@ -30,6 +30,13 @@ def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_tu
     return torch.from_numpy(t[:int(rot_dim) // 2].view(np.int64))
 
 
+def _pack(form, *values):
+    try:
+        return form.pack(*values)
+    except struct.error as e:                          # a number that its field does not hold
+        raise ValueError(str(e)) from None
+
+
 _P, _I32 = ctypes.c_void_p, ctypes.c_int32
 _calls = {}
 
@@ -64,6 +71,8 @@ class PagedCache:
         if k.device.type != "cuda":
             raise ValueError("the cache lives on a CUDA device")
         layers, pages, heads, page, dim = k.shape
+        if lens.dim() != 1:
+            raise ValueError("lens: [requests] is wanted")
         self.device, self.dtype, self._index = k.device, k.dtype, k.get_device()
         self.requests, self.kv_heads, self.head_dim = len(lens), heads, dim
         self.k, self.v, self.tables, self.lens = k, v, tables, lens
@@ -127,6 +136,9 @@ class PagedCache:
 
     def _heads(self, t):
         """Heads of a row tensor [T][heads * head_dim] or [T][heads][head_dim]."""
+        if not 2 <= t.dim() <= 3:
+            raise ValueError(f"q: [tokens][heads * head_dim] or [tokens][heads][head_dim] is wanted, not "
+                             f"{list(t.shape)}")
         return t.shape[1] if t.dim() == 3 else t.shape[1] // self.head_dim
 
     def plan(self, new, first, slots, positions, mask=None, free_count_out=None, stream=None):
@@ -159,7 +171,7 @@ class PagedCache:
         with kv_heads, any stride between tokens; slots [T] or None (slot t for
         token t); freq from ``rotary_frequencies``, on the device; q_out
         contiguous, the cache's type or float32."""
-        tokens, heads, dim = q.shape[0], self._heads(q), self.head_dim
+        heads, tokens, dim = self._heads(q), q.shape[0], self.head_dim
         kv = self.kv_heads * dim
         qs, ks, vs = self._rows("q", q, heads * dim), self._rows("k", k, kv), self._rows("v", v, kv)
         if k.shape[0] != tokens or v.shape[0] != tokens:
@@ -171,8 +183,8 @@ class PagedCache:
         self._check("freq", freq, torch.int64, pairs)
         if slots is not None:
             self._check("slots", slots, torch.int32, tokens)
-        rc = self._rotary(self._at, _ROTARY.pack(
-            tokens, heads, 2 * pairs, rot_offset, interleaved, f32, tokens_per_request, layer, qs, ks, vs,
+        rc = self._rotary(self._at, _pack(
+            _ROTARY, tokens, heads, 2 * pairs, rot_offset, interleaved, f32, tokens_per_request, layer, qs, ks, vs,
             magnitude, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
             0 if slots is None else slots.data_ptr(), q_out.data_ptr()), self._stream(stream))
         if rc:
@@ -191,7 +203,7 @@ class PagedCache:
         contiguous, lse [T][q_heads] float32 or None; first from ``plan``;
         max_new bounds every request's new tokens; mask [tokens] int64 words
         (None: chains); slopes [q_heads] float32 or None."""
-        tokens, heads, dim = q.shape[0], self._heads(q), self.head_dim
+        heads, tokens, dim = self._heads(q), q.shape[0], self.head_dim
         stride = self._rows("q", q, heads * dim)
         if heads % self.kv_heads:
             raise ValueError("q: a multiple of the cache's heads is wanted")
@@ -207,8 +219,8 @@ class PagedCache:
             self._check("lse", lse, torch.float32, tokens * heads)
         if slopes is not None:
             self._check("slopes", slopes, torch.float32, heads)
-        rc = self._attend(self._at, _TREE.pack(
-            tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
+        rc = self._attend(self._at, _pack(
+            _TREE, tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
             first.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if slopes is None else slopes.data_ptr(),
             out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size), self._stream(stream))
         if rc:

@@ -508,3 +508,38 @@ def test_the_binding_functions_make_the_same_calls():
                                            c.free_count)])
         assert host(c.lens).tolist() == [2, 0, 3]
     assert all(torch.equal(x, y) for x, y in zip(*states))
+
+
+def test_shapes_and_numbers_that_do_not_fit_are_refused_as_such():
+    """ValueError for shapes and whole numbers, AvsgError for what the library refuses: not whatever
+    error a bad shape or a number too large would run into."""
+    from decode_serving_gb300.avsg import AvsgError
+    from decode_serving_gb300.paged import PagedCache
+    c = PagedCache.allocate(2, 4, 8, 2, 16, 64)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.zeros(2, 128, dtype=BF16, device="cuda")
+    f = torch.zeros(32, dtype=torch.int64, device="cuda")
+    work = c.attention_workspace(1, 1)
+    for bad in (x[0], x[0, 0], x.reshape(2, 2, 32, 2), x[:, :65]):
+        with pytest.raises(ValueError):
+            c.rotary(bad, x, x, i(2), i(2), f, x)
+        with pytest.raises(ValueError):
+            c.rotary(x, bad, x, i(2), i(2), f, torch.empty_like(x))
+        with pytest.raises(ValueError):
+            c.attend(bad, i(3), torch.empty_like(x), 1, work)
+    for kw in (dict(layer=1 << 40), dict(rot_offset=-(1 << 40)), dict(tokens_per_request=1 << 31)):
+        with pytest.raises(ValueError):
+            c.rotary(x, x, x, i(2), i(2), f, torch.empty_like(x), **kw)
+    for kw in (dict(layer=1 << 40), dict(window=1 << 31)):
+        with pytest.raises(ValueError):
+            c.attend(x, i(3), torch.empty_like(x), 1, work, **kw)
+    with pytest.raises(ValueError):
+        c.attend(x, i(3), torch.empty_like(x), 1 << 31, work)
+    for kw in (dict(softcap=1e39), dict(scale=1e39), dict(scale=float("nan"))):
+        with pytest.raises(AvsgError):
+            c.attend(x, i(3), torch.empty_like(x), 1, work, **kw)
+    with pytest.raises(AvsgError):
+        c.rotary(x, x, x, i(2), i(2), f, torch.empty_like(x), magnitude=float("nan"))
+    with pytest.raises(ValueError):
+        PagedCache(c.k, c.v, c.tables, c.lens[0], c.free, c.free_count)
+    assert c.error()[0] == 0
