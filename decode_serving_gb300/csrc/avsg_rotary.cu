@@ -22,6 +22,7 @@
 // 80; 3 CTAs of 85 registers an SM 70, 4 of 64 75).  8 tokens: 6 us, the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <math.h>
 
 #include "avsg_paged.cuh"
 
@@ -280,7 +281,7 @@ extern "C" int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void
       r->rot_dim < 0 || r->rot_dim % 2 || r->rot_offset < 0 ||
       (int64_t)r->rot_offset + r->rot_dim > p->head_dim || r->tokens_per_request < 1 ||
       r->num_tokens % r->tokens_per_request || r->layer < 0 || r->layer >= p->num_layers ||
-      !(r->magnitude == r->magnitude) || r->reserved0 != 0)
+      !isfinite(r->magnitude) || r->reserved0 != 0)
     return AVSG_ERR_INVALID_ARG;
   if (r->rot_dim > kMaxRot || r->num_q_heads > 65535) return AVSG_ERR_CAPACITY;
   if (r->num_tokens == 0) return AVSG_OK;

@@ -427,7 +427,7 @@ typedef struct avsg_rotary {
   int32_t tokens_per_request; /* n: d_q_out is [T / n][H][n][G][D]; 1 is [T][heads][D] */
   int32_t layer;
   int64_t q_stride, k_stride, v_stride; /* values between tokens' rows */
-  float magnitude;            /* factor on cos and sin (1 for none) */
+  float magnitude;            /* factor on cos and sin (1 for none), finite */
   int32_t reserved0;          /* must be 0 */
   const void* d_q;            /* [T] rows of num_q_heads * D values, the cache's type */
   const void* d_k;            /* [T] rows of H * D */

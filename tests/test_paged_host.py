@@ -81,6 +81,13 @@ def test_bad_rotary(lib, kw, code):
     assert lib.avsg_rotary_write(p, avsg.avsg_rotary(**f), None) == code
 
 
+@pytest.mark.parametrize("magnitude,code", [(math.inf, -1), (-math.inf, -1), (math.nan, -1), (-2.0, 0), (0.0, 0)])
+def test_magnitudes_are_finite(lib, magnitude, code):
+    from decode_serving_gb300 import avsg
+    r = avsg.avsg_rotary(num_tokens=0, num_q_heads=4, rot_dim=64, tokens_per_request=1, magnitude=magnitude)
+    assert lib.avsg_rotary_write(pages()[0], r, None) == code
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(num_tokens=-1), -1), (dict(q_per_kv=0), -1), (dict(q_per_kv=65), -7), (dict(max_new=0), -1),
     (dict(layer=2), -1), (dict(layer=-1), -1), (dict(window=-1), -1), (dict(softmax_scale=-1.0), -1),
