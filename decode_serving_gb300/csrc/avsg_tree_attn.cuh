@@ -904,7 +904,7 @@ cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
   // A few units lie in up to 304 CTAs' shares: eight warps on a row (one: 16 us for 304
   // pieces), a block for 32 shares (one unit of 256 rows, 32768 tokens: 31 us the call, 80 with
   // a block for each share).
-  if ((long long)a.R * a.H * ((a.max_new + a.tpm - 1) / a.tpm) <= kFewUnits)
+  if ((long long)a.R * a.H * (((long long)a.max_new + a.tpm - 1) / a.tpm) <= kFewUnits)
     return launch_pdl(tree_merge_kernel<T, D, kMergeWarps>, dim3((a.ctas + 31) / 32, rows),
                       dim3(kMergeWarps * 32), 0, st, a, MT);
   // Else a warp per row, in few groups: every CTA of the grid without a unit to join costs its

@@ -270,3 +270,11 @@ def test_the_same_bits_from_call_to_call(groups, dim, page):
         s.out.zero_(), s.lse.zero_()
         s.attend(softcap=30.0)
         assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1])
+
+
+@pytest.mark.parametrize("groups,dim,page", KERNELS)
+def test_max_new_is_a_bound_alone(groups, dim, page):
+    """The largest one there is gives what the right one does."""
+    s = Step([400, 17, 0], [12, 1, 7], page, 2, groups, dim, BF16, True)
+    s.attend(most=2**31 - 1)
+    s.check()
