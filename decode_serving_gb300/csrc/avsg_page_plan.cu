@@ -257,16 +257,20 @@ __global__ void __launch_bounds__(kPlanThreads) keep_lengths_kernel(KeepArgs a) 
     const int warp = rank * (kPlanThreads / 32) + (tid >> 5), warps = ctas * (kPlanThreads / 32);
     if (a.path)
       for (int r = warp; r < a.R; r += warps) {
-        const int f = a.first[r], n = a.first[r + 1] - f, k = a.keep[r];
-        for (int i = tid & 31; i < k; i += 32) {
+        const int f = a.first[r], n = a.first[r + 1] - f, k = a.keep[r], lane = tid & 31;
+        if (k <= 0) continue;
+        // (whether rows move, and the pages that stay, are loaded beside the path)
+        const bool moves = a.path[f + k - 1] != k - 1;
+        bool bad_page = false;
+        for (int x = (a.len[r] >> a.shift) + lane; x < s_from[r]; x += 32) {
+          const int32_t id = a.tables[(size_t)r * a.max_pages + x];
+          bad_page |= id < 0 || id >= a.num_pages;
+        }
+        for (int i = lane; i < k; i += 32) {
           const int x = a.path[f + i], before = i ? a.path[f + i - 1] : -1;
           if (x <= before || x < 0 || x >= n) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, i);
         }
-        if (k > 0 && a.path[f + k - 1] != k - 1)
-          for (int x = (a.len[r] >> a.shift) + (tid & 31); x < s_from[r]; x += 32) {
-            const int32_t id = a.tables[(size_t)r * a.max_pages + x];
-            if (id < 0 || id >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
-          }
+        if (moves && bad_page) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
       }
     for (int e = rank * kPlanThreads + tid; e < (int)total; e += ctas * kPlanThreads) {
       const int r = find_request(s_back, a.R, e);

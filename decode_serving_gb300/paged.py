@@ -30,13 +30,6 @@ def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_tu
     return torch.from_numpy(t[:int(rot_dim) // 2].view(np.int64))
 
 
-def _pack(form, *values):
-    try:
-        return form.pack(*values)
-    except struct.error as e:                          # a number that its field does not hold
-        raise ValueError(str(e)) from None
-
-
 _P, _I32 = ctypes.c_void_p, ctypes.c_int32
 _calls = {}
 
@@ -183,10 +176,14 @@ class PagedCache:
         self._check("freq", freq, torch.int64, pairs)
         if slots is not None:
             self._check("slots", slots, torch.int32, tokens)
-        rc = self._rotary(self._at, _pack(
-            _ROTARY, tokens, heads, 2 * pairs, rot_offset, interleaved, f32, tokens_per_request, layer, qs, ks, vs,
-            magnitude, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
-            0 if slots is None else slots.data_ptr(), q_out.data_ptr()), self._stream(stream))
+        try:
+            args = _ROTARY.pack(
+                tokens, heads, 2 * pairs, rot_offset, interleaved, f32, tokens_per_request, layer, qs, ks, vs,
+                magnitude, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), freq.data_ptr(), positions.data_ptr(),
+                0 if slots is None else slots.data_ptr(), q_out.data_ptr())
+        except struct.error as e:                      # a number that its field does not hold
+            raise ValueError(str(e)) from None
+        rc = self._rotary(self._at, args, self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_rotary_write")
 
@@ -219,10 +216,14 @@ class PagedCache:
             self._check("lse", lse, torch.float32, tokens * heads)
         if slopes is not None:
             self._check("slopes", slopes, torch.float32, heads)
-        rc = self._attend(self._at, _pack(
-            _TREE, tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
-            first.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if slopes is None else slopes.data_ptr(),
-            out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size), self._stream(stream))
+        try:
+            args = _TREE.pack(
+                tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
+                first.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if slopes is None else slopes.data_ptr(),
+                out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size)
+        except struct.error as e:                      # a number that its field does not hold
+            raise ValueError(str(e)) from None
+        rc = self._attend(self._at, args, self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_tree_attention")
 
