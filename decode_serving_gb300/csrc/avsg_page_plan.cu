@@ -168,9 +168,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
       }
       slot[x] = (page << a.shift) + (p & page_mask);
       pos[x] = p;
-      if (a.mask && s_first[r + 1] - s_first[r] <= kMaxDrafts) {  // (longer requests are chains)
+      if (a.mask) {
         const unsigned long long m = a.mask[t];
-        if (m) pos[x] = len + __popcll(m) - 1;
+        // (requests of more drafts than a word has bits are chains)
+        if (m && s_first[r + 1] - s_first[r] <= kMaxDrafts) pos[x] = len + __popcll(m) - 1;
       }
     }
     if (a.wide && t4 + 4 <= a.capacity) {
