@@ -58,9 +58,11 @@
 // rows: 233 us, 256 rows: 384 us).
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
 // the waits after it return at once.  A warp whose wait failed issues no copy
-// and no product after it, and passes no buffer on; the others go on with what
-// their barriers still give them.  Copies and products that were issued are
-// awaited all the same before the CTA ends or frees its tensor memory.
+// after it and passes no buffer on, so that none is filled while its barrier
+// still expects a copy; the products after it are of no use to anyone (and
+// harmless: all operands lie where they always do).  Copies and products that
+// were issued are awaited all the same before the CTA ends or frees its tensor
+// memory.
 #include <cuda.h>
 #include <stdlib.h>
 
@@ -1002,11 +1004,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       int ps = 0;                          // halves of this stream since the start
       const uint32_t id_s = instruction<T>(UH, false), id_o = instruction<T>(D, true);
       constexpr uint32_t HALF_TILE = UH / 8 * 1024 * COLS;
-      // A wait of this lane has given up: it issues nothing more, and passes no buffer on.  (Each
-      // lane by itself, without a vote; those that issue are always the same.)
+      // A wait of this lane has given up: it passes no buffer on.  (Each lane by itself, without a
+      // vote: those that pass on are always the same.  Products that heed it too cost a prompt chunk
+      // of heads of 256 7%, 5% with a branch around the wait.)
       bool stop = false;
       auto wait = [&](uint32_t bar, int phase) {
-        if (!stop) stop = !bar_wait(bar, phase & 1, waits);
+        stop |= !bar_wait(bar, phase & 1, waits);
       };
       auto wait_load = [&](int place) -> uint32_t {
         const int i = idx + place, b = i % kRing;
@@ -1019,7 +1022,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         const uint32_t qa = uniform(operand_low(smem + q * M::Q)), to = uniform(tmem + 128 * x + 64 * (hh & 1));
         const uint32_t to_q = uniform(tmem + 128);   // (heads of 256)
         const uint32_t ka = uniform(operand_low(k + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(s_full(x, hh & 1));
-        if (elect_one() && !stop) {
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * 1024 + (ks % 4) * 32) >> 4;
@@ -1037,7 +1040,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         const uint32_t va = uniform(operand_low(v + (SOLO ? 0 : (hh & 1) * HALF_TILE))), bar = uniform(o_done(x));
         const uint32_t from = uniform(tmem + 128 * x + 64 * (hh & 1)), to = uniform(tmem + 256 + 128 * x);
         const uint32_t add = uniform(first ? 0 : 1);
-        if (elect_one() && !stop) {
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < UH / 16; ++ks)
             mma_ts(to, from + ks * 8, operand<COLS>(va + ks * (2048 * COLS >> 4)), id_o, ks > 0 ? 1 : add);
