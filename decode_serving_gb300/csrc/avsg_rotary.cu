@@ -19,7 +19,8 @@
 // once for several loads, all in flight before the first is used.
 // Measured: 16381 tokens of 32 + 8 + 8 heads of 128, half of each head turned:
 // 68 us, 5.9 TB/s of the copy's 6.78 (one token per CTA 100 us, two 77, eight
-// 80; 3 CTAs of 85 registers an SM 70, 4 of 64 75).  8 tokens: 6 us, the launch.
+// 80; 3 CTAs of 85 registers an SM 70, 4 of 64 75).  8 tokens: 2 us a call in a graph, 21 from
+// Python, which is the host's work.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

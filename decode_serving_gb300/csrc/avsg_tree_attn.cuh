@@ -22,14 +22,16 @@
 // * K and V tiles stream through shared memory by 16-byte cp.async, their
 //   page ids looked up one tile ahead; rows past the end are zero-filled;
 // * scores, the running maximum and sum, and the output stay in registers
-//   (fp32); P is rounded to the cache's type for the second product, the only
-//   rounding before the last one.
+//   (fp32); P is rounded to the cache's type for the second product, half a
+//   step and the only rounding before the last one (avsg_tree_umma.cu).
 // Measured (GB300, 6.78 TB/s copy): 64 requests x 8 kv-heads of 1000 tokens,
 // one token each, 4 query heads of 128: 57 us, 4.6 TB/s; 8 x 8 of 4000: 34 us;
-// one request of 4096 tokens and one head: 11.4 us with its merge, of which
+// one request of 4096 tokens and one head: 11 us with its merge, of which
 // the bytes need 0.3 (two dependent chains of loads, lengths - tables - rows
-// and head - partials, and two launches).  Heads of 256 (8 x 8 of 16000): 221
-// us at one token (4.7 TB/s), 297 us at 64 rows, where mma.sync's rate bounds it.
+// and head - partials, and two launches).  Heads of 256 (8 x 8 of 16000, pages
+// of 4): 271 us at one token (3.9 TB/s), 314 us at 64 rows.  With more rows
+// mma.sync's rate bounds it (16 x 8 units of 8192 tokens, 256 rows, heads of
+// 128, pages of 1 or 4: 580 us, 134 on tcgen05 with pages of 16).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -34,7 +34,7 @@
 // the products of one half hide the softmax of the next.  Stream 1's softmax
 // warps write half of the output, its issuing warp passes every tile on.  Q lies
 // in tensor memory, where stream 1's scores would be: a product of 64 keys then
-// takes 32 cycles (4096 after 4096: 621 us, 710 with both operands in shared
+// takes 32 cycles (4096 after 4096: 636 us, 710 with both operands in shared
 // memory).  The ring has 128 KB there; with 192 or 224 HBM gives less (16 x 8
 // units of 32768 tokens: 626 and 632 us, 605 so).
 //
@@ -45,17 +45,22 @@
 // 256 + 128 x.
 //
 // What bounds it.  Up to 128 rows: HBM (16 x 8 units of 32768 tokens, 16-token
-// pages, heads of 128: 322 us, 6.65 of 6.78 TB/s).  256 rows: the tensor cores
-// (64 drafts of 4 heads over the same: 415 to 435 us, 1.3 PFLOP/s; a causal
-// 4096-token chunk after 4096: 333 us, 1.65 PFLOP/s).  A product of 128 rows
+// pages, heads of 128: 318 us, 6.75 of 6.78 TB/s).  256 rows: the tensor cores
+// (64 drafts of 4 heads over the same: 412 to 420 us, 1.3 PFLOP/s; a causal
+// 4096-token chunk after 4096: 332 us, 1.24 PFLOP/s of the pairs that are seen:
+// about 0.7 of what the products' own cycles, 440 + 256 a half, allow).  A product of 128 rows
 // and 64 keys reads both operands from shared memory and takes 55 cycles, not
 // 32: the price of two places for scores.  One place of 128 keys (64 cycles a
 // product) made the streams wait for one another (533 us), and so did weights
 // in shared memory, which free the place early but cost a proxy fence a half
-// (554 us).  Heads of 256: 605 us for 16 x 8 units of 32768 tokens (7.1 TB/s), 621 us for
-// 4096 after 4096 (1.77 PFLOP/s).  Short units pay 6 to 10 us each for their beginning and
+// (554 us).  Heads of 256: 600 us for 16 x 8 units of 32768 tokens (7.2 TB/s), 636 us for
+// 4096 after 4096 (1.30 PFLOP/s of the pairs that are seen; four softmax warps carry all of it,
+// stream 1's wait for the output).  Short units pay 6 to 10 us each for their beginning and
 // end, a third of it hidden by the loads that run ahead (256 x 8 units of 1000 tokens, 64
-// rows: 233 us, 256 rows: 384 us).
+// rows: 234 us, 256 rows: 383 us).
+// P is rounded to the cache's type, half a step, like the result: the error against 64 bits is 1.4
+// times that of fp32 weights in bf16, 1.2 in fp16 (the remainder as a second product would cost the
+// time of the first again, a third of the tensor cores' time).  Sums, maxima and outputs are fp32.
 // Every wait is bounded; a wait that gives up latches AVSG_ERR_TIMEOUT, and
 // the waits after it return at once.  A warp whose wait failed issues no copy
 // after it and passes no buffer on, so that none is filled while its barrier
@@ -80,7 +85,7 @@ constexpr long long kWaitClocks = 4000000000LL;  // about two seconds
 
 struct UmmaArgs {
   TreeArgs t;
-  int box_rows;                            // tokens per TMA box: min(page, 128)
+  int box_rows;                            // tokens per TMA box: min(page, tile)
   int q_vec;                               // rows of q are 16-byte aligned
 #ifdef AVSG_DEBUG_BOUNDS
   long long wait_clocks;                   // what a wait may take
@@ -675,8 +680,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
             // The polynomial for a row whose scores of this half are all near 0, the quotient for the
             // others (see cap_polynomial_reach).  Where all rows are near, the special functions are
-            // left to the weights (16 x 8 units of 16384 tokens, 256 rows, D 128: 369 us; the
-            // quotient alone 432, both in one warp 555; without a cap 230).
+            // left to the weights (16 x 8 units of 16384 tokens, 256 rows, D 128: 358 to 372 us;
+            // the quotient alone 440, both in one warp 560; without a cap 227).
             const float k = a.cap_in * kCapUnit, co = a.cap_out;
             const uint64_t k2 = pair(k, k), one = pair(co, co), c1 = pair(kCap1 * co, kCap1 * co),
                            c2 = pair(kCap2 * co, kCap2 * co), c3 = pair(kCap3 * co, kCap3 * co);
@@ -1181,7 +1186,7 @@ EncodeTiled encode_tiled() {
 }
 
 // Pages as [num_pages][H * page / 8 groups][D / 64 blocks][8 rows][64 columns]
-// (strides of the plain layout), in boxes of min(page, 128) whole rows.
+// (strides of the plain layout), in boxes of min(page, tile) whole rows.
 bool encode_pages(CUtensorMap* map, const unsigned char* pages, const TreeArgs& a, int dtype, int D, int box) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;

@@ -361,7 +361,9 @@ int avsg_read_rows(const void* src, int64_t num_rows, int64_t row_bytes, const i
  * the device until the caller zeroes it.  avsg_page_plan calls on one d_error
  * must not run at the same time.  All memory is the caller's, on the
  * current device (INVALID_ARG for pages of another one), and must stay valid
- * until the enqueued work is done.  Calls on several streams are independent
+ * until the enqueued work is done.  A page belongs to one request: requests
+ * that share one (a common prompt) are not supported, avsg_tree_keep would
+ * give it back twice.  Calls on several streams are independent
  * as long as nothing that one of them writes is used by another at a time.
  */
 #define AVSG_BF16 0
@@ -412,7 +414,8 @@ int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const uint64_t* d_
  *   fraction (2^64 = one turn) of w_i = base^(-2i / rot_dim), scaled for long
  *   contexts: by 1 / factor when original is 0; else pairs that turn at least
  *   high_turns times in `original` tokens keep w_i, pairs below low_turns get
- *   w_i / factor, with a linear ramp in the turns between.
+ *   w_i / factor, with a ramp between that is linear in the turns (a model
+ *   whose ramp is linear in the pair's index needs a table of its own).
  */
 int avsg_rotary_frequencies(int32_t rot_dim, double base, double factor, double low_turns,
                             double high_turns, double original, uint64_t* out);
@@ -470,6 +473,9 @@ int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream);
  * it holds; neither does what lies in the pages behind the last new token.
  * A value of V that is not finite makes the results that see it not finite: an
  * infinity, or NaN where its weight rounds to 0 in the cache's type.
+ * Scores, sums and outputs are fp32; q is read and the weights are multiplied
+ * with V in the cache's type (half a step each), and so is the result.
+ * Outputs must not overlap inputs.
  */
 typedef struct avsg_tree {
   int32_t num_tokens;   /* rows of d_q, d_out and d_lse (at least d_first[R]; the
@@ -504,7 +510,8 @@ int avsg_tree_attention_workspace(const avsg_pages* p, int32_t q_per_kv, int32_t
  * D of 64, 128 or 256 (UNSUPPORTED else).  Latched errors: BAD_SELECTION (a
  * page id outside the pool, a negative length, rows past num_tokens; position
  * = the key), CAPACITY (more than max_new new tokens, or than the table
- * holds); d_out of such a call is undefined, nothing else is written.
+ * holds), TIMEOUT (a wait inside the kernel gave up after about two seconds);
+ * d_out and d_lse of such a call are undefined, nothing else is written.
  */
 int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void* stream);
 
