@@ -1010,8 +1010,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const uint32_t id_s = instruction<T>(UH, false), id_o = instruction<T>(D, true);
       constexpr uint32_t HALF_TILE = UH / 8 * 1024 * COLS;
       // A wait of this lane has given up: it passes no buffer on.  (Each lane by itself, without a
-      // vote: those that pass on are always the same.  Products that heed it too cost a prompt chunk
-      // of heads of 256 7%, 5% with a branch around the wait.)
+      // vote: those that pass on are always the same.  A branch around the waits would cost a prompt
+      // chunk of heads of 256 5%, products that heed it capped calls 1.5%.)
       bool stop = false;
       auto wait = [&](uint32_t bar, int phase) {
         stop |= !bar_wait(bar, phase & 1, waits);
