@@ -79,7 +79,8 @@ class PagedCache:
         self._check("free", free, torch.int32, pages)
         self._check("free_count", free_count, torch.int32, 1)
         self._error = torch.zeros(4, dtype=torch.int32, device=k.device)
-        torch.cuda.current_stream(k.device).synchronize()  # (any stream may read it from here on)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(k.device).synchronize()  # (any stream may read it from here on)
         self._pages = C.avsg_pages(len(lens), layers, pages, heads, page, dim, tables.shape[1],
                                    _TYPES[k.dtype], k.data_ptr(), v.data_ptr(), tables.data_ptr(),
                                    lens.data_ptr(), free.data_ptr(), free_count.data_ptr(),

@@ -543,3 +543,22 @@ def test_shapes_and_numbers_that_do_not_fit_are_refused_as_such():
     with pytest.raises(ValueError):
         PagedCache(c.k, c.v, c.tables, c.lens[0], c.free, c.free_count)
     assert c.error()[0] == 0
+
+
+def test_a_cache_made_in_a_capture():
+    """Its error word is zeroed by each replay, behind which the graph's calls run."""
+    from decode_serving_gb300.paged import PagedCache
+    old = PagedCache.allocate(1, 2, 2, 1, 16, 64)
+    first, slots, pos = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 3, 3))
+    new, count = dev(np.array([3])), torch.zeros(1, dtype=torch.int32, device="cuda")
+    old.plan(new, first, slots, pos, free_count_out=count)
+    want = host(slots).copy()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        cache = PagedCache(old.k, old.v, old.tables, old.lens, old.free, old.free_count)
+        cache.plan(new, first, slots, pos, free_count_out=count)
+    for _ in range(2):
+        slots.zero_()
+        graph.replay()
+        assert cache.error()[0] == 0 and (host(slots) == want).all()
