@@ -150,6 +150,18 @@ class avsg_tree(ctypes.Structure):
     ]
 
 
+class avsg_prefixes(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("d_leader", ctypes.c_void_p),
+        ("d_shared", ctypes.c_void_p),
+        ("d_first", ctypes.c_void_p),
+        ("d_token", ctypes.c_void_p),
+        ("d_request", ctypes.c_void_p),
+    ]
+
+
 AVSG_NUM_KERNELS = 8
 
 
@@ -191,6 +203,19 @@ SIGNATURES = {
                                       ctypes.POINTER(ctypes.c_size_t)],
     "avsg_tree_attention": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_tree), _P],
     "avsg_tree_keep": [ctypes.POINTER(avsg_pages), _P, _P, _I32, _P, _P, _P, _P],
+    "avsg_rotary_write_axes": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_rotary), _I32, _P, _P],
+    "avsg_page_fork_workspace": [ctypes.POINTER(avsg_pages), ctypes.POINTER(ctypes.c_size_t)],
+    "avsg_page_fork": [ctypes.POINTER(avsg_pages), _P, _P, _P, ctypes.c_size_t, _P],
+    "avsg_tree_keep_shared": [ctypes.POINTER(avsg_pages), _P, _P, _P, _I32, _P, _P, _P, _P],
+    "avsg_page_compact_workspace": [ctypes.POINTER(avsg_pages), ctypes.POINTER(ctypes.c_size_t)],
+    "avsg_page_compact": [ctypes.POINTER(avsg_pages)] + [_P] * 6 + [ctypes.c_size_t, _P],
+    "avsg_prefix_find_workspace": [ctypes.POINTER(avsg_pages), ctypes.POINTER(ctypes.c_size_t)],
+    "avsg_prefix_find": [ctypes.POINTER(avsg_pages), _P, _I32, ctypes.POINTER(avsg_prefixes), _P,
+                         ctypes.c_size_t, _P],
+    "avsg_prefix_attention_workspace": [ctypes.POINTER(avsg_pages), _I32, _I32, _I32,
+                                        ctypes.POINTER(ctypes.c_size_t)],
+    "avsg_prefix_attention": [ctypes.POINTER(avsg_pages), ctypes.POINTER(avsg_tree),
+                              ctypes.POINTER(avsg_prefixes), _P],
     "avsg_read_rows": [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, _I32, _P, _P],
 }
 
@@ -372,6 +397,69 @@ def avsg_tree_keep(pages: avsg_pages, d_first, d_path, num_path, d_keep, d_len_o
                    stream=0) -> None:
     _check(load_library().avsg_tree_keep(pages, d_first, d_path or None, num_path, d_keep, d_len_out,
                                          d_free_count_out, stream or None), "avsg_tree_keep")
+
+
+def avsg_rotary_write_axes(pages: avsg_pages, args: "avsg_rotary", num_axes, d_axis, stream=0) -> None:
+    _check(load_library().avsg_rotary_write_axes(pages, args, num_axes, d_axis or None, stream or None),
+           "avsg_rotary_write_axes")
+
+
+def avsg_page_fork_workspace(pages: avsg_pages) -> int:
+    """Bytes of workspace avsg_page_fork needs."""
+    n = ctypes.c_size_t()
+    _check(load_library().avsg_page_fork_workspace(pages, ctypes.byref(n)), "avsg_page_fork_workspace")
+    return n.value
+
+
+def avsg_page_fork(pages: avsg_pages, d_parent, d_shares, d_work, work_bytes, stream=0) -> None:
+    _check(load_library().avsg_page_fork(pages, d_parent, d_shares, d_work, work_bytes, stream or None),
+           "avsg_page_fork")
+
+
+def avsg_tree_keep_shared(pages: avsg_pages, d_shares, d_first, d_path, num_path, d_keep, d_len_out,
+                          d_free_count_out, stream=0) -> None:
+    _check(load_library().avsg_tree_keep_shared(pages, d_shares, d_first, d_path or None, num_path, d_keep,
+                                                d_len_out, d_free_count_out, stream or None),
+           "avsg_tree_keep_shared")
+
+
+def avsg_page_compact_workspace(pages: avsg_pages) -> int:
+    """Bytes of workspace avsg_page_compact needs."""
+    n = ctypes.c_size_t()
+    _check(load_library().avsg_page_compact_workspace(pages, ctypes.byref(n)), "avsg_page_compact_workspace")
+    return n.value
+
+
+def avsg_page_compact(pages: avsg_pages, d_shares, d_shares_out, d_tables_out, d_free_out, d_map, d_work,
+                      work_bytes, stream=0) -> None:
+    _check(load_library().avsg_page_compact(pages, d_shares or None, d_shares_out or None, d_tables_out,
+                                            d_free_out, d_map, d_work, work_bytes, stream or None),
+           "avsg_page_compact")
+
+
+def avsg_prefix_find_workspace(pages: avsg_pages) -> int:
+    """Bytes of workspace avsg_prefix_find needs."""
+    n = ctypes.c_size_t()
+    _check(load_library().avsg_prefix_find_workspace(pages, ctypes.byref(n)), "avsg_prefix_find_workspace")
+    return n.value
+
+
+def avsg_prefix_find(pages: avsg_pages, d_first, min_tokens, prefixes: avsg_prefixes, d_work, work_bytes,
+                     stream=0) -> None:
+    _check(load_library().avsg_prefix_find(pages, d_first, min_tokens, prefixes, d_work, work_bytes,
+                                           stream or None), "avsg_prefix_find")
+
+
+def avsg_prefix_attention_workspace(pages: avsg_pages, q_per_kv, max_new, num_tokens) -> int:
+    """Bytes of workspace avsg_prefix_attention needs."""
+    n = ctypes.c_size_t()
+    _check(load_library().avsg_prefix_attention_workspace(pages, q_per_kv, max_new, num_tokens, ctypes.byref(n)),
+           "avsg_prefix_attention_workspace")
+    return n.value
+
+
+def avsg_prefix_attention(pages: avsg_pages, args: "avsg_tree", prefixes: avsg_prefixes, stream=0) -> None:
+    _check(load_library().avsg_prefix_attention(pages, args, prefixes, stream or None), "avsg_prefix_attention")
 
 
 def avsg_strerror(code: int) -> str:

@@ -201,6 +201,7 @@ struct KeepArgs {
   int32_t* free_list;
   const int32_t* count;
   int32_t* count_out;
+  const int32_t* shares;         // or null: no page is shared
   DevErr* err;
 };
 
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kPlanThreads) keep_lengths_kernel(KeepArgs a) 
     for (int e = rank * kPlanThreads + tid; e < (int)total; e += ctas * kPlanThreads) {
       const int r = find_request(s_back, a.R, e);
       const int32_t id = a.tables[(size_t)r * a.max_pages + s_from[r] + e - s_back[r]];
-      if (id < 0 || id >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
+      if (id < 0 || id >= a.num_pages || (a.shares && a.shares[id] != 0)) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
     }
     __threadfence();
   }
@@ -434,9 +435,9 @@ extern "C" int avsg_page_plan(const avsg_pages* p, const int32_t* d_new, const u
   return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
 }
 
-extern "C" int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const int32_t* d_path,
-                              int32_t num_path, const int32_t* d_keep, int32_t* d_len_out,
-                              int32_t* d_free_count_out, void* stream) {
+static int tree_keep(const avsg_pages* p, const int32_t* d_shares, const int32_t* d_first, const int32_t* d_path,
+                     int32_t num_path, const int32_t* d_keep, int32_t* d_len_out, int32_t* d_free_count_out,
+                     void* stream) {
   int rc = check_pages(p);
   if (rc != AVSG_OK) return rc;
   if (!d_first || !d_keep || !d_len_out || !d_free_count_out || num_path < 0) return AVSG_ERR_INVALID_ARG;
@@ -459,6 +460,7 @@ extern "C" int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const
   a.free_list = p->d_free;
   a.count = p->d_free_count;
   a.count_out = d_free_count_out;
+  a.shares = d_shares;
   a.err = reinterpret_cast<DevErr*>(p->d_error);
   const size_t smem = (2 * (size_t)a.R + 1) * sizeof(int32_t);
   const int ctas = cluster_for((long long)a.R * 64);  // a warp per 32 kept drafts
@@ -485,4 +487,19 @@ extern "C" int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const
     e = launch_pdl(keep_rows_kernel, dim3(a.R, p->num_layers), dim3(kMoveThreads), 0, st, m);
   }
   return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
+}
+
+extern "C" int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const int32_t* d_path,
+                              int32_t num_path, const int32_t* d_keep, int32_t* d_len_out,
+                              int32_t* d_free_count_out, void* stream) {
+  return tree_keep(p, nullptr, d_first, d_path, num_path, d_keep, d_len_out, d_free_count_out, stream);
+}
+
+extern "C" int avsg_tree_keep_shared(const avsg_pages* p, const int32_t* d_shares, const int32_t* d_first,
+                                     const int32_t* d_path, int32_t num_path, const int32_t* d_keep,
+                                     int32_t* d_len_out, int32_t* d_free_count_out, void* stream) {
+  const int rc = check_pages(p);
+  if (rc != AVSG_OK) return rc;
+  if (!d_shares) return AVSG_ERR_INVALID_ARG;
+  return tree_keep(p, d_shares, d_first, d_path, num_path, d_keep, d_len_out, d_free_count_out, stream);
 }

@@ -11,6 +11,7 @@ namespace avsg {
 constexpr int kMaxPagedRequests = 8192;  // lengths of all requests are scanned by every CTA
 constexpr int kMaxDrafts = 64;           // bits of a draft's ancestor mask
 constexpr int kMaxDevicesPaged = 64;
+constexpr int kMaxColumns = 1 << 30;     // table columns of the calls that walk whole rows
 
 // Device of the current context and its SM count; d_ptr must be memory of
 // that device (a tensor of another one would fault in the kernel).

@@ -1,0 +1,237 @@
+// avsg_prefix_attention: tree attention in which the prefix that a group of
+// requests shares is computed once for all of them.
+//
+// Softmax over a row's keys splits over any partition of them: with (m, l, o) the maximum,
+// the sum of 2^(s - m) and the output not divided by it of either part,
+//   out = sum_i o_i 2^(m_i - m) / sum_i l_i 2^(m_i - m),  m = max_i m_i.
+// So there are two lists of units, each cut into equal shares as in
+// avsg_tree_attn.cuh:
+//   part 0  (group, kv-head, m-tile): the group's new tokens, listed by
+//           avsg_prefix_find, as rows, its prefix as keys;
+//   part 1  (request, kv-head, m-tile): a request's new tokens, its keys
+//           behind the prefix (all of them where it has none, and then the output itself);
+// and a kernel that joins a row's pieces of both.  The parts are launches of
+// their own: a group has many rows and a long prefix (tcgen05's work), a request often few rows
+// and few keys of its own (mma.sync's).  Part 1 does not wait for part 0
+// before it begins -- its blocks fill SMs that part 0 leaves -- but before it ends,
+// so that what follows it follows both.
+#include "avsg_tree_plan.cuh"
+
+namespace avsg {
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+struct JoinPart {
+  const int4* unit;              // see TreeArgs
+  const float* rows;
+  const float* rows_ml;
+  const float* partial;
+  const float* ml;
+  int ctas, MT;
+};
+struct JoinArgs {
+  JoinPart part[2];
+  const int32_t* first;
+  unsigned char* out;
+  float* lse;
+  DevErr* err;
+  int R, H, G, T;
+};
+
+// A warp joins the pieces of one row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(JoinArgs a) {
+  constexpr int VPL = D / 32;
+  griddep_wait();
+  if (load_err(a.err) != 0) return;
+  const int lane = threadIdx.x & 31, heads = a.H * a.G;
+  const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int t = (int)(row / heads), hg = (int)(row - (long long)t * heads), h = hg / a.G, g = hg - h * a.G;
+  if (t >= a.T || t >= a.first[a.R]) return;
+  const int4 own = a.part[1].unit[(long long)t * a.H + h];
+  if (own.y < 0) return;                   // written by its part
+  int4 pre = make_int4(0, -1, 0, 0);
+  if (own.w) pre = a.part[0].unit[(long long)t * a.H + h];
+  auto pieces = [&](const int4& u) { return u.y < 0 ? 0 : u.y == 0 ? 1 : u.y; };
+  auto fits = [&](const JoinPart& p, const int4& u) {
+    return u.y <= 0 || (u.x >= 0 && u.x < p.ctas && u.y <= p.ctas - u.x && u.z >= 0 && u.z < p.MT / a.G);
+  };
+  if ((own.w && pre.y < 0) || !fits(a.part[0], pre) || !fits(a.part[1], own)) {
+    // (a token that no group lists)
+    if (lane == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, t);
+    return;
+  }
+  const int n0 = pieces(pre), n = n0 + pieces(own);
+  // place of piece i: its row among the part's partials or rows
+  auto place = [&](int i, const float*& ml, const float*& o) {
+    const bool second = i >= n0;
+    const JoinPart& p = a.part[second];
+    const int4 u = second ? own : pre;
+    const int j = second ? i - n0 : i;
+    if (u.y == 0) {
+      ml = p.rows_ml + row * 2;
+      o = p.rows + row * D;
+    } else {
+      // the first piece is the second partial of its CTA, the others the first ones of theirs
+      const long long slot = (long long)(2 * (u.x + j) + (j == 0 ? 1 : 0)) * p.MT + u.z * a.G + g;
+      ml = p.ml + slot * 2;
+      o = p.partial + slot * D;
+    }
+  };
+  float top = -INFINITY, sum = 0.f, o[VPL];
+#pragma unroll
+  for (int x = 0; x < VPL; ++x) o[x] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float *ml = nullptr, *from = nullptr;
+    float2 y = make_float2(-INFINITY, 0.f);
+    if (i0 + lane < n) {
+      place(i0 + lane, ml, from);
+      y = *reinterpret_cast<const float2*>(ml);
+    }
+    float now = y.x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+    now = fmaxf(now, top);
+    const float use = now == -INFINITY ? 0.f : now, old = tree::ex2(top - use);
+    top = now;
+    const float f = tree::ex2(y.x - use);
+    float add = y.y * f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+    sum = sum * old + add;
+#pragma unroll
+    for (int x = 0; x < VPL; ++x) o[x] *= old;
+    const int most = min(32, n - i0);
+#pragma unroll 4
+    for (int j = 0; j < most; ++j) {
+      const float w = __shfl_sync(0xffffffffu, f, j);
+      const float* p = reinterpret_cast<const float*>(
+                           __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), j)) + lane * VPL;
+      if constexpr (VPL >= 4) {
+#pragma unroll
+        for (int x = 0; x < VPL; x += 4) {
+          const float4 z = *reinterpret_cast<const float4*>(p + x);
+          o[x] += z.x * w;
+          o[x + 1] += z.y * w;
+          o[x + 2] += z.z * w;
+          o[x + 3] += z.w * w;
+        }
+      } else {
+        const float2 z = *reinterpret_cast<const float2*>(p);
+        o[0] += z.x * w;
+        o[1] += z.y * w;
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  unsigned char* dst = a.out + (row * D + lane * VPL) * 2;
+#pragma unroll
+  for (int x = 0; x < VPL; x += 2)
+    *reinterpret_cast<uint32_t*>(dst + x * 2) = tree::pack<T>(o[x] * inv, o[x + 1] * inv);
+  if (a.lse && lane == 0) {
+    constexpr float shift = std::is_same<T, __half>::value ? tree::kHalfShift : 0.f;
+    a.lse[row] = sum == 0.f ? -INFINITY : (top - shift) * 0.6931471805599453f + logf(sum);
+  }
+}
+
+template <typename T>
+cudaError_t launch_join(const JoinArgs& a, int D, cudaStream_t st) {
+  const long long rows = (long long)a.T * a.H * a.G;
+  const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))), block(kJoinThreads);
+  return D == 64    ? launch_pdl(prefix_join_kernel<T, 64>, grid, block, 0, st, a)
+         : D == 128 ? launch_pdl(prefix_join_kernel<T, 128>, grid, block, 0, st, a)
+                    : launch_pdl(prefix_join_kernel<T, 256>, grid, block, 0, st, a);
+}
+
+// The kernel of part 0: every new token may be a row of one group.
+Plan plan_prefix(const avsg_pages* p, int G, int num_tokens, int sms) {
+  return plan_attention(p, G, num_tokens, sms);
+}
+
+struct PrefixWork {
+  size_t unit[2], rows_ml[2], rows[2], part[2], bytes;
+};
+PrefixWork prefix_layout(const avsg_pages* p, int G, int max_new, int num_tokens, int sms) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t T = num_tokens, heads = (size_t)p->num_kv_heads * G;
+  PrefixWork w;
+  size_t at = 0;
+  for (int i = 0; i < 2; ++i) {
+    w.unit[i] = at;
+    w.rows_ml[i] = w.unit[i] + up(T * p->num_kv_heads * sizeof(int4));
+    w.rows[i] = w.rows_ml[i] + up(T * heads * 2 * sizeof(float));
+    w.part[i] = w.rows[i] + up(T * heads * p->head_dim * sizeof(float));
+    at = w.part[i] + up(workspace_bytes(p->head_dim, G, i == 0 ? (num_tokens < 1 ? 1 : num_tokens) : max_new, sms));
+  }
+  w.bytes = at;
+  return w;
+}
+
+}  // namespace
+}  // namespace avsg
+
+using namespace avsg;
+
+extern "C" int avsg_prefix_attention_workspace(const avsg_pages* p, int32_t q_per_kv, int32_t max_new,
+                                               int32_t num_tokens, size_t* bytes) {
+  const int rc = check_attention(p, q_per_kv, max_new);
+  if (rc != AVSG_OK) return rc;
+  if (!bytes || num_tokens < 0) return AVSG_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  const int rd = paged_device(p->d_k, &dev, &sms);
+  if (rd != AVSG_OK) return rd;
+  *bytes = prefix_layout(p, q_per_kv, max_new, num_tokens, sms).bytes;
+  return AVSG_OK;
+}
+
+extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, const avsg_prefixes* x, void* stream) {
+  if (!x || x->num_tokens < 0 || x->reserved0 != 0) return AVSG_ERR_INVALID_ARG;
+  TreeArgs a{};
+  int dev = 0, sms = 0;
+  const int rc = tree_args(p, t, &a, &dev, &sms);
+  if (rc != AVSG_OK || a.T == 0) return rc;
+  if (!x->d_shared || !x->d_first || (x->num_tokens > 0 && (!x->d_token || !x->d_request)))
+    return AVSG_ERR_INVALID_ARG;
+  const int D = p->head_dim, G = t->q_per_kv;
+  const PrefixWork w = prefix_layout(p, G, t->max_new, t->num_tokens, sms);
+  if (t->work_bytes < w.bytes) return AVSG_ERR_CAPACITY;
+  if ((int64_t)a.T * a.H * G > (int64_t)INT32_MAX * (kJoinThreads / 32)) return AVSG_ERR_CAPACITY;
+  unsigned char* work = static_cast<unsigned char*>(t->d_work);
+  a.places = x->num_tokens;
+  a.shared = x->d_shared;
+  a.group_first = x->d_first;
+  a.token = x->d_token;
+  a.request = x->d_request;
+  JoinArgs j{};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  for (int i = 0; i < 2; ++i) {
+    const Plan plan = i == 0 ? plan_prefix(p, G, t->num_tokens, sms) : plan_attention(p, G, t->max_new, sms);
+    const Workspace l = tree_layout(plan, D);
+    TreeArgs b = a;
+    b.part = i;
+    b.unit = reinterpret_cast<int4*>(work + w.unit[i]);
+    b.rows_ml = reinterpret_cast<float*>(work + w.rows_ml[i]);
+    b.rows = reinterpret_cast<float*>(work + w.rows[i]);
+    b.ml = reinterpret_cast<float*>(work + w.part[i] + l.ml);
+    b.partial = reinterpret_cast<float*>(work + w.part[i] + l.part);
+    b.tpm = plan.MT / G;
+    b.ctas = plan.ctas;
+    b.begin = plan.begin;
+    j.part[i] = JoinPart{b.unit, b.rows, b.rows_ml, b.partial, b.ml, plan.ctas, plan.MT};
+    const cudaError_t e = plan.umma ? launch_prefix_umma(b, p->dtype, D, dev, st)
+                                    : launch_prefix_part(b, p->dtype, D, plan.wm, dev, st);
+    if (e != cudaSuccess) return AVSG_ERR_CUDA;
+  }
+  j.first = t->d_first;
+  j.out = a.out;
+  j.lse = a.lse;
+  j.err = a.err;
+  j.R = a.R;
+  j.H = a.H;
+  j.G = G;
+  j.T = a.T;
+  const cudaError_t e =
+      p->dtype == AVSG_BF16 ? launch_join<__nv_bfloat16>(j, D, st) : launch_join<__half>(j, D, st);
+  return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
+}

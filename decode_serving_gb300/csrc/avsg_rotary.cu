@@ -11,6 +11,9 @@
 // (at most half a turn, 2^-32 turns per unit), go to sincospif; what is left
 // is the rounding to fp32, 2^-25 turns (2e-7 rad), at any position.
 //
+// With several axes (time, height, width of an image's or a video's patches)
+// pair i turns by the position on axis[i], one more load for a token's angle.
+//
 // What bounds it: bytes.  q, k and v are read once and written once; the
 // angles of a token are computed once per CTA into shared memory and used by
 // all its heads.  A thread owns one place of one head -- two chunks of 16
@@ -47,7 +50,9 @@ struct RotArgs {
   void* kp;
   void* vp;
   const unsigned long long* freq;
-  const int32_t* pos;
+  const int32_t* pos;            // [axes][T]
+  const int32_t* axis;           // [rot / 2] the axis of a pair's position, or null: one axis
+  int axes;
   const int32_t* slot;
   DevErr* err;
 };
@@ -91,15 +96,16 @@ __device__ __forceinline__ void store_vec(TO* p, const float* x) {
 }
 
 // T: type of q, k, v and the cache; TQ: type of q_out; VEC: values per chunk;
-// TOK: tokens per CTA.
-template <typename T, typename TQ, int VEC, int TOK>
+// TOK: tokens per CTA; AXES: positions of several axes (as a switch inside one kernel it
+// cost the one-axis prompt 15%, 68 to 79 us).
+template <typename T, typename TQ, int VEC, int TOK, bool AXES>
 __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
   extern __shared__ float2 s_cs[];            // [TOK][rot / 2] cos, sin
   const int tid = threadIdx.x, half = a.rot >> 1;
   const int t0 = blockIdx.x * TOK;
   const int groups = half / VEC, units = a.unit_heads * a.per_head;
   griddep_wait();
-  const bool latched = load_err(a.err) != 0;
+  bool latched = load_err(a.err) != 0;
 
   // One place of one head: values d0 .. and d1 .. of it (d1 < 0: one chunk alone; d0 < 0: none).
   const T* src;
@@ -155,7 +161,17 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
   for (int x = tid; x < TOK * half; x += blockDim.x) {
     const int j = x / half, i = x - j * half, t = t0 + j;
     if (t >= a.T) break;
-    const unsigned long long turn = (unsigned long long)(long long)a.pos[t] * a.freq[i];
+    long long at = t;
+    if constexpr (AXES) {
+      int axis = a.axis[i];
+      if (axis < 0 || axis >= a.axes) {    // (every CTA sees every pair: nothing is written)
+        raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, i);
+        latched = true;
+        axis = 0;
+      }
+      at += (long long)axis * a.T;
+    }
+    const unsigned long long turn = (unsigned long long)(long long)a.pos[at] * a.freq[i];
     float sn, cs;
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
     s_cs[x] = make_float2(cs * a.magnitude, sn * a.magnitude);
@@ -234,7 +250,7 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
   }
 }
 
-template <typename T, typename TQ, int VEC>
+template <typename T, typename TQ, int VEC, bool AXES>
 cudaError_t launch_rotary(const RotArgs& in, int sms, cudaStream_t st) {
   RotArgs a = in;
   const int qk = a.rot / 2 / VEC + ((a.D - a.rot) / VEC + 1) / 2, v = (a.D / VEC + 1) / 2;
@@ -252,11 +268,11 @@ cudaError_t launch_rotary(const RotArgs& in, int sms, cudaStream_t st) {
   const int most = (4 * sms + ctas - 1) / ctas;
   if (split > most) split = most;
   const size_t smem = (size_t)tok * (a.rot / 2) * sizeof(float2);
-  if (many) return launch_pdl(rotary_kernel<T, TQ, VEC, kRotTokens>, dim3(ctas, split), dim3(threads), smem, st, a);
-  return launch_pdl(rotary_kernel<T, TQ, VEC, 1>, dim3(ctas, split), dim3(threads), smem, st, a);
+  if (many) return launch_pdl(rotary_kernel<T, TQ, VEC, kRotTokens, AXES>, dim3(ctas, split), dim3(threads), smem, st, a);
+  return launch_pdl(rotary_kernel<T, TQ, VEC, 1, AXES>, dim3(ctas, split), dim3(threads), smem, st, a);
 }
 
-template <typename T, typename TQ>
+template <typename T, typename TQ, bool AXES>
 cudaError_t launch_rotary_vec(const RotArgs& a, int sms, cudaStream_t st) {
   // The widest chunk that every row start, the rotated part and its halves
   // are a multiple of, and that q, k, v are aligned to.
@@ -265,9 +281,17 @@ cudaError_t launch_rotary_vec(const RotArgs& a, int sms, cudaStream_t st) {
                    reinterpret_cast<uintptr_t>(a.v) |
                    (reinterpret_cast<uintptr_t>(a.q_out) / (sizeof(TQ) / 2));
   bits |= (long long)(ptrs / 2);
-  if (bits % 8 == 0) return launch_rotary<T, TQ, 8>(a, sms, st);
-  if (bits % 4 == 0) return launch_rotary<T, TQ, 4>(a, sms, st);
-  return launch_rotary<T, TQ, 1>(a, sms, st);
+  if (bits % 8 == 0) return launch_rotary<T, TQ, 8, AXES>(a, sms, st);
+  if (bits % 4 == 0) return launch_rotary<T, TQ, 4, AXES>(a, sms, st);
+  return launch_rotary<T, TQ, 1, AXES>(a, sms, st);
+}
+template <bool AXES>
+cudaError_t launch_rotary_any(const RotArgs& a, int dtype, bool q_f32, int sms, cudaStream_t st) {
+  if (dtype == AVSG_BF16)
+    return q_f32 ? launch_rotary_vec<__nv_bfloat16, float, AXES>(a, sms, st)
+                 : launch_rotary_vec<__nv_bfloat16, __nv_bfloat16, AXES>(a, sms, st);
+  return q_f32 ? launch_rotary_vec<__half, float, AXES>(a, sms, st)
+               : launch_rotary_vec<__half, __half, AXES>(a, sms, st);
 }
 
 }  // namespace
@@ -275,7 +299,8 @@ cudaError_t launch_rotary_vec(const RotArgs& a, int sms, cudaStream_t st) {
 
 using namespace avsg;
 
-extern "C" int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream) {
+static int rotary_write(const avsg_pages* p, const avsg_rotary* r, int32_t axes, const int32_t* d_axis,
+                        void* stream) {
   int rc = check_pages(p);
   if (rc != AVSG_OK) return rc;
   if (!r || r->num_tokens < 0 || r->num_q_heads < 1 || r->num_q_heads % p->num_kv_heads ||
@@ -327,15 +352,24 @@ extern "C" int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void
   a.vp = static_cast<unsigned char*>(p->d_v) + r->layer * layer;
   a.freq = reinterpret_cast<const unsigned long long*>(r->d_freq);
   a.pos = r->d_pos;
+  a.axis = d_axis;
+  a.axes = axes;
   a.slot = r->d_slot;
   a.err = reinterpret_cast<DevErr*>(p->d_error);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (p->dtype == AVSG_BF16)
-    e = r->q_f32 ? launch_rotary_vec<__nv_bfloat16, float>(a, sms, st)
-                 : launch_rotary_vec<__nv_bfloat16, __nv_bfloat16>(a, sms, st);
-  else
-    e = r->q_f32 ? launch_rotary_vec<__half, float>(a, sms, st)
-                 : launch_rotary_vec<__half, __half>(a, sms, st);
+  const cudaError_t e = d_axis ? launch_rotary_any<true>(a, p->dtype, r->q_f32, sms, st)
+                               : launch_rotary_any<false>(a, p->dtype, r->q_f32, sms, st);
   return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
+}
+
+extern "C" int avsg_rotary_write(const avsg_pages* p, const avsg_rotary* r, void* stream) {
+  return rotary_write(p, r, 1, nullptr, stream);
+}
+
+extern "C" int avsg_rotary_write_axes(const avsg_pages* p, const avsg_rotary* r, int32_t num_axes,
+                                      const int32_t* d_axis, void* stream) {
+  const int rc = check_pages(p);
+  if (rc != AVSG_OK) return rc;
+  if (!r || num_axes < 1 || (r->rot_dim > 0 && !d_axis)) return AVSG_ERR_INVALID_ARG;
+  return rotary_write(p, r, num_axes, d_axis, stream);
 }

@@ -36,6 +36,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 
 #include "avsg_paged.cuh"
@@ -56,7 +57,7 @@ struct TreeArgs {
   int4* head;                    // [ctas] {pieces, first token, kv-head, rows} of the unit that
                                  // begins in the CTA's share and ends in another (pieces 0: none)
   float* ml;                     // [2 * ctas][MT][2] running maximum (log2) and sum of a partial
-  float* part;                   // [2 * ctas][MT][D] its output, not divided by the sum
+  float* partial;                // [2 * ctas][MT][D] its output, not divided by the sum
   DevErr* err;
   long long q_stride;            // values between tokens of q
   int R, H, G, T;
@@ -69,6 +70,19 @@ struct TreeArgs {
   int begin;
   float score_log2;              // scale * log2(e)
   float cap_in, cap_out;         // 2 log2(e) scale / cap, cap * log2(e); cap_in 0: no cap
+  // Attention over common prefixes (avsg_prefix_api.cu).  part 0: the keys of a group's prefix,
+  // for the new tokens of all its members; 1: every request's own keys.  No part writes the
+  // output of a request that has a prefix.
+  int part;
+  int places;                    // entries of token and request
+  const int32_t* shared;         // [R] tokens of the prefix
+  const int32_t* group_first;    // [R + 1] a leader's first place
+  const int32_t* token;          // [places] the token in a place, and its request
+  const int32_t* request;
+  int4* unit;                    // [T][H] {CTA of the unit's begin, pieces, its token, prefix}; pieces 0:
+                                 // a row of `rows`, -1: the output is written
+  float* rows;                   // [T][H][G][D] outputs of units that lie in one share
+  float* rows_ml;                // [T][H][G][2]
 };
 
 // Splits of the row count per m-tile, and launchers of one head width each.
@@ -77,6 +91,9 @@ cudaError_t launch_tree_d128(const TreeArgs& a, int dtype, int wm, int dev, cuda
 cudaError_t launch_tree_d256(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 // Pages of at least 8 tokens, 256 rows per m-tile, 128 for D of 256 (avsg_tree_umma.cu).
 cudaError_t launch_tree_umma(const TreeArgs& a, int dtype, int D, int dev, cudaStream_t st);
+// One part of an attention over common prefixes, without the joining of its pieces.
+cudaError_t launch_prefix_part(const TreeArgs& a, int dtype, int D, int wm, int dev, cudaStream_t st);
+cudaError_t launch_prefix_umma(const TreeArgs& a, int dtype, int D, int dev, cudaStream_t st);
 
 namespace tree {
 
@@ -189,17 +206,29 @@ __device__ __forceinline__ float cap_polynomial_reach(float far, float cap_out) 
   return far <= kCapNear || cap_out > kCapLarge ? kCapNear : -1.f;
 }
 
-// One request as the kernels see it.  A request with a bad length is latched
-// and has no work.  Its rows are cut into mts units of tpm tokens per kv-head.
-template <int KT>
-struct Req {
+// One request as the kernels see it (or one group, whose keys are its
+// prefix).  A request with a bad length is latched and has no work.  Its rows
+// are cut into mts units of tpm tokens per kv-head.
+template <bool SHARED>
+struct Fresh {};
+template <>
+struct Fresh<true> {
+  int fresh;                               // new tokens that are keys
+};
+template <int KT, bool SHARED>
+struct Req : Fresh<SHARED> {
   int len, n, f, lo, mts, begin;
   bool chain;
+
+  __device__ int new_keys() const {
+    if constexpr (SHARED) return this->fresh;
+    else return n;
+  }
 
   // Places of unit mt in the list: `begin` for its beginning, then its
   // tiles, counted from key lo, up to the last key that a row may see.
   __device__ int places(int mt, int tpm) const {
-    return begin + (len - lo + (chain ? min(n, (mt + 1) * tpm) : n) + KT - 1) / KT;
+    return begin + (len - lo + (chain ? min(n, (mt + 1) * tpm) : new_keys()) + KT - 1) / KT;
   }
   // Places of the units before mt.
   __device__ long long before(int mt, int tpm) const {
@@ -211,9 +240,31 @@ struct Req {
     return n ? before(mts - 1, tpm) + places(mts - 1, tpm) : 0;
   }
 };
-template <int KT>
-__device__ __forceinline__ Req<KT> load_req(const TreeArgs& a, int r) {
-  Req<KT> q;
+template <int KT, bool SHARED>
+__device__ __forceinline__ Req<KT, SHARED> load_req(const TreeArgs& a, int r) {
+  Req<KT, SHARED> q;
+  if constexpr (SHARED) {
+    const int len = a.len[r], common = a.shared[r], page_mask = (1 << a.shift) - 1;
+    if (a.part == 0) {
+      q.f = a.group_first[r];
+      const int end = a.group_first[r + 1];
+      q.len = common;
+      q.n = end - q.f;
+      q.fresh = 0;
+      q.begin = a.begin;
+      q.chain = false;
+      if (q.f < 0 || end < q.f || end > a.places || common < 0 || common > len || (common & page_mask) != 0 ||
+          (common >> a.shift) > a.max_pages) {
+        raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
+        q.n = 0;
+      }
+      if (common == 0) q.n = 0;
+      // no member is shorter than its prefix: what lies before that one's window nobody sees
+      q.lo = a.window > 0 ? max(0, min(common - a.window + 1, common - 1)) & ~(KT - 1) : 0;
+      q.mts = (q.n + a.tpm - 1) / a.tpm;
+      return q;
+    }
+  }
   q.f = a.first[r];
   const int end = a.first[r + 1];
   q.len = a.len[r];
@@ -230,6 +281,16 @@ __device__ __forceinline__ Req<KT> load_req(const TreeArgs& a, int r) {
   }
   q.chain = !a.mask || q.n > kMaxDrafts;
   q.lo = a.window > 0 && q.len >= a.window ? (q.len - a.window + 1) & ~(KT - 1) : 0;
+  if constexpr (SHARED) {                  // from the prefix on, in tiles counted from there
+    const int common = a.shared[r];
+    if (common < 0 || common > q.len || (common & ((1 << a.shift) - 1)) != 0) {
+      if (q.n) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, -1);
+      q.n = q.len = q.lo = 0;
+    } else {
+      q.lo = common + (a.window > 0 ? max(0, q.len - a.window + 1 - common) & ~(KT - 1) : 0);
+    }
+    q.fresh = q.n;
+  }
   q.mts = (q.n + a.tpm - 1) / a.tpm;
   return q;
 }
@@ -254,29 +315,29 @@ struct Piece {
 };
 
 // Where a CTA's share begins, found by one of its threads.
-template <int KT>
+template <int KT, bool SHARED>
 struct Begin {
-  Req<KT> q;
+  Req<KT, SHARED> q;
   int r;
   long long before;                        // list position of the request's first place
 };
 
 // The CTA's share of the list: every thread walks it alike.
-template <int KT>
+template <int KT, bool SHARED>
 struct Walk {
-  Req<KT> q;
+  Req<KT, SHARED> q;
   long long at, end, W;                    // list positions, length of the list
   int C;                                   // CTAs with a share
   int r, h, mt, ta;                        // ta: the next place of the unit
 
   // Finds the share (all threads of the block; barriers inside).  False: no work, or an
   // error latched before (its word and the lengths are read side by side).
-  __device__ bool begin(const TreeArgs& a, long long* s_warp, Begin<KT>* s_begin) {
+  __device__ bool begin(const TreeArgs& a, long long* s_warp, Begin<KT, SHARED>* s_begin) {
     const bool latched = load_err(a.err) != 0;
     const int per = (a.R + blockDim.x - 1) / blockDim.x;
     const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
     long long mine = 0;
-    for (int i = r0; i < r1; ++i) mine += load_req<KT>(a, i).per_head(a.tpm) * a.H;
+    for (int i = r0; i < r1; ++i) mine += load_req<KT, SHARED>(a, i).per_head(a.tpm) * a.H;
     long long before = block_exclusive(mine, s_warp, &W);
     const long long fit = W / a.min_tiles;
     C = fit < 1 ? 1 : fit < a.ctas ? (int)fit : a.ctas;
@@ -286,7 +347,7 @@ struct Walk {
     end = (cta + 1) * W / C;
     if (before <= at && at < before + mine)
       for (int i = r0; i < r1; ++i) {
-        const Req<KT> req = load_req<KT>(a, i);
+        const Req<KT, SHARED> req = load_req<KT, SHARED>(a, i);
         const long long w = req.per_head(a.tpm) * a.H;
         if (at < before + w) {
           s_begin->q = req;
@@ -332,6 +393,13 @@ struct Walk {
       p.all_see = q.len + (q.chain ? p.tok0 + 1 : 0);
       // (a position is the number of a word's bits, those past the request's tokens too)
       p.far_pos = q.len + (q.chain ? p.tok0 + p.ntok : kMaxDrafts) - 1;
+      if constexpr (SHARED) {
+        if (a.part == 0) {                 // no new token is a key; rows lie anywhere behind
+          p.n = 0;
+          p.limit = q.len;
+          p.far_pos = INT_MAX - 1024;  // (room for sums)
+        }
+      }
       // tiles that lie before the window of every row have no work
       int skip = a.begin;
       if (a.window > 0 && q.chain)
@@ -345,7 +413,7 @@ struct Walk {
           if (++h == a.H) {
             h = 0;
             if (at < end) {
-              do q = load_req<KT>(a, ++r); // (one with work follows: at < end <= W)
+              do q = load_req<KT, SHARED>(a, ++r); // (one with work follows: at < end <= W)
               while (q.n == 0 && r + 1 < a.R);
             }
           }
@@ -364,9 +432,42 @@ struct Walk {
   }
 };
 
-template <typename T_, int D_, int WM_>
+// The token in a row of a piece.
+template <bool SHARED>
+__device__ __forceinline__ int token_of(const TreeArgs& a, const Piece& p, int tok) {
+  if constexpr (SHARED) {
+    if (a.part == 0) {
+      const int t = a.token[p.f + tok];
+      if (t >= 0 && t < a.T) return t;
+      raise_error(a.err, AVSG_ERR_BAD_SELECTION, p.r, p.f + tok);
+      return 0;
+    }
+  }
+  return p.f + tok;
+}
+// The position of that token where it is another request's (part 0), wanted for biases and windows.
+__device__ __forceinline__ int member_position(const TreeArgs& a, const Piece& p, int tok, int t) {
+  const int r = a.request[p.f + tok];
+  if (r < 0 || r >= a.R) {
+    raise_error(a.err, AVSG_ERR_BAD_SELECTION, p.r, p.f + tok);
+    return 0;
+  }
+  const int f = a.first[r];
+  const unsigned long long w = a.mask && a.first[r + 1] - f <= kMaxDrafts ? a.mask[t] : 0;
+  return a.len[r] + (w ? __popcll(w) - 1 : t - f);
+}
+// (SHARED) Notes where the partial outputs of a unit's tokens lie; tid of `threads` threads.
+__device__ __forceinline__ void note_unit(const TreeArgs& a, const Piece& p, int cta, int tid, int threads) {
+  const int prefix = a.part == 1 && a.shared[p.r] > 0;
+  const int pieces = !p.whole ? p.last - cta + 1 : a.part == 1 && !prefix ? -1 : 0;
+  for (int x = tid; x < p.ntok; x += threads)
+    a.unit[(long long)token_of<true>(a, p, p.tok0 + x) * a.H + p.h] = make_int4(cta, pieces, x, prefix);
+}
+
+template <typename T_, int D_, int WM_, bool SHARED_>
 struct Shape {
   using T = T_;
+  static constexpr bool SHARED = SHARED_;
   // Heads of 256 values leave room for one CTA per SM: eight warps, where each can have 16 keys.
   static constexpr int D = D_, WM = WM_, WARPS = D_ == 256 && WM_ > 1 ? 8 : 4, WK = WARPS / WM_, MT = 16 * WM_;
   static constexpr int THREADS = 32 * WARPS;
@@ -388,10 +489,10 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
   constexpr int kThreads = SH::THREADS;
   constexpr int D = SH::D, WM = SH::WM, WK = SH::WK, MT = SH::MT, NK = SH::NK, S = SH::STAGES;
   constexpr int CPR = D / 8;                         // 16-byte chunks per row
-  constexpr bool HALF = std::is_same<T, __half>::value;
+  constexpr bool HALF = std::is_same<T, __half>::value, SHARED = SH::SHARED;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_warp[kThreads / 32];
-  __shared__ Begin<KT> s_begin;
+  __shared__ Begin<KT, SHARED> s_begin;
   __shared__ float s_m[WK][MT], s_l[WK][MT];
   __shared__ int s_depth[kMaxDrafts];
   long long* s_row = reinterpret_cast<long long*>(smem + S * 2 * SH::TILE);
@@ -402,10 +503,12 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
   const int cta = blockIdx.x;
   int4 head = make_int4(0, 0, 0, 0);
 
-  griddep_wait();
-  Walk<KT> walk;
+  // (part 1 of an attention over prefixes may run beside part 0, which it waits for at its end)
+  if (!SHARED || a.part == 0) griddep_wait();
+  Walk<KT, SHARED> walk;
   if (!walk.begin(a, s_warp, &s_begin)) {
-    if (tid == 0) a.head[cta] = head;
+    if (SHARED) griddep_wait();
+    else if (tid == 0) a.head[cta] = head;
     return;
   }
 
@@ -470,12 +573,16 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
       const bool ok = rl < rows;
       tok[x] = ok ? pc.tok0 + lt : -1;                  // -1: a padding row, sees no new token
       q_pos[x] = pc.len + max(tok[x], 0);
-      if (!pc.chain && ok) {
+      int token = pc.f + tok[x];
+      if (SHARED && a.part == 0) {
+        if (ok) token = token_of<SHARED>(a, pc, tok[x]);
+        if (ok && (a.slopes || a.window > 0)) q_pos[x] = member_position(a, pc, tok[x], token);
+      } else if (!pc.chain && ok) {
         bits[x] = a.mask[pc.f + tok[x]];
         if (bits[x]) q_pos[x] = pc.len + __popcll(bits[x]) - 1;
       }
       if (a.slopes && ok) slope[x] = a.slopes[h * a.G + gg] * 1.4426950408889634f;
-      q_row[x] = ok ? a.q + ((long long)(pc.f + tok[x]) * a.q_stride + (long long)(h * a.G + gg) * D) * 2
+      q_row[x] = ok ? a.q + ((long long)token * a.q_stride + (long long)(h * a.G + gg) * D) * 2
                     : nullptr;
     }
     uint32_t qf[SH::Q_SMEM ? 1 : D / 16][4];
@@ -754,7 +861,9 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
       for (int row = 0; row < 2; ++row)
         *reinterpret_cast<float2*>(s_o + (wk * MT + wm * 16 + g + 8 * row) * SH::OP + x * 8 + 2 * c) =
             make_float2(acc[x][2 * row], acc[x][2 * row + 1]);
-    const bool whole = pc.whole;
+    // (SHARED: what goes to the output undivided by its sum is joined later)
+    const bool direct = !SHARED || (a.part == 1 && a.shared[pc.r] == 0);
+    const bool whole = pc.whole && direct;
     const int slot = 2 * cta + (pc.begins ? 1 : 0);
     if (tid < rows) {
       float top = -INFINITY, sum = 0.f;
@@ -778,7 +887,12 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
                          : (top - (HALF ? kHalfShift : 0.f)) * 0.6931471805599453f + logf(sum);
         }
       } else {
-        *reinterpret_cast<float2*>(a.ml + ((long long)slot * MT + tid) * 2) = make_float2(top, sum);
+        float* ml = a.ml + ((long long)slot * MT + tid) * 2;
+        if (SHARED && pc.whole) {
+          const int lt = tid / a.G, gg = tid - lt * a.G;
+          ml = a.rows_ml + ((long long)token_of<SHARED>(a, pc, pc.tok0 + lt) * a.H * a.G + h * a.G + gg) * 2;
+        }
+        *reinterpret_cast<float2*>(ml) = make_float2(top, sum);
       }
     }
     __syncthreads();
@@ -800,12 +914,19 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
         *reinterpret_cast<uint2*>(a.out + (at_row * D + c4) * 2) =
             make_uint2(pack<T>(o.x, o.y), pack<T>(o.z, o.w));
       } else {
-        *reinterpret_cast<float4*>(a.part + ((long long)slot * MT + row) * D + c4) = o;
+        float* part = a.partial + ((long long)slot * MT + row) * D;
+        if (SHARED && pc.whole) {
+          const int lt = row / a.G, gg = row - lt * a.G;
+          part = a.rows + ((long long)token_of<SHARED>(a, pc, pc.tok0 + lt) * a.H * a.G + h * a.G + gg) * D;
+        }
+        *reinterpret_cast<float4*>(part + c4) = o;
       }
     }
+    if (SHARED && pc.begins) note_unit(a, pc, cta, tid, kThreads);
     if (!whole && pc.begins) head = make_int4(pc.last - cta + 1, pc.f + pc.tok0, h, rows);
   }
-  if (tid == 0) a.head[cta] = head;
+  if (SHARED) griddep_wait();
+  else if (tid == 0) a.head[cta] = head;
 }
 
 // Joins the partials of the units that cross CTAs.  WPR warps work on one row,
@@ -851,7 +972,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a
           const float2 ml = *reinterpret_cast<const float2*>(a.ml + slot(i) * 2);
           const float f = ex2(ml.x - use);
           sum += ml.y * f;
-          const float* p = a.part + slot(i) * D + lane * VPL;
+          const float* p = a.partial + slot(i) * D + lane * VPL;
           if constexpr (VPL >= 4) {
 #pragma unroll
             for (int x = 0; x < VPL; x += 4) {
@@ -915,26 +1036,26 @@ cudaError_t launch_merge(const TreeArgs& a, int MT, cudaStream_t st) {
   return launch_pdl(tree_merge_kernel<T, D, 1>, dim3(a.ctas, groups), dim3(kMergeWarps * 32), 0, st, a, MT);
 }
 
-template <typename T, int D, int WM>
+template <typename T, int D, int WM, bool SHARED>
 cudaError_t launch_one(const TreeArgs& a, int dev, cudaStream_t st) {
-  using SH = Shape<T, D, WM>;
+  using SH = Shape<T, D, WM, SHARED>;
   static SmemLimit limit;
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(tree_attn_kernel<SH>), SH::SMEM, dev);
   if (e == cudaSuccess)
     e = launch_pdl(tree_attn_kernel<SH>, dim3(a.ctas), dim3(SH::THREADS), SH::SMEM, st, a);
-  return e != cudaSuccess ? e : launch_merge<T, D>(a, SH::MT, st);
+  return e != cudaSuccess || SHARED ? e : launch_merge<T, D>(a, SH::MT, st);
 }
 
-template <int D>
+template <int D, bool SHARED>
 cudaError_t launch_width(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st) {
   if (dtype == AVSG_BF16) {
-    if (wm == 1) return launch_one<__nv_bfloat16, D, 1>(a, dev, st);
-    if (wm == 2) return launch_one<__nv_bfloat16, D, 2>(a, dev, st);
-    return launch_one<__nv_bfloat16, D, 4>(a, dev, st);
+    if (wm == 1) return launch_one<__nv_bfloat16, D, 1, SHARED>(a, dev, st);
+    if (wm == 2) return launch_one<__nv_bfloat16, D, 2, SHARED>(a, dev, st);
+    return launch_one<__nv_bfloat16, D, 4, SHARED>(a, dev, st);
   }
-  if (wm == 1) return launch_one<__half, D, 1>(a, dev, st);
-  if (wm == 2) return launch_one<__half, D, 2>(a, dev, st);
-  return launch_one<__half, D, 4>(a, dev, st);
+  if (wm == 1) return launch_one<__half, D, 1, SHARED>(a, dev, st);
+  if (wm == 2) return launch_one<__half, D, 2, SHARED>(a, dev, st);
+  return launch_one<__half, D, 4, SHARED>(a, dev, st);
 }
 
 }  // namespace tree

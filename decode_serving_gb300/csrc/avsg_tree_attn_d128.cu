@@ -3,6 +3,6 @@
 
 namespace avsg {
 cudaError_t launch_tree_d128(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st) {
-  return tree::launch_width<128>(a, dtype, wm, dev, st);
+  return tree::launch_width<128, false>(a, dtype, wm, dev, st);
 }
 }  // namespace avsg

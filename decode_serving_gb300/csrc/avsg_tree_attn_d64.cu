@@ -3,6 +3,6 @@
 
 namespace avsg {
 cudaError_t launch_tree_d64(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st) {
-  return tree::launch_width<64>(a, dtype, wm, dev, st);
+  return tree::launch_width<64, false>(a, dtype, wm, dev, st);
 }
 }  // namespace avsg

@@ -1,6 +1,8 @@
 """A paged device cache for decoding with drafted tokens: marshalling around
-avsg_page_plan, avsg_rotary_write, avsg_tree_attention and avsg_tree_keep
-(include/avsg.h has the layouts and the rules).
+avsg_page_plan, avsg_rotary_write, avsg_tree_attention and avsg_tree_keep, and
+for requests that share pages avsg_page_fork, avsg_page_compact,
+avsg_prefix_find and avsg_prefix_attention (include/avsg.h has the layouts and
+the rules).
 
 All tensors are the caller's, contiguous and on one CUDA device; shapes, types
 and devices are checked here (``ValueError``), the rest by the library
@@ -20,6 +22,8 @@ _TYPES = {torch.bfloat16: C.AVSG_BF16, torch.float16: C.AVSG_F16}
 # The argument structures as bytes: a third of the time that filling them field by field takes.
 _ROTARY = struct.Struct("8i3qfi7P")
 _TREE = struct.Struct("5i2fiq7PN")
+_PREFIXES = struct.Struct("2i5P")
+assert _PREFIXES.size == ctypes.sizeof(C.avsg_prefixes)
 assert _ROTARY.size == ctypes.sizeof(C.avsg_rotary) and _TREE.size == ctypes.sizeof(C.avsg_tree)
 
 
@@ -30,7 +34,20 @@ def rotary_frequencies(rot_dim, base=10000.0, factor=1.0, low_turns=1.0, high_tu
     return torch.from_numpy(t[:int(rot_dim) // 2].view(np.int64))
 
 
-_P, _I32 = ctypes.c_void_p, ctypes.c_int32
+def rotary_axes(sections, dealt=False) -> torch.Tensor:
+    """The ``axes`` of ``PagedCache.rotary`` (a host tensor, int32): sections[a] pairs of a head
+    turn by axis a, one section after the other or, ``dealt``, a pair of each axis in turn as
+    long as it has some left."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0:
+        raise ValueError("sections: the number of pairs of each axis is wanted")
+    out = [a for a, n in enumerate(sections) for _ in range(n)]
+    if dealt:
+        out = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+    return torch.tensor(out, dtype=torch.int32)
+
+
+_P, _I32, _SIZE = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _calls = {}
 
 
@@ -39,9 +56,38 @@ def _library():
     if not _calls:
         lib = C.load_library()
         for name, args in (("avsg_page_plan", [_P, _P, _P, _I32, _I32] + [_P] * 5), ("avsg_rotary_write", [_P] * 3),
-                           ("avsg_tree_attention", [_P] * 3), ("avsg_tree_keep", [_P, _P, _P, _I32] + [_P] * 4)):
+                           ("avsg_tree_attention", [_P] * 3), ("avsg_tree_keep", [_P, _P, _P, _I32] + [_P] * 4),
+                           ("avsg_rotary_write_axes", [_P, _P, _I32, _P, _P]),
+                           ("avsg_page_fork", [_P] * 4 + [_SIZE, _P]),
+                           ("avsg_tree_keep_shared", [_P] * 4 + [_I32] + [_P] * 4),
+                           ("avsg_page_compact", [_P] * 7 + [_SIZE, _P]),
+                           ("avsg_prefix_find", [_P, _P, _I32, _P, _P, _SIZE, _P]),
+                           ("avsg_prefix_attention", [_P] * 4)):
             _calls[name] = ctypes.CFUNCTYPE(ctypes.c_int, *args)((name, lib))
     return _calls
+
+
+def _int32(x):
+    """x, if an int32 holds it (struct.error: it does not)."""
+    return struct.unpack("i", struct.pack("i", x))[0]
+
+
+class Prefixes:
+    """Groups of requests with a common prefix, as ``PagedCache.find_prefixes`` writes them: leader
+    and shared [requests], first [requests + 1], token and request [tokens], int32 (avsg_prefixes)."""
+
+    def __init__(self, leader, shared, first, token, request):
+        n, tokens = leader.numel(), token.numel()
+        for name, t, count in (("leader", leader, n), ("shared", shared, n), ("first", first, n + 1),
+                               ("token", token, tokens), ("request", request, tokens)):
+            if t.dtype is not torch.int32 or t.device != leader.device or t.numel() != count or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous torch.int32 tensor of {count} values on "
+                                 f"{leader.device} is wanted, not {t.dtype} {list(t.shape)} on {t.device}")
+        self.leader, self.shared, self.first, self.token, self.request = leader, shared, first, token, request
+        self.requests, self._index = n, leader.get_device()
+        self._args = _PREFIXES.pack(tokens, 0, leader.data_ptr(), shared.data_ptr(), first.data_ptr(),
+                                    token.data_ptr(), request.data_ptr())
 
 
 class PagedCache:
@@ -49,7 +95,8 @@ class PagedCache:
 
     k, v [layers][num_pages][kv_heads][page_tokens][head_dim] bf16 or fp16;
     tables [requests][max_pages], lens [requests], free [num_pages] and
-    free_count [1] int32.  New tokens are ragged rows: request r owns rows
+    free_count [1] int32; shares [num_pages] int32, or None where no page is
+    shared: how many requests hold a page beyond the first (``fork``).  New tokens are ragged rows: request r owns rows
     first[r] .. first[r + 1] of every per-token tensor.
 
     Calls are enqueued on torch's current stream, so that they follow the
@@ -57,7 +104,7 @@ class PagedCache:
     its handle (0: the default stream).
     """
 
-    def __init__(self, k, v, tables, lens, free, free_count):
+    def __init__(self, k, v, tables, lens, free, free_count, shares=None):
         if k.dim() != 5 or v.shape != k.shape or k.dtype not in _TYPES or v.dtype != k.dtype:
             raise ValueError("k and v: [layers][num_pages][kv_heads][page_tokens][head_dim], "
                              "both bfloat16 or both float16")
@@ -78,6 +125,9 @@ class PagedCache:
         self._check("lens", lens, torch.int32, len(lens))
         self._check("free", free, torch.int32, pages)
         self._check("free_count", free_count, torch.int32, 1)
+        self.shares, self.pages, self.max_pages = shares, pages, tables.shape[1]
+        if shares is not None:
+            self._check("shares", shares, torch.int32, pages)
         self._error = torch.zeros(4, dtype=torch.int32, device=k.device)
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(k.device).synchronize()  # (any stream may read it from here on)
@@ -89,17 +139,20 @@ class PagedCache:
         calls = _library()
         self._plan, self._rotary = calls["avsg_page_plan"], calls["avsg_rotary_write"]
         self._attend, self._keep = calls["avsg_tree_attention"], calls["avsg_tree_keep"]
+        self._calls = calls
 
     @classmethod
     def allocate(cls, requests, max_pages, num_pages, kv_heads, page_tokens, head_dim, layers=1,
-                 dtype=torch.bfloat16, device="cuda") -> "PagedCache":
-        """An empty cache: no tokens, every page free (taken from 0 upward)."""
+                 dtype=torch.bfloat16, device="cuda", sharing=False) -> "PagedCache":
+        """An empty cache: no tokens, every page free (taken from 0 upward); with ``sharing`` its
+        requests can share pages."""
         shape = (layers, num_pages, kv_heads, page_tokens, head_dim)
         ints = dict(dtype=torch.int32, device=device)
         return cls(torch.zeros(shape, dtype=dtype, device=device),
                    torch.zeros(shape, dtype=dtype, device=device),
                    torch.zeros(requests, max_pages, **ints), torch.zeros(requests, **ints),
-                   torch.arange(num_pages - 1, -1, -1, **ints), torch.full((1,), num_pages, **ints))
+                   torch.arange(num_pages - 1, -1, -1, **ints), torch.full((1,), num_pages, **ints),
+                   torch.zeros(num_pages, **ints) if sharing else None)
 
     def _check(self, name, t, dtype, count):
         """t: contiguous, of this type and this many values, on the cache's device."""
@@ -158,13 +211,15 @@ class PagedCache:
             raise C.AvsgError(rc, "avsg_page_plan")
 
     def rotary(self, q, k, v, positions, slots, freq, q_out, layer=0, rot_offset=0,
-               interleaved=False, magnitude=1.0, tokens_per_request=1, stream=None):
+               interleaved=False, magnitude=1.0, tokens_per_request=1, stream=None, axes=None):
         """Rotates q into q_out and k into the pages, stores v beside it.
 
         q [T][q_heads * head_dim] (or [T][q_heads][head_dim]), k and v like it
         with kv_heads, any stride between tokens; slots [T] or None (slot t for
         token t); freq from ``rotary_frequencies``, on the device; q_out
-        contiguous, the cache's type or float32."""
+        contiguous, the cache's type or float32.  axes [pairs] int32
+        (``rotary_axes``, on the device): positions are [axes][T], and a pair
+        turns by the position on its axis."""
         heads, tokens, dim = self._heads(q), q.shape[0], self.head_dim
         kv = self.kv_heads * dim
         qs, ks, vs = self._rows("q", q, heads * dim), self._rows("k", k, kv), self._rows("v", v, kv)
@@ -173,7 +228,13 @@ class PagedCache:
         f32 = q_out.dtype is torch.float32
         pairs = freq.numel()
         self._check("q_out", q_out, torch.float32 if f32 else self.dtype, tokens * heads * dim)
-        self._check("positions", positions, torch.int32, tokens)
+        if axes is None:
+            self._check("positions", positions, torch.int32, tokens)
+        else:
+            if positions.dim() != 2 or positions.shape[0] < 1:
+                raise ValueError("positions: [axes][tokens] is wanted")
+            self._check("positions", positions, torch.int32, positions.shape[0] * tokens)
+            self._check("axes", axes, torch.int32, pairs)
         self._check("freq", freq, torch.int64, pairs)
         if slots is not None:
             self._check("slots", slots, torch.int32, tokens)
@@ -184,7 +245,11 @@ class PagedCache:
                 0 if slots is None else slots.data_ptr(), q_out.data_ptr())
         except struct.error as e:                      # a number that its field does not hold
             raise ValueError(str(e)) from None
-        rc = self._rotary(self._at, args, self._stream(stream))
+        if axes is None:
+            rc = self._rotary(self._at, args, self._stream(stream))
+        else:
+            rc = self._calls["avsg_rotary_write_axes"](self._at, args, positions.shape[0], axes.data_ptr(),
+                                                       self._stream(stream))
         if rc:
             raise C.AvsgError(rc, "avsg_rotary_write")
 
@@ -201,6 +266,13 @@ class PagedCache:
         contiguous, lse [T][q_heads] float32 or None; first from ``plan``;
         max_new bounds every request's new tokens; mask [tokens] int64 words
         (None: chains); slopes [q_heads] float32 or None."""
+        args = self._tree(q, first, out, max_new, work, mask, lse, layer, scale, softcap, window, slopes)
+        rc = self._attend(self._at, args, self._stream(stream))
+        if rc:
+            raise C.AvsgError(rc, "avsg_tree_attention")
+
+    def _tree(self, q, first, out, max_new, work, mask, lse, layer, scale, softcap, window, slopes):
+        """The packed arguments of an attention."""
         heads, tokens, dim = self._heads(q), q.shape[0], self.head_dim
         stride = self._rows("q", q, heads * dim)
         if heads % self.kv_heads:
@@ -218,20 +290,18 @@ class PagedCache:
         if slopes is not None:
             self._check("slopes", slopes, torch.float32, heads)
         try:
-            args = _TREE.pack(
+            return _TREE.pack(
                 tokens, heads // self.kv_heads, max_new, layer, window, scale, softcap, 0, stride, q.data_ptr(),
                 first.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if slopes is None else slopes.data_ptr(),
                 out.data_ptr(), 0 if lse is None else lse.data_ptr(), work.data_ptr(), size)
         except struct.error as e:                      # a number that its field does not hold
             raise ValueError(str(e)) from None
-        rc = self._attend(self._at, args, self._stream(stream))
-        if rc:
-            raise C.AvsgError(rc, "avsg_tree_attention")
 
     def keep(self, first, path, keep, lens_out=None, free_count_out=None, stream=None):
         """Keeps the accepted drafts of every layer and frees the pages past the
         new lengths.  keep [requests] int32: kept tokens, or -1: the request
-        ends; path [tokens] int32 or None: the first keep[r] ones."""
+        ends (one that holds shared pages ends by ``fork``); path [tokens]
+        int32 or None: the first keep[r] ones."""
         r = self.requests
         lens = self.lens if lens_out is None else lens_out
         count = self.free_count if free_count_out is None else free_count_out
@@ -243,10 +313,111 @@ class PagedCache:
         if path is not None:
             paths = path.numel()
             self._check("path", path, torch.int32, paths)
-        rc = self._keep(self._at, first.data_ptr(), None if path is None else path.data_ptr(), paths,
-                        keep.data_ptr(), lens.data_ptr(), count.data_ptr(), self._stream(stream))
+        args = (first.data_ptr(), None if path is None else path.data_ptr(), paths, keep.data_ptr(),
+                lens.data_ptr(), count.data_ptr(), self._stream(stream))
+        if self.shares is None:
+            rc = self._keep(self._at, *args)
+        else:
+            rc = self._calls["avsg_tree_keep_shared"](self._at, self.shares.data_ptr(), *args)
         if rc:
             raise C.AvsgError(rc, "avsg_tree_keep")
+
+    def _workspace(self, size):
+        return torch.empty(size, dtype=torch.uint8, device=self.device)
+
+    def fork_workspace(self) -> torch.Tensor:
+        """Scratch of ``fork``; calls that may overlap need one each."""
+        return self._workspace(C.avsg_page_fork_workspace(self._pages))
+
+    def fork(self, parent, work, stream=None):
+        """Request r goes on as what request parent[r] was: itself, a copy of
+        another that shares its full pages, or (-1) nothing.  parent
+        [requests] int32.  Tables, lengths, shares and free pages change in
+        place; between steps, when every token is committed."""
+        if self.shares is None:
+            raise ValueError("the cache has no shares: its requests cannot share pages")
+        self._check("parent", parent, torch.int32, self.requests)
+        size = work.numel()
+        self._check("work", work, torch.uint8, size)
+        rc = self._calls["avsg_page_fork"](self._at, parent.data_ptr(), self.shares.data_ptr(), work.data_ptr(),
+                                           size, self._stream(stream))
+        if rc:
+            raise C.AvsgError(rc, "avsg_page_fork")
+
+    def compact_workspace(self) -> torch.Tensor:
+        """Scratch of ``compact``; calls that may overlap need one each."""
+        return self._workspace(C.avsg_page_compact_workspace(self._pages))
+
+    def compact(self, page_map, work, tables_out=None, free_out=None, shares_out=None, stream=None):
+        """Moves the pages in use to the front of the pool, whole and in all
+        layers.  page_map [num_pages] int32 receives each page's new id, -1
+        for a free one; tables, free pages and shares change in place unless
+        others are given for them."""
+        tables = self.tables if tables_out is None else tables_out
+        free = self.free if free_out is None else free_out
+        shares = self.shares if shares_out is None else shares_out
+        self._check("page_map", page_map, torch.int32, self.pages)
+        self._check("tables_out", tables, torch.int32, self.requests * self.max_pages)
+        self._check("free_out", free, torch.int32, self.pages)
+        old, new = None, None
+        if self.shares is not None:
+            self._check("shares_out", shares, torch.int32, self.pages)
+            old, new = self.shares.data_ptr(), shares.data_ptr()
+        elif shares is not None:
+            raise ValueError("shares_out: the cache has no shares")
+        size = work.numel()
+        self._check("work", work, torch.uint8, size)
+        rc = self._calls["avsg_page_compact"](self._at, old, new, tables.data_ptr(), free.data_ptr(),
+                                              page_map.data_ptr(), work.data_ptr(), size, self._stream(stream))
+        if rc:
+            raise C.AvsgError(rc, "avsg_page_compact")
+
+    def prefix_arrays(self, tokens) -> Prefixes:
+        """Arrays for the groups of steps of up to so many new tokens (no groups yet)."""
+        ints = dict(dtype=torch.int32, device=self.device)
+        return Prefixes(torch.arange(self.requests, **ints), torch.zeros(self.requests, **ints),
+                        torch.zeros(self.requests + 1, **ints), torch.full((tokens,), -1, **ints),
+                        torch.full((tokens,), -1, **ints))
+
+    def prefix_workspace(self) -> torch.Tensor:
+        """Scratch of ``find_prefixes``; calls that may overlap need one each."""
+        return self._workspace(C.avsg_prefix_find_workspace(self._pages))
+
+    def _prefixes(self, prefixes):
+        if prefixes.requests != self.requests or prefixes._index != self._index:
+            raise ValueError(f"prefixes: arrays of {self.requests} requests on {self.device} are wanted")
+        return prefixes._args
+
+    def find_prefixes(self, first, prefixes, work, min_tokens=256, stream=None):
+        """Finds the groups of requests with new tokens whose tables begin
+        with the same pages, at least min_tokens of committed tokens, and
+        lists each group's new tokens; once per step, after ``plan``.  first
+        from ``plan``."""
+        self._check("first", first, torch.int32, self.requests + 1)
+        size = work.numel()
+        self._check("work", work, torch.uint8, size)
+        try:
+            least = _int32(min_tokens)
+        except struct.error as e:
+            raise ValueError(str(e)) from None
+        rc = self._calls["avsg_prefix_find"](self._at, first.data_ptr(), least, self._prefixes(prefixes),
+                                             work.data_ptr(), size, self._stream(stream))
+        if rc:
+            raise C.AvsgError(rc, "avsg_prefix_find")
+
+    def attend_prefixes_workspace(self, q_per_kv, max_new, tokens) -> torch.Tensor:
+        """Scratch of ``attend_prefixes`` for up to so many rows of q; calls that may overlap need one each."""
+        return self._workspace(C.avsg_prefix_attention_workspace(self._pages, q_per_kv, max_new, tokens))
+
+    def attend_prefixes(self, q, first, prefixes, out, max_new, work, mask=None, lse=None, layer=0, scale=0.0,
+                        softcap=0.0, window=0, slopes=None, stream=None):
+        """``attend`` with every group's prefix read and multiplied once for
+        all of its members; prefixes from ``find_prefixes``, for the same
+        tables, lengths and first."""
+        args = self._tree(q, first, out, max_new, work, mask, lse, layer, scale, softcap, window, slopes)
+        rc = self._calls["avsg_prefix_attention"](self._at, args, self._prefixes(prefixes), self._stream(stream))
+        if rc:
+            raise C.AvsgError(rc, "avsg_prefix_attention")
 
     def error(self):
         """(code, request, position) of the first latched device error, code 0

@@ -361,9 +361,9 @@ int avsg_read_rows(const void* src, int64_t num_rows, int64_t row_bytes, const i
  * the device until the caller zeroes it.  avsg_page_plan calls on one d_error
  * must not run at the same time.  All memory is the caller's, on the
  * current device (INVALID_ARG for pages of another one), and must stay valid
- * until the enqueued work is done.  A page belongs to one request: requests
- * that share one (a common prompt) are not supported, avsg_tree_keep would
- * give it back twice.  Calls on several streams are independent
+ * until the enqueued work is done.  A page belongs to one request unless
+ * avsg_page_fork shares it; a cache with shared pages is kept by
+ * avsg_tree_keep_shared, as avsg_tree_keep would give a shared page back twice.  Calls on several streams are independent
  * as long as nothing that one of them writes is used by another at a time.
  */
 #define AVSG_BF16 0
@@ -533,6 +533,116 @@ int avsg_tree_attention(const avsg_pages* p, const avsg_tree* t, void* stream);
 int avsg_tree_keep(const avsg_pages* p, const int32_t* d_first, const int32_t* d_path,
                    int32_t num_path, const int32_t* d_keep, int32_t* d_len_out, int32_t* d_free_count_out,
                    void* stream);
+
+/*
+ * Rotary positions of several axes (time, height, width of an image's or a
+ * video's patches): as avsg_rotary_write, but r->d_pos is int32 [num_axes][T]
+ * and pair i of a head turns by the position on axis d_axis[i] (device int32
+ * [rot_dim / 2], each in [0, num_axes): else BAD_SELECTION is latched and nothing
+ * is written).
+ */
+int avsg_rotary_write_axes(const avsg_pages* p, const avsg_rotary* r, int32_t num_axes,
+                           const int32_t* d_axis, void* stream);
+
+/*
+ * Shared pages.  Requests with a common beginning (samples of one prompt, beams,
+ * a batch behind one system prompt) hold the same full pages: d_shares[page],
+ * int32 [num_pages], counts the requests that hold a page beyond the first; it is 0 for
+ * free pages and for pages of one request, so a new cache's is all zeros.
+ * avsg_page_plan, avsg_rotary_write and both attentions take such a cache as
+ * it is: new tokens never lie in a shared page.
+ *
+ * avsg_page_fork -- requests continue as copies of others.
+ *   d_parent : int32 [R]: request r becomes what request d_parent[r] was
+ *              (itself: it stays; -1: it ends, with length 0 and no pages).
+ *              Several may have the same parent, and a parent may itself
+ *              become another: samples, beams that replace beams, ends.
+ * The full pages of the parent's committed tokens are shared.  Its partly
+ * filled last page stays with the parent if that stays, else goes to its
+ * lowest child; every other child takes a page from the stack (in request
+ * order) and the filled rows are copied there in all layers.  Pages that
+ * nobody holds any more go back after that, in the reverse order of taking, listed by
+ * the highest request that held them and by column.  Tables, lengths, shares, stack and count
+ * change in place; table entries behind a request's pages are left as they are.  New tokens that are
+ * not committed (avsg_tree_keep) are not looked at: fork between steps.
+ * Latched errors (BAD_SELECTION: a parent, length, page id or count out of
+ * range; CAPACITY: too few free pages or table columns, or more pages than the pool) leave everything as
+ * it was.  d_work: 256-byte aligned, any contents; max_pages up to 2^30.
+ */
+int avsg_page_fork_workspace(const avsg_pages* p, size_t* bytes);
+int avsg_page_fork(const avsg_pages* p, const int32_t* d_parent, int32_t* d_shares, void* d_work,
+                   size_t work_bytes, void* stream);
+
+/*
+ * avsg_tree_keep_shared -- avsg_tree_keep for a cache with shared pages.  A
+ * request that ends here (d_keep -1) and holds a shared page latches
+ * BAD_SELECTION, and everything stays as it was: such requests end by avsg_page_fork.
+ */
+int avsg_tree_keep_shared(const avsg_pages* p, const int32_t* d_shares, const int32_t* d_first,
+                          const int32_t* d_path, int32_t num_path, const int32_t* d_keep, int32_t* d_len_out,
+                          int32_t* d_free_count_out, void* stream);
+
+/*
+ * avsg_page_compact -- the pages in use move to the front of the pool.
+ * Pages in use are those that are not on the stack, whoever holds them.  With
+ * n of them, the i-th of those at or above n (by id) moves to the i-th free
+ * id below n, whole and in all layers; pages above n can then be given to something
+ * else, or the pool cut off there.
+ *   d_shares, d_shares_out : as above, both or neither NULL.
+ *   d_tables_out : [R][max_pages], receives the tables (entries behind a
+ *                  request's pages as they were).
+ *   d_free_out   : [num_pages], receives the stack: pages are taken from n upward
+ *                  (entries at or above the count, which stays, as they were).
+ *   d_map        : int32 [num_pages], receives each page's new id, -1 for a free one.
+ * Each output may be the input itself (d_tables, d_free, d_shares); outputs that are not
+ * leave the input as it was.  Latched errors (BAD_SELECTION: an id out of
+ * range or twice on the stack, a held page that is free, a negative length; CAPACITY: more tokens than the
+ * table holds) leave everything as it was.  d_work: 256-byte aligned, any contents; max_pages up to 2^30.
+ */
+int avsg_page_compact_workspace(const avsg_pages* p, size_t* bytes);
+int avsg_page_compact(const avsg_pages* p, const int32_t* d_shares, int32_t* d_shares_out, int32_t* d_tables_out,
+                      int32_t* d_free_out, int32_t* d_map, void* d_work, size_t work_bytes, void* stream);
+
+/* Groups of requests with a common prefix, and their new tokens in order. */
+typedef struct avsg_prefixes {
+  int32_t num_tokens;   /* entries of d_token and d_request: at least the step's new tokens */
+  int32_t reserved0;    /* must be 0 */
+  int32_t* d_leader;    /* [R] the lowest request of the group, the request itself if it is alone */
+  int32_t* d_shared;    /* [R] tokens of the group's prefix, whole pages; 0: alone */
+  int32_t* d_first;     /* [R + 1] first place of the group that the request leads (exclusive sum) */
+  int32_t* d_token;     /* [num_tokens] the token in each place, -1 behind the last */
+  int32_t* d_request;   /* [num_tokens] its request, -1 behind the last */
+} avsg_prefixes;
+
+/*
+ * avsg_prefix_find -- finds the step's groups from the tables (once per step,
+ * after avsg_page_plan; every layer's attention uses them).  Requests with new
+ * tokens whose tables begin with the same page form a group, if the full
+ * pages that all of them have in common hold at least min_tokens committed
+ * tokens (and there are two members).  d_first: as written by avsg_page_plan.
+ * Latched errors (BAD_SELECTION: a negative length, bad first tokens, a first
+ * page outside the pool; CAPACITY: more full pages than columns) leave the outputs as they were.
+ * d_work: 256-byte aligned, any contents; max_pages up to 2^30.
+ */
+int avsg_prefix_find_workspace(const avsg_pages* p, size_t* bytes);
+int avsg_prefix_find(const avsg_pages* p, const int32_t* d_first, int32_t min_tokens, const avsg_prefixes* x,
+                     void* d_work, size_t work_bytes, void* stream);
+
+/*
+ * avsg_prefix_attention -- avsg_tree_attention in which the keys of a group's
+ * prefix are read and multiplied once for the new tokens of all its members.
+ * The same results up to rounding: masks, chains, positions, caps, biases and
+ * windows are those of avsg_tree_attention, whatever the groups are.
+ *   t : as for avsg_tree_attention; t->d_work and t->work_bytes go by this
+ *       operator's workspace, which grows with the tokens.
+ *   x : the groups, as avsg_prefix_find wrote them for these tables, lengths
+ *       and first tokens (arrays that do not fit them give undefined results;
+ *       indices out of range are latched: BAD_SELECTION).
+ * Every member's d_shared[r] must be its leader's.  Errors and rounding as avsg_tree_attention.
+ */
+int avsg_prefix_attention_workspace(const avsg_pages* p, int32_t q_per_kv, int32_t max_new, int32_t num_tokens,
+                                    size_t* bytes);
+int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, const avsg_prefixes* x, void* stream);
 
 /* Error text, and the cudaError_t behind the last AVSG_ERR_CUDA of a handle. */
 const char* avsg_strerror(int code);
