@@ -40,6 +40,21 @@ struct SmemLimit {
   }
 };
 
+// Asks once per device for the shared memory split that the attention kernels have: a kernel of another
+// one would wait until the SM is empty.
+struct SmemSplit {
+  bool done[kMaxDevicesPaged] = {};
+  cudaError_t ask(const void* kernel, int dev) {
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+  }
+};
+
 // Exclusive prefix of v over the block's threads; *total receives the sum.
 // s_warp: one slot per warp, reusable after the next __syncthreads.
 template <typename T>

@@ -12,9 +12,10 @@
 //           behind the prefix (all of them where it has none, and then the output itself);
 // and a kernel that joins a row's pieces of both.  The parts are launches of
 // their own: a group has many rows and a long prefix (tcgen05's work), a request often few rows
-// and few keys of its own (mma.sync's).  Part 1 does not wait for part 0
-// before it begins -- its blocks fill SMs that part 0 leaves -- but before it ends,
-// so that what follows it follows both.
+// and few keys of its own (mma.sync's).  They run side by side: part 1 does
+// not wait for part 0 before it begins, only before it ends, so that what follows it follows
+// both; and each part's list is cut into as many shares as its cost gives it
+// SMs, the CTAs behind that leave at once.
 #include "avsg_tree_plan.cuh"
 
 namespace avsg {
@@ -39,20 +40,26 @@ struct JoinArgs {
   int R, H, G, T;
 };
 
-// A warp joins the pieces of one row.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(JoinArgs a) {
-  constexpr int VPL = D / 32;
+// WPR warps join the pieces of one row, each every WPR-th of them.  Two dependent chains of loads: where the pieces lie, then
+// their maxima, sums and outputs side by side, up to kJoinAhead outputs before the first weight is known.
+// What bounds it is how many rows are on their way, hence few registers.
+constexpr int join_blocks(int D, int WPR) { return D == 256 ? 3 : WPR == 1 ? 8 : 5; }
+template <typename T, int D, int WPR>
+__global__ void __launch_bounds__(kJoinThreads, join_blocks(D, WPR)) prefix_join_kernel(JoinArgs a) {
+  constexpr int VPL = D / 32, ROWS = kJoinThreads / 32 / WPR, kJoinAhead = WPR == 1 && D < 256 ? 2 : 4;
+  __shared__ float s_o[WPR > 1 ? kJoinThreads / 32 : 1][D], s_ml[kJoinThreads / 32][2];
   griddep_wait();
-  if (load_err(a.err) != 0) return;
-  const int lane = threadIdx.x & 31, heads = a.H * a.G;
-  const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.H * a.G;
+  const int part = warp % WPR;             // of the row's warps
+  const long long row = (long long)blockIdx.x * ROWS + warp / WPR;
   const int t = (int)(row / heads), hg = (int)(row - (long long)t * heads), h = hg / a.G, g = hg - h * a.G;
-  if (t >= a.T || t >= a.first[a.R]) return;
+  if (t >= a.T) return;
+  const int tokens = a.first[a.R], latched = load_err(a.err);
   const int4 own = a.part[1].unit[(long long)t * a.H + h];
-  if (own.y < 0) return;                   // written by its part
-  int4 pre = make_int4(0, -1, 0, 0);
-  if (own.w) pre = a.part[0].unit[(long long)t * a.H + h];
+  int4 pre = a.part[0].unit[(long long)t * a.H + h];  // (any contents, where the token has no prefix)
+  // (own.y < 0: written by its part; a row's warps all leave or none)
+  if (latched != 0 || t >= tokens || own.y < 0) return;
+  if (!own.w) pre = make_int4(0, -1, 0, 0);
   auto pieces = [&](const int4& u) { return u.y < 0 ? 0 : u.y == 0 ? 1 : u.y; };
   auto fits = [&](const JoinPart& p, const int4& u) {
     return u.y <= 0 || (u.x >= 0 && u.x < p.ctas && u.y <= p.ctas - u.x && u.z >= 0 && u.z < p.MT / a.G);
@@ -62,9 +69,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(JoinArgs a) {
     if (lane == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, t);
     return;
   }
-  const int n0 = pieces(pre), n = n0 + pieces(own);
-  // place of piece i: its row among the part's partials or rows
-  auto place = [&](int i, const float*& ml, const float*& o) {
+  const int n0 = pieces(pre), all = n0 + pieces(own);
+  const int n = (all - part + WPR - 1) / WPR;  // this warp's
+  // where piece i lies among the part's partials or rows
+  auto place = [&](int k, const float*& ml, const float*& o) {
+    const int i = k * WPR + part;
     const bool second = i >= n0;
     const JoinPart& p = a.part[second];
     const int4 u = second ? own : pre;
@@ -89,6 +98,24 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(JoinArgs a) {
       place(i0 + lane, ml, from);
       y = *reinterpret_cast<const float2*>(ml);
     }
+    const int most = min(32, n - i0);
+    float z[kJoinAhead][VPL];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j) {
+        const float* p = reinterpret_cast<const float*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(from), (j0 + j) & 31)) + lane * VPL;
+        if (j0 + j < most) {
+          if constexpr (VPL >= 4) {
+#pragma unroll
+            for (int x = 0; x < VPL; x += 4) *reinterpret_cast<float4*>(z[j] + x) = *reinterpret_cast<const float4*>(p + x);
+          } else {
+            *reinterpret_cast<float2*>(z[j]) = *reinterpret_cast<const float2*>(p);
+          }
+        }
+      }
+    };
+    fetch(0);
     float now = y.x;
 #pragma unroll
     for (int d = 16; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
@@ -102,26 +129,43 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(JoinArgs a) {
     sum = sum * old + add;
 #pragma unroll
     for (int x = 0; x < VPL; ++x) o[x] *= old;
-    const int most = min(32, n - i0);
-#pragma unroll 4
-    for (int j = 0; j < most; ++j) {
-      const float w = __shfl_sync(0xffffffffu, f, j);
-      const float* p = reinterpret_cast<const float*>(
-                           __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), j)) + lane * VPL;
-      if constexpr (VPL >= 4) {
+    for (int j0 = 0; j0 < most; j0 += kJoinAhead) {
+      if (j0 > 0) fetch(j0);
 #pragma unroll
-        for (int x = 0; x < VPL; x += 4) {
-          const float4 z = *reinterpret_cast<const float4*>(p + x);
-          o[x] += z.x * w;
-          o[x + 1] += z.y * w;
-          o[x + 2] += z.z * w;
-          o[x + 3] += z.w * w;
-        }
-      } else {
-        const float2 z = *reinterpret_cast<const float2*>(p);
-        o[0] += z.x * w;
-        o[1] += z.y * w;
+      for (int j = 0; j < kJoinAhead; ++j) {
+        const float w = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+        if (j0 + j < most)
+#pragma unroll
+          for (int x = 0; x < VPL; ++x) o[x] += z[j][x] * w;
       }
+    }
+  }
+  if constexpr (WPR > 1) {
+    // the row's warps: one barrier of theirs, as other rows of the block may have left
+#pragma unroll
+    for (int x = 0; x < VPL; ++x) s_o[warp][lane * VPL + x] = o[x];
+    if (lane == 0) {
+      s_ml[warp][0] = top;
+      s_ml[warp][1] = sum;
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WPR), "n"(32 * WPR) : "memory");
+    if (part != 0) return;
+    float tops[WPR];
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      tops[w] = s_ml[warp + w][0];
+      top = fmaxf(top, tops[w]);
+    }
+    const float use = top == -INFINITY ? 0.f : top;
+    sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < VPL; ++x) o[x] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float f = tree::ex2(tops[w] - use);
+      sum += s_ml[warp + w][1] * f;
+#pragma unroll
+      for (int x = 0; x < VPL; ++x) o[x] += s_o[warp + w][lane * VPL + x] * f;
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -135,18 +179,30 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(JoinArgs a) {
   }
 }
 
-template <typename T>
-cudaError_t launch_join(const JoinArgs& a, int D, cudaStream_t st) {
+template <typename T, int D, int WPR>
+cudaError_t launch_join_one(const JoinArgs& a, int dev, cudaStream_t st) {
+  constexpr int ROWS = kJoinThreads / 32 / WPR;
+  static SmemSplit split;
+  auto kernel = prefix_join_kernel<T, D, WPR>;
+  const cudaError_t e = split.ask(reinterpret_cast<const void*>(kernel), dev);
+  if (e != cudaSuccess) return e;
   const long long rows = (long long)a.T * a.H * a.G;
-  const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))), block(kJoinThreads);
-  return D == 64    ? launch_pdl(prefix_join_kernel<T, 64>, grid, block, 0, st, a)
-         : D == 128 ? launch_pdl(prefix_join_kernel<T, 128>, grid, block, 0, st, a)
-                    : launch_pdl(prefix_join_kernel<T, 256>, grid, block, 0, st, a);
+  return launch_pdl(kernel, dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(kJoinThreads), 0, st, a);
 }
-
-// The kernel of part 0: every new token may be a row of one group.
-Plan plan_prefix(const avsg_pages* p, int G, int num_tokens, int sms) {
-  return plan_attention(p, G, num_tokens, sms);
+template <typename T, int D>
+cudaError_t launch_join_width(const JoinArgs& a, int sms, int dev, cudaStream_t st) {
+  const long long rows = (long long)a.T * a.H * a.G;
+  // few rows may have many pieces each: several warps a row as long as all blocks fit the SMs at once
+  const long long fit = (long long)sms * join_blocks(D, 4) * (kJoinThreads / 32);
+  if (rows * 4 <= fit) return launch_join_one<T, D, 4>(a, dev, st);
+  if (rows * 2 <= fit) return launch_join_one<T, D, 2>(a, dev, st);
+  return launch_join_one<T, D, 1>(a, dev, st);
+}
+template <typename T>
+cudaError_t launch_join(const JoinArgs& a, int D, int sms, int dev, cudaStream_t st) {
+  return D == 64    ? launch_join_width<T, 64>(a, sms, dev, st)
+         : D == 128 ? launch_join_width<T, 128>(a, sms, dev, st)
+                    : launch_join_width<T, 256>(a, sms, dev, st);
 }
 
 struct PrefixWork {
@@ -203,10 +259,25 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
   a.group_first = x->d_first;
   a.token = x->d_token;
   a.request = x->d_request;
+  a.sms = sms;
+  a.lead = 1000;                           // 10 us
   JoinArgs j{};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Plan plans[2] = {plan_attention(p, G, t->num_tokens, sms), plan_attention(p, G, t->max_new, sms)};
   for (int i = 0; i < 2; ++i) {
-    const Plan plan = i == 0 ? plan_prefix(p, G, t->num_tokens, sms) : plan_attention(p, G, t->max_new, sms);
+    Plan& plan = plans[i];
+    // a unit takes 4 us and 1.2 a tile with mma.sync; on tcgen05 9 us and 1.6, with up to 128 rows 7.7 and 1.1
+    plan.begin = !plan.umma ? 3 : i == 0 ? 6 : 7;
+    a.cost[i].keys = plan.umma && D != 256 ? 128 : 64;
+    a.cost[i].tpm = plan.MT / G;
+    a.cost[i].begin = plan.begin;
+    // (in hundredths of a microsecond; part 1, whose units end one by one, counts a fifth more)
+    a.cost[i].tile = plan.tile * (i == 0 ? 10 : 12);
+    a.cost[i].small = plan.small * (i == 0 ? 10 : 12);
+    a.cost[i].per_sm = plan.ctas / sms;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const Plan& plan = plans[i];
     const Workspace l = tree_layout(plan, D);
     TreeArgs b = a;
     b.part = i;
@@ -217,7 +288,14 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
     b.partial = reinterpret_cast<float*>(work + w.part[i] + l.part);
     b.tpm = plan.MT / G;
     b.ctas = plan.ctas;
-    b.begin = plan.begin;
+    b.w_full = b.w_small = 1;
+    if (i == 0 && plan.umma && D != 256) {
+      b.w_full = 3;
+      b.w_small = 2;
+      b.small_rows = plan.MT / 2;
+    }
+    b.begin = plan.begin * b.w_full;
+    b.min_tiles = 2 * b.w_full;
     j.part[i] = JoinPart{b.unit, b.rows, b.rows_ml, b.partial, b.ml, plan.ctas, plan.MT};
     const cudaError_t e = plan.umma ? launch_prefix_umma(b, p->dtype, D, dev, st)
                                     : launch_prefix_part(b, p->dtype, D, plan.wm, dev, st);
@@ -232,6 +310,6 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
   j.G = G;
   j.T = a.T;
   const cudaError_t e =
-      p->dtype == AVSG_BF16 ? launch_join<__nv_bfloat16>(j, D, st) : launch_join<__half>(j, D, st);
+      p->dtype == AVSG_BF16 ? launch_join<__nv_bfloat16>(j, D, sms, dev, st) : launch_join<__half>(j, D, sms, dev, st);
   return e == cudaSuccess ? AVSG_OK : AVSG_ERR_CUDA;
 }

@@ -74,6 +74,17 @@ struct TreeArgs {
   // for the new tokens of all its members; 1: every request's own keys.  No part writes the
   // output of a request that has a prefix.
   int part;
+  // How the SMs are divided between the parts, by what their lists cost (in hundredths of an SM's
+  // microsecond; nothing but the time depends on it).
+  struct Cost {
+    int keys, tpm, begin;        // keys of a tile, tokens per m-tile, see `begin`
+    int tile, small;             // of a tile, with more than half an m-tile's rows and with fewer
+    int per_sm;                  // CTAs
+  } cost[2];
+  // Places of a tile in the list, of m-tiles with up to small_rows rows and with more.
+  int w_small, w_full, small_rows;
+  int sms;
+  int lead;                      // part 0's begin and end beyond part 1's, in hundredths of a microsecond
   int places;                    // entries of token and request
   const int32_t* shared;         // [R] tokens of the prefix
   const int32_t* group_first;    // [R + 1] a leader's first place
@@ -214,6 +225,7 @@ struct Fresh {};
 template <>
 struct Fresh<true> {
   int fresh;                               // new tokens that are keys
+  int w, w_last;                           // places of a tile, of the last m-tile's
 };
 template <int KT, bool SHARED>
 struct Req : Fresh<SHARED> {
@@ -227,12 +239,20 @@ struct Req : Fresh<SHARED> {
 
   // Places of unit mt in the list: `begin` for its beginning, then its
   // tiles, counted from key lo, up to the last key that a row may see.
-  __device__ int places(int mt, int tpm) const {
-    return begin + (len - lo + (chain ? min(n, (mt + 1) * tpm) : new_keys()) + KT - 1) / KT;
+  __device__ int tiles(int mt, int tpm) const {
+    return (len - lo + (chain ? min(n, (mt + 1) * tpm) : new_keys()) + KT - 1) / KT;
   }
+  __device__ int weight(int mt) const {
+    if constexpr (SHARED) return mt == mts - 1 ? this->w_last : this->w;
+    else return 1;
+  }
+  __device__ int places(int mt, int tpm) const { return begin + tiles(mt, tpm) * weight(mt); }
   // Places of the units before mt.
   __device__ long long before(int mt, int tpm) const {
     if (mt == 0) return 0;
+    if constexpr (SHARED) {
+      if (!chain) return (long long)mt * (begin + tiles(0, tpm) * this->w);
+    }
     if (!chain) return (long long)mt * places(0, tpm);
     return (long long)mt * begin + floor_sum(mt, KT, tpm, (long long)(len - lo) + tpm + KT - 1);
   }
@@ -262,6 +282,8 @@ __device__ __forceinline__ Req<KT, SHARED> load_req(const TreeArgs& a, int r) {
       // no member is shorter than its prefix: what lies before that one's window nobody sees
       q.lo = a.window > 0 ? max(0, min(common - a.window + 1, common - 1)) & ~(KT - 1) : 0;
       q.mts = (q.n + a.tpm - 1) / a.tpm;
+      q.w = a.w_full;
+      q.w_last = (q.n - (q.mts - 1) * a.tpm) * a.G <= a.small_rows ? a.w_small : a.w_full;
       return q;
     }
   }
@@ -290,6 +312,7 @@ __device__ __forceinline__ Req<KT, SHARED> load_req(const TreeArgs& a, int r) {
       q.lo = common + (a.window > 0 ? max(0, q.len - a.window + 1 - common) & ~(KT - 1) : 0);
     }
     q.fresh = q.n;
+    q.w = q.w_last = 1;                    // (a chain's sums know one weight)
   }
   q.mts = (q.n + a.tpm - 1) / a.tpm;
   return q;
@@ -314,6 +337,36 @@ struct Piece {
   }
 };
 
+// What part `part` of an attention over prefixes costs in all of request (or group) r's units of one kv-head.
+__device__ __forceinline__ float part_cost(const TreeArgs& a, int part, int r) {
+  const TreeArgs::Cost& c = a.cost[part];
+  const int common = max(a.shared[r], 0);
+  int n, keys;
+  if (part == 0) {
+    n = common > 0 ? max(a.group_first[r + 1] - a.group_first[r], 0) : 0;
+    keys = a.window > 0 ? min(common, a.window) : common;
+  } else {
+    n = max(a.first[r + 1] - a.first[r], 0);
+    keys = max(a.len[r] - common, 0);
+    if (a.window > 0) keys = min(keys, a.window);
+    keys = min(keys, INT_MAX - 1024) + min(n, kMaxDrafts);
+  }
+  const int full = n / c.tpm, rest = n - full * c.tpm;
+  const float tiles = (float)((keys + c.keys - 1) / c.keys);
+  return (float)(c.begin * c.tile) * (float)(full + (rest > 0)) +
+         tiles * ((float)full * (float)c.tile + (float)(rest == 0 ? 0 : 2 * rest > c.tpm ? c.tile : c.small));
+}
+
+// SMs of part 0: the fewest with which it ends no later than part 1 on the others, `lead` before it.
+__device__ __forceinline__ int first_sms(const TreeArgs& a, float c0, float c1) {
+  if (c0 == 0.f) return 0;
+  if (c1 == 0.f) return a.sms;
+  // the positive root k of  c0 / k + lead = c1 / (sms - k)  (short calls need no room for the lead)
+  const float n = (float)a.sms, lead = fminf((float)a.lead, 0.5f * (c0 + c1) / n), b = c0 + c1 - lead * n;
+  const float k = __fdividef(2.f * c0 * n, b + sqrtf(b * b + 4.f * lead * c0 * n));
+  return min(max((int)ceilf(k), 1), a.sms - 1);
+}
+
 // Where a CTA's share begins, found by one of its threads.
 template <int KT, bool SHARED>
 struct Begin {
@@ -336,11 +389,41 @@ struct Walk {
     const bool latched = load_err(a.err) != 0;
     const int per = (a.R + blockDim.x - 1) / blockDim.x;
     const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
+    float2 c = make_float2(0.f, 0.f);
+    if constexpr (SHARED)
+      for (int i = r0; i < r1; ++i) {      // (first, so that all their loads are on the way together)
+        c.x += part_cost(a, 0, i);
+        c.y += part_cost(a, 1, i);
+      }
     long long mine = 0;
     for (int i = r0; i < r1; ++i) mine += load_req<KT, SHARED>(a, i).per_head(a.tpm) * a.H;
+    int ctas = a.ctas;
+    if constexpr (SHARED) {
+      // The parts run side by side, each on its share of the SMs: the CTAs behind it have no work.
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        c.x += __shfl_xor_sync(0xffffffffu, c.x, d);
+        c.y += __shfl_xor_sync(0xffffffffu, c.y, d);
+      }
+      float2* s_cost = reinterpret_cast<float2*>(s_warp);
+      if ((threadIdx.x & 31) == 0) s_cost[threadIdx.x >> 5] = c;
+      __syncthreads();
+      c = make_float2(0.f, 0.f);
+      for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+        c.x += s_cost[w].x;
+        c.y += s_cost[w].y;
+      }
+      __syncthreads();
+      int first = first_sms(a, c.x * a.H, c.y * a.H);
+      // Part 0 as a whole number of CTAs per kv-head, where that costs little: one group's units are alike,
+      // and a CTA with a piece of two pays for two beginnings and ends (63 us instead of 56).
+      const int near = max(1, (first + a.H / 2) / a.H) * a.H;
+      if (c.x > 0.f && c.y > 0.f && near < a.sms && abs(near - first) <= first / 12) first = near;
+      ctas = max(1, a.part == 0 ? first * a.cost[0].per_sm : (a.sms - first) * a.cost[1].per_sm);
+    }
     long long before = block_exclusive(mine, s_warp, &W);
     const long long fit = W / a.min_tiles;
-    C = fit < 1 ? 1 : fit < a.ctas ? (int)fit : a.ctas;
+    C = fit < 1 ? 1 : fit < ctas ? (int)fit : ctas;
     const int cta = blockIdx.x;
     if (__syncthreads_or(latched) || W == 0 || cta >= C) return false;  // (alike in the whole block)
     at = cta * W / C;
@@ -379,6 +462,7 @@ struct Walk {
     while (at < end) {
       const int all = q.places(mt, a.tpm);
       const int t0 = ta, t1 = (int)min((long long)all, ta + (end - at));
+      const int weight = q.weight(mt);
       const long long unit_end = at - ta + all;
       const int lo = q.lo;                 // (q may move on below)
       p.r = r;
@@ -418,6 +502,18 @@ struct Walk {
             }
           }
         }
+      }
+      if constexpr (SHARED) {
+        // a tile is the CTA's in whose share its first place lies (a share has at least a tile's places)
+        auto up = [&](int places) { return max(0, places - a.begin + weight - 1) / weight; };
+        const int first = up(t0), from = max(first, skip - a.begin), to = up(t1);
+        if (from >= to) continue;
+        p.j0 = lo + from * KT;
+        p.count = to - from;
+        p.begins = first <= skip - a.begin;
+        p.whole = p.begins && to == up(all);
+        p.last = (int)(((unit_end - weight + 1) * C - 1) / W);
+        return true;
       }
       const int from = max(t0, skip);
       if (from >= t1) continue;
@@ -505,6 +601,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
 
   // (part 1 of an attention over prefixes may run beside part 0, which it waits for at its end)
   if (!SHARED || a.part == 0) griddep_wait();
+  if (SHARED) griddep_launch();
   Walk<KT, SHARED> walk;
   if (!walk.begin(a, s_warp, &s_begin)) {
     if (SHARED) griddep_wait();
@@ -512,7 +609,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
     return;
   }
 
-  griddep_launch();                                  // (the merge waits for the whole grid anyway)
+  if (!SHARED) griddep_launch();                     // (the merge waits for the whole grid anyway)
   Piece pc;
   while (walk.next(a, pc)) {
     const int rows = pc.ntok * a.G, count = pc.count, h = pc.h;
@@ -780,12 +877,15 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
           }
         l[row] = l[row] * corr[row] + sum;
       }
+      // (mostly no row of the warp has a new maximum)
+      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
-        acc[x][0] *= corr[0];
-        acc[x][1] *= corr[0];
-        acc[x][2] *= corr[1];
-        acc[x][3] *= corr[1];
+        for (int x = 0; x < D / 8; ++x) {
+          acc[x][0] *= corr[0];
+          acc[x][1] *= corr[0];
+          acc[x][2] *= corr[1];
+          acc[x][3] *= corr[1];
+        }
       }
       if (!bad_v) {
 #pragma unroll

@@ -189,6 +189,15 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
           "r"(dst), "l"(map), "r"(bar), "r"(0), "r"(group), "r"(page)
       : "memory");
 }
+// The same as the L2's first candidate for eviction.
+__device__ __forceinline__ void tma_box_once(uint32_t dst, const CUtensorMap* map, uint32_t bar, int group, int page,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%3, %3, %3, %4, %5}], [%2], %6;" ::
+          "r"(dst), "l"(map), "r"(bar), "r"(0), "r"(group), "r"(page), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
@@ -451,6 +460,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (!SHARED || a.part == 0) griddep_wait();  // (part 1 waits for part 0 at its end)
+  if (SHARED) griddep_launch();
   Walk<UT, SHARED> walk;
   const bool idle = !walk.begin(a, s_warp, &s_begin);
   tc_fence_after();
@@ -462,7 +472,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
-  griddep_launch();
+  if (!SHARED) griddep_launch();
 #ifdef AVSG_DEBUG_BOUNDS
   const Waits waits{ua.wait_clocks, &s_give_up, a.err};
 #else
@@ -528,6 +538,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       // q into shared memory, a row by D / 8 lanes; rows past the unit's are zeros
       const bool warp_live = rl - lane < s.ntok * a.G;
       bool q_loading = false;
+      // (part 0) a member's token, looked up once by the lane whose row it is in
+      int token = 0;
+      if (SHARED && a.part == 0 && mine) token = token_of<SHARED>(a, s, s.tok0 + lt);
       if (two || x == 0) {
         if (warp_live) {
           constexpr int LPR = D / 8, RPI = 32 / LPR;
@@ -540,9 +553,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           for (int it = 0; it < 32 / RPI; ++it) {
             const bool ok = r < rows;
             const unsigned char* src = ok ? base + (t * a.q_stride + g * D) * 2 : a.q;
-            if (SHARED && a.part == 0 && ok)
-              src = a.q + ch * 16 + ((long long)token_of<SHARED>(a, s, s.tok0 + t) * a.q_stride +
-                                     ((long long)s.h * G + g) * D) * 2;
+            if constexpr (SHARED) {
+              const int of = __shfl_sync(0xffffffffu, token, it * RPI + lane / LPR);
+              if (a.part == 0 && ok) src = a.q + ch * 16 + ((long long)of * a.q_stride + ((long long)s.h * G + g) * D) * 2;
+            }
             const uint32_t dst =
                 SOLO ? smem + M::STAGE + at * M::STAGE_ROW + ch * 16
                      : to + (at / 8) * (1024 * COLS) + (at & 7) * 128 + (((ch & 7) ^ (at & 7)) << 4);
@@ -564,7 +578,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       int q_pos = s.len + max(tok, 0);
       unsigned long long bits = 0;
       if (SHARED && a.part == 0) {
-        if (mine && (a.slopes || a.window > 0)) q_pos = member_position(a, s, tok, token_of<SHARED>(a, s, tok));
+        if (mine && (a.slopes || a.window > 0)) q_pos = member_position(a, s, tok, token);
       } else if (!s.chain && mine) {
         bits = a.mask[s.f + tok];
         if (bits) q_pos = s.len + __popcll(bits) - 1;
@@ -879,15 +893,23 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const float sum = l * f0 + l1 * f1;
       // (SHARED: only requests without a prefix write their output here)
       const bool whole = s.whole && (!SHARED || (a.part == 1 && a.shared[s.r] == 0));
-      const int token = token_of<SHARED>(a, s, max(tok, 0));
+      if (!SHARED || a.part == 1) token = s.f + max(tok, 0);
       const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
       const long long at = (long long)token * a.H * a.G + s.h * a.G + gg;
       const long long slot = SHARED && s.whole ? at : ((long long)(2 * cta + (s.begins ? 1 : 0)) * M::ROWS + rl);
       float* const partial = SHARED && s.whole ? a.rows : a.partial;
+      if (SHARED && !two && !SOLO && !whole) asm volatile("bar.sync 2, 256;" ::: "memory");  // (see below)
       if (warp_live) {
         const uint32_t from = two ? to : tmem + lanes + 256;
         const float g0 = f0 * inv, g1 = f1 * inv;  // (inv is 1 where the output is not divided yet)
         uint32_t w0[32], w1[32];
+        // (SHARED, where most units leave partials: document of 32768 tokens before 64 requests, 7.0 us from
+        // the last product to the CTA's end otherwise, 5.0 so; single units of the tree attention lose 1 to 2%.)
+        // Partials pass through shared memory, so that a store writes whole lines and not 16 bytes of 32
+        // rows: this warp's part of q's place, which the products are done with (4 KB of 32 rows by 32
+        // columns, 16-byte chunks swapped by the row).  Up to 128 rows, m and l lie there too: read by now.
+        const uint32_t shown = __ballot_sync(0xffffffffu, mine);
+        unsigned char* const st = smem_raw + (SOLO ? M::STAGE + warp * 4096 : x * M::Q + (warp & 3) * (32 * D * 2));
 #pragma unroll 1
         for (int c = two ? 0 : x * (D / 64); c < (two ? D / 32 : (x + 1) * (D / 64)); ++c) {
           tm_ld32(from + c * 32, w0);
@@ -902,8 +924,22 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             w0[y] = __float_as_uint(o);
           }
           auto o = [&](int y) { return __uint_as_float(w0[y]); };
-          if (!mine) {
-          } else if (whole) {
+          if (SHARED && !whole) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              *reinterpret_cast<float4*>(st + lane * 128 + ((y ^ (lane & 7)) << 4)) =
+                  make_float4(o(4 * y), o(4 * y + 1), o(4 * y + 2), o(4 * y + 3));
+            __syncwarp();
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int r = 4 * y + (lane >> 3);
+              const long long to_row = __shfl_sync(0xffffffffu, slot, r);
+              if (shown >> r & 1)
+                *reinterpret_cast<float4*>(partial + to_row * D + c * 32 + (lane & 7) * 4) =
+                    *reinterpret_cast<const float4*>(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            }
+          } else if (!mine) {
+          } else if (SHARED || whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + (at * D + c * 32) * 2);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
@@ -997,6 +1033,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     };
     bool have = more;
     if (have) look_up();
+    uint64_t policy = 0;
+    if constexpr (SHARED) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     while (have) {
       const int now = page, now_group = group, now_v = is_v, b = to, phase = use;
       have = more;
@@ -1006,9 +1044,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       end = phase * kRing + b + 1;
       if (lane == 0) bar_expect(full(b), n * ua.box_rows * D * 2);
       __syncwarp();
-      if (now >= 0)
+      if constexpr (SHARED) {
+        if (now >= 0)
+          tma_box_once(smem + M::RING + b * M::TILE + lane * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
+                       now_group, now, policy);
+      } else if (now >= 0) {
         tma_box(smem + M::RING + b * M::TILE + lane * ua.box_rows * D * 2, now_v ? &v_map : &k_map, full(b),
                 now_group, now);
+      }
     }
     // every copy of this warp has landed before the CTA may end
     for (int b = part; b < kRing && b < end; b += 2) bar_drain(full(b), ((end - 1 - b) / kRing) & 1);
