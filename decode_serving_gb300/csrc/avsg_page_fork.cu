@@ -1,27 +1,31 @@
 // avsg_page_fork: requests continue as copies of others, with shared pages.
 //
-// Request r becomes what request parent[r] was: the full pages of the old row
-// are held by both, its partly filled last page (if it has one) stays with the
-// parent or, if that goes on as something else, with the lowest of its
-// children, and is copied for the others.  With t_q = number of requests r with parent[r] == q
-// ("times" below), each old row q stood for one holder of its full pages
-// and stands for t_q afterwards, so a page has
-//     shares' = shares + sum over the rows q that hold it of (t_q - 1)
-// holders beyond the first, and is free when that is -1.  Rows with t_q = 1
-// change nothing, so that a call in which few requests change touches few pages.
+// Request r becomes what request q = parent[r] was: the full pages of the old
+// row q are held by both, its partly filled last page (if it has one) stays
+// with q or, if q goes on as something else, with the lowest of its children,
+// and is copied for the others.  A request that becomes another one lets go of its old row's full
+// pages (and of the last one, if nobody goes on with its row) and takes hold of q's;
+// a page that both rows have in the same place changes nothing.  So
+//     shares' = shares + (requests that take hold of the page) - (that let go of it)
+// holders beyond the first, and the page is free when that is -1.
 //
 // What bounds it.  The rows of the copied pages: 2 bytes moved per byte, by
 // fork_copy_kernel.  What comes before, tables and counts, is latency: one cluster of up to
 // 8 CTAs whose hardware barriers part the phases
-//   check      lengths, parents, ids; marks of the touched pages cleared; rows
-//              that others still need after they are overwritten set aside
-//   count      (t_q - 1) added to each page's mark, its last row noted
-//   back       pages without a holder counted, item by item
+//   check      lengths, parents, ids; marks of the pages that change holders
+//              cleared; rows that others still need after they are overwritten set aside
+//   count      gains and losses added to each page's mark, the last request that touches it noted
+//   back       pages without a holder counted, piece by piece
 //   write      shares, free stack
 //   write      tables, lengths
+// Only requests that become others are looked at, a row and its parent's side
+// by side; where their rows agree (beams and samples of one prompt, but for
+// the last pages) nothing is counted, and where all of them do, the middle three are left out.
 // Nothing is written before every check has passed.  Sums and maxima of whole
 // numbers decide everything, so that the result does not depend on an order.
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "avsg_paged.cuh"
 
@@ -56,6 +60,7 @@ struct ForkArgs {
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(ForkArgs a) {
   extern __shared__ int32_t s_mem[];
   __shared__ long long s_warp[kForkThreads / 32];
+  __shared__ int s_any[kForkCluster];
   int32_t* s_len = s_mem;                  // [R] each
   int32_t* s_parent = s_len + a.R;
   int32_t* s_times = s_parent + a.R;
@@ -68,6 +73,7 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(ForkArgs a) {
   const int warp = rank * (kForkThreads / 32) + (tid >> 5), warps = ctas * (kForkThreads / 32);
   const int page_mask = (1 << a.shift) - 1;
   const int items = a.R * a.pieces;
+  auto started = cluster.barrier_arrive();  // (s_any is written by other CTAs)
 
   for (int r = tid; r < a.R; r += kForkThreads) {
     s_times[r] = 0;
@@ -120,76 +126,107 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(ForkArgs a) {
   // end of the piece that begins at column x0 of a row with this many
   auto piece_end = [&](int x0, int columns) { return columns - x0 > a.cols ? x0 + a.cols : columns; };
 
+  // What request r lets go of and takes hold of, in the columns of its piece.  A partly filled last
+  // page is nobody else's: it changes hands, or goes with a row that nobody goes on with.
+  auto each_column = [&](int i, auto&& f) {
+    const int r = i / a.pieces, q = s_parent[r], x0 = (i - r * a.pieces) * a.cols;
+    if (q == r) return;
+    const int lose = s_times[r] == 0 ? held(r) : s_len[r] >> a.shift, gain = q < 0 ? 0 : s_len[q] >> a.shift;
+    const int x1 = piece_end(x0, max(lose, gain));
+    const int32_t* mine = a.tables + (size_t)r * a.max_pages;
+    const int32_t* theirs = a.tables + (size_t)max(q, 0) * a.max_pages;
+#pragma unroll 2
+    for (int x = x0; x < x1; x += 32) {
+      const int at = x + lane;
+      const int32_t from = at < lose && at < x1 ? mine[at] : -1, to = at < gain && at < x1 ? theirs[at] : -1;
+      f(r, at, at < lose && at < x1, from, at < gain && at < x1, to);
+    }
+  };
+  // (request, whether it lets go): at most one of a page's marks
+  auto mark = [](int r, bool loses) { return 2 * r + (loses ? 1 : 0); };
+
   // check
+  bool any = false;
   if (ok) {
-    for (int r = rank * kForkThreads + tid; r < a.R; r += ctas * kForkThreads)
+    for (int r = rank * kForkThreads + tid; r < a.R; r += ctas * kForkThreads) {
+      const int q = s_parent[r];
+      if (q < 0 || q == r || (s_len[q] & page_mask) == 0) continue;
+      const int32_t last = a.tables[(size_t)q * a.max_pages + (s_len[q] >> a.shift)];
+      if (last < 0 || last >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, q, s_len[q] >> a.shift);
       if (s_copy[r] >= 0) {
-        const int q = s_parent[r], to = a.free_list[count - 1 - s_copy[r]];
+        const int to = a.free_list[count - 1 - s_copy[r]];
         if (to < 0 || to >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, count - 1 - s_copy[r]);
-        a.copies[s_copy[r]] = make_int4(a.tables[(size_t)q * a.max_pages + (s_len[q] >> a.shift)], to,
-                                        s_len[q] & page_mask, 0);
+        a.copies[s_copy[r]] = make_int4(last, to, s_len[q] & page_mask, 0);
       }
+    }
     if (rank == 0 && tid == 0) *a.num_copies = num_copies;
     for (int i = warp; i < items; i += warps) {
-      const int q = i / a.pieces, x0 = (i - q * a.pieces) * a.cols, x1 = piece_end(x0, held(q));
-      const bool changes = s_times[q] != 1, set_aside = s_parent[q] != q && s_times[q] > 0;
-      if (!changes && !set_aside) continue;
-      const int32_t* row = a.tables + (size_t)q * a.max_pages;
-#pragma unroll 4
-      for (int x = x0 + lane; x < x1; x += 32) {
-        const int32_t id = row[x];
-        if (id < 0 || id >= a.num_pages) {
-          raise_error(a.err, AVSG_ERR_BAD_SELECTION, q, x);
-        } else if (changes) {
-          a.delta[id] = 0;
-          a.last[id] = -1;
+      each_column(i, [&](int r, int x, bool loses, int32_t from, bool gains, int32_t to) {
+        if (loses && (from < 0 || from >= a.num_pages)) {
+          raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, x);
+        } else if (gains && (to < 0 || to >= a.num_pages)) {
+          raise_error(a.err, AVSG_ERR_BAD_SELECTION, s_parent[r], x);
+        } else if (from != to) {
+          any = true;
+          if (loses) {
+            a.delta[from] = 0;
+            a.last[from] = -1;
+          }
+          if (gains) {
+            a.delta[to] = 0;
+            a.last[to] = -1;
+          }
         }
-        if (set_aside) a.aside[(size_t)q * a.max_pages + x] = id;
-      }
+      });
+      const int q = i / a.pieces;
+      if (s_parent[q] == q || s_times[q] == 0) continue;
+      const int x0 = (i - q * a.pieces) * a.cols, x1 = piece_end(x0, held(q));
+      for (int x = x0 + lane; x < x1; x += 32)
+        a.aside[(size_t)q * a.max_pages + x] = a.tables[(size_t)q * a.max_pages + x];
     }
     __threadfence();
   }
+  any = __syncthreads_or(any);
+  cluster.barrier_wait(std::move(started));
+  if (tid < ctas) *cluster.map_shared_rank(&s_any[rank], tid) = any;
   cluster.sync();
   ok = !__syncthreads_or(!ok || load_err(a.err) != 0);
   // (every CTA sees the same words, so all go on or none; those that stop keep the barriers)
+  any = false;
+  for (int c = 0; c < ctas; ++c) any |= s_any[c] != 0;
 
-  // Of a row that changes counts, its held pages one by one: full or the last, partly filled one.
-  // The latter is nobody else's; it only changes hands, or goes.
-  auto each_page = [&](int i, auto&& f) {
-    const int q = i / a.pieces, x0 = (i - q * a.pieces) * a.cols;
-    if (s_times[q] == 1) return;
-    const int full = s_len[q] >> a.shift, x1 = piece_end(x0, s_times[q] == 0 ? held(q) : full);
-    const int32_t* row = a.tables + (size_t)q * a.max_pages;
-    for (int x = x0; x < x1; x += 32) {
-      const bool have = x + lane < x1;
-      f(q, have, have ? row[x + lane] : 0);
-    }
-  };
-  // count
-  if (ok)
-    for (int i = warp; i < items; i += warps)
-      each_page(i, [&](int q, bool have, int32_t id) {
-        if (!have) return;
-        atomicAdd(a.delta + id, s_times[q] - 1);
-        atomicMax(a.last + id, q);
-      });
-  __threadfence();
-  cluster.sync();
-  // back: a page that goes is given back by the last row that held it
-  if (ok)
-    for (int i = warp; i < items; i += warps) {
-      int n = 0;
-      each_page(i, [&](int q, bool have, int32_t id) {
-        n += have && __ldcg(a.last + id) == q && a.shares[id] + __ldcg(a.delta + id) < 0;
-      });
-#pragma unroll
-      for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-      if (lane == 0) a.back[i] = n;
-    }
-  __threadfence();
-  cluster.sync();
   long long total = 0;
-  {
+  const long long left = (long long)count - num_copies;
+  if (any) {
+    // count
+    if (ok)
+      for (int i = warp; i < items; i += warps)
+        each_column(i, [&](int r, int, bool loses, int32_t from, bool gains, int32_t to) {
+          if (from == to) return;
+          if (loses) {
+            atomicAdd(a.delta + from, -1);
+            atomicMax(a.last + from, mark(r, true));
+          }
+          if (gains) {
+            atomicAdd(a.delta + to, 1);
+            atomicMax(a.last + to, mark(r, false));
+          }
+        });
+    __threadfence();
+    cluster.sync();
+    // back: a page that goes is given back by the last request that held it
+    if (ok)
+      for (int i = warp; i < items; i += warps) {
+        int n = 0;
+        each_column(i, [&](int r, int, bool loses, int32_t from, bool, int32_t to) {
+          n += loses && from != to && __ldcg(a.last + from) == mark(r, true) &&
+               a.shares[from] + __ldcg(a.delta + from) < 0;
+        });
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) a.back[i] = n;
+      }
+    __threadfence();
+    cluster.sync();
     const int each = (items + kForkThreads - 1) / kForkThreads;
     const int i0 = min(items, tid * each), i1 = min(items, i0 + each);
     long long n = 0;
@@ -201,25 +238,26 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(ForkArgs a) {
         s_at[i] = (int)at;
         at += __ldcg(a.back + i);
       }
+    if (ok && left + total > a.num_pages) {
+      if (rank == 0 && tid == 0) raise_error(a.err, AVSG_ERR_CAPACITY, -1, -1);
+      ok = false;
+    }
+    __syncthreads();
   }
-  const long long left = (long long)count - num_copies;
-  if (ok && left + total > a.num_pages) {
-    if (rank == 0 && tid == 0) raise_error(a.err, AVSG_ERR_CAPACITY, -1, -1);
-    ok = false;
-  }
-  __syncthreads();
   griddep_launch();
   // write: shares and the stack (the reverse order of taking)
-  if (ok)
+  if (ok && any)
     for (int i = warp; i < items; i += warps) {
       int at = s_at[i];
-      each_page(i, [&](int q, bool have, int32_t id) {
-        const bool own = have && __ldcg(a.last + id) == q;
-        const int now = own ? a.shares[id] + __ldcg(a.delta + id) : 0;
+      each_column(i, [&](int r, int, bool loses, int32_t from, bool gains, int32_t to) {
+        const bool own_to = gains && from != to && __ldcg(a.last + to) == mark(r, false);
+        if (own_to) a.shares[to] += __ldcg(a.delta + to);
+        const bool own = loses && from != to && __ldcg(a.last + from) == mark(r, true);
+        const int now = own ? a.shares[from] + __ldcg(a.delta + from) : 0;
         const unsigned gone = __ballot_sync(0xffffffffu, own && now < 0);
-        if (own) a.shares[id] = max(now, 0);
+        if (own) a.shares[from] = max(now, 0);
         if (own && now < 0)
-          a.free_list[left + total - 1 - (at + __popc(gone & ((1u << lane) - 1)))] = id;
+          a.free_list[left + total - 1 - (at + __popc(gone & ((1u << lane) - 1)))] = from;
         at += __popc(gone);
       });
     }

@@ -892,13 +892,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const float f0 = ex2(m - use), f1 = ex2(m1 - use);
       const float sum = l * f0 + l1 * f1;
       // (SHARED: only requests without a prefix write their output here)
-      const bool whole = s.whole && (!SHARED || (a.part == 1 && a.shared[s.r] == 0));
-      if (!SHARED || a.part == 1) token = s.f + max(tok, 0);
-      const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-      const long long at = (long long)token * a.H * a.G + s.h * a.G + gg;
+      const bool direct = SHARED && s.whole && a.part == 1 && a.shared[s.r] == 0;
+      auto whole = [&] { return SHARED ? direct : s.whole; };
+      if (SHARED && a.part == 1) token = s.f + max(tok, 0);
+      const float inv = whole() ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      const long long at = (long long)(SHARED ? token : s.f + max(tok, 0)) * a.H * a.G + s.h * a.G + gg;
       const long long slot = SHARED && s.whole ? at : ((long long)(2 * cta + (s.begins ? 1 : 0)) * M::ROWS + rl);
-      float* const partial = SHARED && s.whole ? a.rows : a.partial;
-      if (SHARED && !two && !SOLO && !whole) asm volatile("bar.sync 2, 256;" ::: "memory");  // (see below)
+      auto partial = [&] { return SHARED && s.whole ? a.rows : a.partial; };
+      if (SHARED && !two && !SOLO && !direct) asm volatile("bar.sync 2, 256;" ::: "memory");  // (see below)
       if (warp_live) {
         const uint32_t from = two ? to : tmem + lanes + 256;
         const float g0 = f0 * inv, g1 = f1 * inv;  // (inv is 1 where the output is not divided yet)
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         // Partials pass through shared memory, so that a store writes whole lines and not 16 bytes of 32
         // rows: this warp's part of q's place, which the products are done with (4 KB of 32 rows by 32
         // columns, 16-byte chunks swapped by the row).  Up to 128 rows, m and l lie there too: read by now.
-        const uint32_t shown = __ballot_sync(0xffffffffu, mine);
+        const uint32_t shown = SHARED ? __ballot_sync(0xffffffffu, mine) : 0;
         unsigned char* const st = smem_raw + (SOLO ? M::STAGE + warp * 4096 : x * M::Q + (warp & 3) * (32 * D * 2));
 #pragma unroll 1
         for (int c = two ? 0 : x * (D / 64); c < (two ? D / 32 : (x + 1) * (D / 64)); ++c) {
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             w0[y] = __float_as_uint(o);
           }
           auto o = [&](int y) { return __uint_as_float(w0[y]); };
-          if (SHARED && !whole) {
+          if (SHARED && !direct) {
 #pragma unroll
             for (int y = 0; y < 8; ++y)
               *reinterpret_cast<float4*>(st + lane * 128 + ((y ^ (lane & 7)) << 4)) =
@@ -935,25 +936,25 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               const int r = 4 * y + (lane >> 3);
               const long long to_row = __shfl_sync(0xffffffffu, slot, r);
               if (shown >> r & 1)
-                *reinterpret_cast<float4*>(partial + to_row * D + c * 32 + (lane & 7) * 4) =
+                *reinterpret_cast<float4*>(partial() + to_row * D + c * 32 + (lane & 7) * 4) =
                     *reinterpret_cast<const float4*>(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
             }
           } else if (!mine) {
-          } else if (SHARED || whole) {
+          } else if (SHARED || s.whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + (at * D + c * 32) * 2);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               dst[y] = make_uint4(pack<T>(o(8 * y), o(8 * y + 1)), pack<T>(o(8 * y + 2), o(8 * y + 3)),
                                   pack<T>(o(8 * y + 4), o(8 * y + 5)), pack<T>(o(8 * y + 6), o(8 * y + 7)));
           } else {
-            float4* dst = reinterpret_cast<float4*>(partial + slot * D + c * 32);
+            float4* dst = reinterpret_cast<float4*>(a.partial + slot * D + c * 32);
 #pragma unroll
             for (int y = 0; y < 8; ++y) dst[y] = make_float4(o(4 * y), o(4 * y + 1), o(4 * y + 2), o(4 * y + 3));
           }
           __syncwarp();
         }
         if (mine && (two || x == 0)) {
-          if (!whole)
+          if (!whole())
             *reinterpret_cast<float2*>((SHARED && s.whole ? a.rows_ml : a.ml) + slot * 2) = make_float2(top, sum);
           else if (a.lse)
             a.lse[at] = sum == 0.f ? -INFINITY : (top - SHIFT) * 0.6931471805599453f + logf(sum);
@@ -964,12 +965,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         asm volatile("bar.sync 6, 256;" ::: "memory");  // the rows are written
         if (mine && (two || x == 0)) {
           const unsigned char* q =
-              a.q + ((long long)token * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
-          if (whole)
+              a.q + ((long long)(SHARED ? token : s.f + tok) * a.q_stride + (long long)(s.h * a.G + gg) * D) * 2;
+          if (whole())
             add_bad_values<T, T, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, inv,
                                     reinterpret_cast<T*>(a.out) + at * D);
           else
-            add_bad_values<T, float, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, 1.f, partial + slot * D);
+            add_bad_values<T, float, D>(a, s, q, tok, q_pos, bits, slope, use - SHIFT, 1.f, partial() + slot * D);
         }
       }
       idx += 2 * s.count;
