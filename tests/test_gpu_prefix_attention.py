@@ -465,3 +465,82 @@ def test_masks_of_long_requests_are_not_looked_at():
     s.dmask = dev(s.mask, torch.int64)
     s.attend(window=100)
     s.check(window=100)
+
+
+def test_calls_in_a_row_do_not_reach_into_one_another():
+    """Two batches in turn with one workspace and nothing waited for in between: long prefixes beside
+    short own keys, and the other way round."""
+    a = Shared([6000, 6100, 6050, 40], [1, 1, 1, 1], 16, 2, 4, 128, BF16, False, [((0, 1, 2), 370)], seed=1)
+    b = Shared([9000, 300, 290, 700], [16, 3, 8, 1], 16, 2, 4, 128, BF16, True, [((1, 2), 17)], seed=2)
+    work = a.cache.attend_prefixes_workspace(4, 16, 28)
+    want = []
+    for s in (a, b):
+        s.attend(work=work, most=16)
+        torch.cuda.synchronize()
+        s.check()
+        want.append((s.out.clone(), s.lse.clone()))
+    got = []
+    for k in range(40):
+        s = (a, b)[k % 2]
+        s.out.zero_()
+        s.attend(work=work, most=16)
+        got.append((s.out.clone(), s.lse.clone()))
+    torch.cuda.synchronize()
+    for k, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[k % 2])), k
+
+
+def test_groups_that_change_between_replays():
+    """One captured attention, with other groups, lengths and first tokens at each replay."""
+    cases = [([400, 410, 420, 30], [((0, 1, 2), 25)]), ([400, 410, 420, 410], [((0, 2), 20), ((1, 3), 3)]),
+             ([17, 300, 5, 290], [((1, 3), 18)]), ([50, 60, 70, 80], [])]
+    base = Shared([420] * 4, [3, 1, 2, 4], 16, 2, 4, 128, F16, True, [], seed=3)
+    work, find = base.cache.attend_prefixes_workspace(4, 4, base.total), base.cache.prefix_workspace()
+
+    def step():
+        base.cache.find_prefixes(base.first, base.x, find, min_tokens=16)
+        base.attend(work=work, most=4)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    for lens, share in cases:
+        s = Shared(lens, [3, 1, 2, 4], 16, 2, 4, 128, F16, True, share, seed=3, least=16)
+        base.lens = np.array(lens, np.int32)
+        base.cache.lens.copy_(dev(base.lens))
+        base.cache.tables.zero_()
+        base.cache.tables[:, :s.cache.max_pages].copy_(s.cache.tables)
+        base.k[:, :s.k.shape[1]].copy_(s.k)
+        base.v[:, :s.v.shape[1]].copy_(s.v)
+        base.q.copy_(s.q)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(base.x.shared, s.x.shared)
+        base.check()
+
+
+def test_the_binding_s_functions_beside_the_methods():
+    from decode_serving_gb300 import avsg
+    s = Shared([300, 290, 60], [2, 5, 1], 16, 2, 4, 128, BF16, True, [((0, 1), 16)])
+    s.attend()
+    torch.cuda.synchronize()
+    x = s.cache.prefix_arrays(s.total)
+    args = avsg.avsg_prefixes(num_tokens=s.total, d_leader=x.leader.data_ptr(), d_shared=x.shared.data_ptr(),
+                              d_first=x.first.data_ptr(), d_token=x.token.data_ptr(), d_request=x.request.data_ptr())
+    pages = s.cache._pages
+    n = avsg.avsg_prefix_find_workspace(pages)
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
+    avsg.avsg_prefix_find(pages, s.first.data_ptr(), 1, args, work.data_ptr(), n)
+    n = avsg.avsg_prefix_attention_workspace(pages, 4, 5, s.total)
+    work2 = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros_like(s.out), torch.zeros_like(s.lse)
+    t = avsg.avsg_tree(num_tokens=s.total, q_per_kv=4, max_new=5, layer=0, q_stride=8 * 128, d_q=s.q.data_ptr(),
+                       d_first=s.first.data_ptr(), d_mask=s.dmask.data_ptr(), d_out=out.data_ptr(),
+                       d_lse=lse.data_ptr(), d_work=work2.data_ptr(), work_bytes=n)
+    avsg.avsg_prefix_attention(pages, t, args)
+    torch.cuda.synchronize()
+    assert s.cache.error()[0] == 0 and torch.equal(out, s.out) and torch.equal(lse, s.lse)
+    assert all(torch.equal(a, b) for a, b in zip((x.leader, x.shared, x.first, x.token, x.request),
+                                                 (s.x.leader, s.x.shared, s.x.first, s.x.token, s.x.request)))

@@ -420,3 +420,53 @@ def test_refusals():
     rotary(pos, axes)
     assert c.error()[0] == 0
     assert math.isfinite(float(out.float().sum()))
+
+
+def test_forks_in_a_row_do_not_reach_into_one_another():
+    """Nothing is waited for between forks (their copies run beside their tables), compactions among them."""
+    r = np.random.default_rng(11)
+    p = Pool([100, 37, 0, 90, 5, 64] * 8, 16, spare=2500, layers=3, heads=2, dim=128, room=2)
+    fork, pack = p.cache.fork_workspace(), p.cache.compact_workspace()
+    page_map = torch.zeros(p.cache.pages, dtype=torch.int32, device="cuda")
+    parents = [np.where(r.random(48) < 0.4, np.arange(48), r.integers(-1 if k == 20 else 0, 48, 48)) for k in range(30)]
+    on_device = [dev(x) for x in parents]
+    torch.cuda.synchronize()
+    for k, x in enumerate(on_device):
+        p.cache.fork(x, fork)
+        if k % 10 == 5:
+            p.cache.compact(page_map, pack)
+    torch.cuda.synchronize()
+    for k, x in enumerate(parents):
+        p.lens, p.tables, p.free, p.count, p.shares = want_of.fork(p.lens, x, p.tables, p.free, p.count, p.shares, 16,
+                                                                   p.pages)
+        if k % 10 == 5:
+            p.tables, p.free, p.shares, _ = want_of.compact(p.lens, p.tables, p.free, p.count, p.shares, 16, p.pages)
+    p.check()
+
+
+def test_the_binding_s_functions_beside_the_methods():
+    from decode_serving_gb300 import avsg
+    p = Pool([100, 37, 0, 90], 16, groups=[((0, 3), 4)], layers=2)
+    c, pages, parent = p.cache, p.cache._pages, dev(np.array([0, 0, 3, -1]))
+    n = avsg.avsg_page_fork_workspace(pages)
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
+    avsg.avsg_page_fork(pages, parent.data_ptr(), c.shares.data_ptr(), work.data_ptr(), n)
+    torch.cuda.synchronize()
+    p.lens, p.tables, p.free, p.count, p.shares = want_of.fork(p.lens, host(parent), p.tables, p.free, p.count, p.shares,
+                                                               16, p.pages)
+    p.check()
+    n = avsg.avsg_page_compact_workspace(pages)
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
+    page_map = torch.zeros_like(c.free)
+    avsg.avsg_page_compact(pages, c.shares.data_ptr(), c.shares.data_ptr(), c.tables.data_ptr(), c.free.data_ptr(),
+                           page_map.data_ptr(), work.data_ptr(), n)
+    torch.cuda.synchronize()
+    p.tables, p.free, p.shares, where = want_of.compact(p.lens, p.tables, p.free, p.count, p.shares, 16, p.pages)
+    p.check()
+    assert (host(page_map) == where).all()
+    first = torch.zeros(5, dtype=torch.int32, device="cuda")
+    keep = dev(np.array([0, 0, 0, 0]))
+    avsg.avsg_tree_keep_shared(pages, c.shares.data_ptr(), first.data_ptr(), 0, 0, keep.data_ptr(), c.lens.data_ptr(),
+                               c.free_count.data_ptr())
+    torch.cuda.synchronize()
+    p.check()
