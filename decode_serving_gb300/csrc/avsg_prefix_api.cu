@@ -42,11 +42,13 @@ struct JoinArgs {
 
 // WPR warps join the pieces of one row, each every WPR-th of them.  Two dependent chains of loads: where the pieces lie, then
 // their maxima, sums and outputs side by side, up to kJoinAhead outputs before the first weight is known.
-// What bounds it is how many rows are on their way, hence few registers.
-constexpr int join_blocks(int D, int WPR) { return D == 256 ? 3 : WPR == 1 ? 8 : 5; }
+// What bounds it is how many bytes are on their way (20 000 rows of 3 pieces: 13 us; with two outputs
+// ahead in 32 registers and 8 blocks an SM 16).
+constexpr int kJoinAhead = 4;
+constexpr int join_blocks(int D) { return D == 256 ? 3 : 5; }
 template <typename T, int D, int WPR>
-__global__ void __launch_bounds__(kJoinThreads, join_blocks(D, WPR)) prefix_join_kernel(JoinArgs a) {
-  constexpr int VPL = D / 32, ROWS = kJoinThreads / 32 / WPR, kJoinAhead = WPR == 1 && D < 256 ? 2 : 4;
+__global__ void __launch_bounds__(kJoinThreads, join_blocks(D)) prefix_join_kernel(JoinArgs a) {
+  constexpr int VPL = D / 32, ROWS = kJoinThreads / 32 / WPR;
   __shared__ float s_o[WPR > 1 ? kJoinThreads / 32 : 1][D], s_ml[kJoinThreads / 32][2];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.H * a.G;
@@ -193,7 +195,7 @@ template <typename T, int D>
 cudaError_t launch_join_width(const JoinArgs& a, int sms, int dev, cudaStream_t st) {
   const long long rows = (long long)a.T * a.H * a.G;
   // few rows may have many pieces each: several warps a row as long as all blocks fit the SMs at once
-  const long long fit = (long long)sms * join_blocks(D, 4) * (kJoinThreads / 32);
+  const long long fit = (long long)sms * join_blocks(D) * (kJoinThreads / 32);
   if (rows * 4 <= fit) return launch_join_one<T, D, 4>(a, dev, st);
   if (rows * 2 <= fit) return launch_join_one<T, D, 2>(a, dev, st);
   return launch_join_one<T, D, 1>(a, dev, st);

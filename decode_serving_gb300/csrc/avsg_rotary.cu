@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
   const int t0 = blockIdx.x * TOK;
   const int groups = half / VEC, units = a.unit_heads * a.per_head;
   griddep_wait();
-  bool latched = load_err(a.err) != 0;
+  const bool latched = load_err(a.err) != 0;
+  int bad_axis = -1;
 
   // One place of one head: values d0 .. and d1 .. of it (d1 < 0: one chunk alone; d0 < 0: none).
   const T* src;
@@ -144,6 +145,21 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
       if (d1 >= 0) x1[j].raw = __ldcs(reinterpret_cast<const typename Chunk<2 * VEC>::type*>(p + d1));
     }
   };
+  // With several axes, the first angle's axis and its token's positions on three of them before all
+  // else: one load behind the other cost 2 us more.
+  struct Place {
+    int axis, pos[3];
+  } ahead = {0, {0, 0, 0}};
+  auto fetch = [&](int x) {
+    Place p;
+    const int j = x / half, i = x - j * half, t = min(t0 + j, a.T - 1);
+    p.axis = a.axis[i];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) p.pos[k] = a.pos[(long long)(k < a.axes ? k : 0) * a.T + t];
+    return p;
+  };
+  if constexpr (AXES)
+    if (tid < TOK * half) ahead = fetch(tid);
   // The first place's rows are on their way while slots are read and angles computed (rows of
   // padding are read too, but go nowhere).
   int u = blockIdx.y * blockDim.x + tid;
@@ -161,22 +177,30 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(RotArgs a) {
   for (int x = tid; x < TOK * half; x += blockDim.x) {
     const int j = x / half, i = x - j * half, t = t0 + j;
     if (t >= a.T) break;
-    long long at = t;
+    int pos;
     if constexpr (AXES) {
-      int axis = a.axis[i];
-      if (axis < 0 || axis >= a.axes) {    // (every CTA sees every pair: nothing is written)
-        raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, i);
-        latched = true;
-        axis = 0;
+      // (Every CTA sees every pair: nothing is written.  Latched behind the loop: inside it, the branch
+      // cost a long prompt 15 us of 72.)
+      Place p = ahead;
+      if (x != tid) p = fetch(x);
+      if (p.axis < 0 || p.axis >= a.axes) {
+        bad_axis = i;
+        p.axis = 0;
       }
-      at += (long long)axis * a.T;
+      pos = p.axis == 0 ? p.pos[0] : p.axis == 1 ? p.pos[1] : p.pos[2];
+      if (p.axis > 2) pos = a.pos[(long long)p.axis * a.T + t];
+    } else {
+      pos = a.pos[t];
     }
-    const unsigned long long turn = (unsigned long long)(long long)a.pos[at] * a.freq[i];
+    const unsigned long long turn = (unsigned long long)(long long)pos * a.freq[i];
     float sn, cs;
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
     s_cs[x] = make_float2(cs * a.magnitude, sn * a.magnitude);
   }
-  if (__syncthreads_or(latched)) return;
+  if (__syncthreads_or(latched || bad_axis >= 0)) {
+    if (bad_axis >= 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, bad_axis);
+    return;
+  }
   griddep_launch();
 
   for (;;) {

@@ -614,12 +614,17 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
   while (walk.next(a, pc)) {
     const int rows = pc.ntok * a.G, count = pc.count, h = pc.h;
     const int32_t* table = a.tables + (size_t)pc.r * a.max_pages;
-    auto find_row = [&](int i) -> long long {        // row of key (tid % KT) of the i-th tile
+    // Row of key (tid % KT) of the i-th tile, in two steps: its page, and a tile later, when the page has
+    // come, the row (a check right behind the load holds the tile up for as long as the load takes).
+    constexpr int32_t kNoPage = INT_MIN;
+    auto find_page = [&](int i) -> int32_t {
       const int j = pc.j0 + i * KT + (tid & (KT - 1));
-      if (i >= count || j >= pc.limit) return -1;
-      const int32_t page = __ldg(table + (j >> a.shift));
+      return i < count && j < pc.limit ? __ldg(table + (j >> a.shift)) : kNoPage;
+    };
+    auto row_of = [&](int i, int32_t page) -> long long {
+      const int j = pc.j0 + i * KT + (tid & (KT - 1));
       if (page < 0 || page >= a.num_pages) {
-        raise_error(a.err, AVSG_ERR_BAD_SELECTION, pc.r, j);
+        if (i < count && j < pc.limit) raise_error(a.err, AVSG_ERR_BAD_SELECTION, pc.r, j);
         return -1;
       }
       return (((long long)page * a.H + h) << a.shift) + (j & ((1 << a.shift) - 1));
@@ -640,11 +645,11 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
 
     __syncthreads();                                 // the stages are free (earlier segment)
     if (tid < KT) {
-      long long rr[S - 1];
+      int32_t page[S - 1];
 #pragma unroll
-      for (int i = 0; i < S - 1; ++i) rr[i] = find_row(i);
+      for (int i = 0; i < S - 1; ++i) page[i] = find_page(i);
 #pragma unroll
-      for (int i = 0; i < S - 1; ++i) s_row[i * KT + tid] = rr[i];
+      for (int i = 0; i < S - 1; ++i) s_row[i * KT + tid] = row_of(i, page[i]);
     }
     if (!pc.chain && tid >= KT && tid - KT < pc.n) {
       const unsigned long long w = a.mask[pc.f + tid - KT];
@@ -656,7 +661,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
       if (i < count) issue(i);
       cp_commit();
     }
-    long long next_row = tid < KT ? find_row(S - 1) : -1;
+    int32_t next_page = tid < KT ? find_page(S - 1) : kNoPage;
 
     // The two rows of this thread.
     int tok[2], q_pos[2];
@@ -717,12 +722,12 @@ __global__ void __launch_bounds__(SH::THREADS, SH::CTAS_PER_SM) tree_attn_kernel
 
     for (int i = 0; i < count; ++i) {
       const int st = i % S;
-      if (tid < KT) s_row[((i + S - 1) % S) * KT + tid] = next_row;
+      if (tid < KT) s_row[((i + S - 1) % S) * KT + tid] = row_of(i + S - 1, next_page);
       cp_wait<S - 2>();
       __syncthreads();                               // tile i is here; stage (i - 1) % S is free
       if (i + S - 1 < count) issue((i + S - 1) % S);
       cp_commit();
-      if (tid < KT) next_row = find_row(i + S);
+      if (tid < KT) next_page = find_page(i + S);
 
       unsigned char* kst = smem + st * 2 * SH::TILE;
       const uint32_t ka = smem_u32(kst), va = ka + SH::TILE;

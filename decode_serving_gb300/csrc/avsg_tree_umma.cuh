@@ -1001,7 +1001,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       }
     };
     while (more && (buf & 1) != part) step();
-    int page = -1, group = 0, is_v = 0, to = 0, use = 0;  // this warp's next load, this lane's box
+    // This warp's next load, this lane's box.  Its page is checked when it is used: right behind the
+    // lookup, the check would hold the load before it up.
+    int page = -1, group = 0, is_v = 0, to = 0, use = 0, of = 0, key = -1;
     int end = 0;                           // the loads before this one were issued
     auto look_up = [&]() {
       const bool two = !SOLO && s.ntok * a.G > UM;
@@ -1018,14 +1020,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         t = z >= pairs ? s.count - 2 + z - pairs : (z >> 1) + ((z & 1) ? 2 : 0);
       }
       const int j = s.j0 + (s.count - 1 - t) * UT + lane * ua.box_rows;
-      page = -1;
+      page = key = -1;
       if (lane < boxes && j < s.limit) {
         page = __ldg(a.tables + (size_t)s.r * a.max_pages + (j >> a.shift));
         group = ((s.h << a.shift) + (j & ((1 << a.shift) - 1))) >> 3;
-        if (page < 0 || page >= a.num_pages) {
-          raise_error(a.err, AVSG_ERR_BAD_SELECTION, s.r, j);
-          page = -1;
-        }
+        of = s.r;
+        key = j;
       }
       to = buf;
       use = idx / kRing;
@@ -1037,9 +1037,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     uint64_t policy = 0;
     if constexpr (SHARED) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     while (have) {
-      const int now = page, now_group = group, now_v = is_v, b = to, phase = use;
+      int now = page;
+      const int now_group = group, now_v = is_v, b = to, phase = use, now_of = of, now_key = key;
       have = more;
       if (more) look_up();
+      if (now < 0 || now >= a.num_pages) {
+        if (now_key >= 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, now_of, now_key);
+        now = -1;
+      }
       const int n = __popc(__ballot_sync(0xffffffffu, now >= 0));
       if (!__all_sync(0xffffffffu, bar_wait(empty(b), (phase & 1) ^ 1, waits))) break;
       end = phase * kRing + b + 1;
