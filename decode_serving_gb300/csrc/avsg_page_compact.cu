@@ -8,10 +8,15 @@
 // live - 1 - (x - f(x)) from the last one backwards.
 //
 // What bounds it: the pages that move, read once and written once in every
-// layer.  The bitmap, its sums, the list of holes and the check of all held
-// entries are one cluster's work (latency); everything is written by the
-// second kernel, which takes tables, shares and stack element by element, so
-// that outputs may be the inputs, and pages in pieces of 4 KB by the warp.
+// layer.  The bitmap, its sums, the lists of holes and movers and the check of
+// all held entries come before (latency): for pools of up to 65536 pages every
+// CTA builds the bitmap in its own shared memory, and no CTA needs another one;
+// for larger ones it is one cluster's work, in global memory.  Everything else
+// is written by the second kernel, which takes tables, shares and stack
+// element by element, so that outputs may be the inputs, and pages in pieces of 4 KB by the warp.
+// Measured: 64 requests of up to 1500 tokens, a third of the pool free, 8
+// layers, 0.54 GB of K and V moved: 176 us (6.1 TB/s read and written, 90% of the copy's
+// rate); a pool of one layer and 150 pages 10.4 us (12.7 with the cluster's barriers).
 #include <cooperative_groups.h>
 
 #include "avsg_paged.cuh"
@@ -43,6 +48,45 @@ struct CompactArgs {
 
 __device__ __forceinline__ int free_before(const uint32_t* bits, const int32_t* before, int id) {
   return __ldcg(before + (id >> 5)) + __popc(__ldcg(bits + (id >> 5)) & ((1u << (id & 31)) - 1));
+}
+
+// One word's results: free ids before it, its holes and movers.  sum: free ids before the word.
+__device__ __forceinline__ void list_word(const CompactArgs& a, int live, int w, uint32_t b, int sum) {
+  a.bits[w] = b;
+  a.before[w] = sum;
+  if (live >> 5 == w) {
+    a.live[0] = live;
+    a.live[1] = sum + __popc(b & ((1u << (live & 31)) - 1));
+  }
+  // (the ids of the word that lie in the pool)
+  const uint32_t ids = a.num_pages - w * 32 >= 32 ? 0xffffffffu : (1u << (a.num_pages - w * 32)) - 1;
+  if (w >= live >> 5)
+    for (uint32_t u = ~b & ids; u; u &= u - 1) {
+      const int x = __ffs(u) - 1, id = w * 32 + x;
+      if (id >= live) a.movers[live - 1 - (id - sum - __popc(b & ((1u << x) - 1)))] = id;
+    }
+  for (; b; b &= b - 1, ++sum) {
+    const int id = w * 32 + __ffs(b) - 1;
+    if (id < live) a.holes[sum] = id;
+  }
+}
+// What request r holds lies in the pool and is in use (a warp).
+template <typename F>
+__device__ __forceinline__ void check_held(const CompactArgs& a, int r, F&& is_free) {
+  const int len = a.len[r];
+  const long long held = ((long long)len + (1 << a.shift) - 1) >> a.shift;
+  if (len < 0 || held > a.max_pages) {
+    raise_error(a.err, len < 0 ? AVSG_ERR_BAD_SELECTION : AVSG_ERR_CAPACITY, r, -1);
+    return;
+  }
+  const int32_t* row = a.tables + (size_t)r * a.max_pages;
+  int bad = -1;                            // (latched behind the loop, which then has its loads side by side)
+#pragma unroll 4
+  for (int x = threadIdx.x & 31; x < (int)held; x += 32) {
+    const int32_t id = row[x];
+    if (id < 0 || id >= a.num_pages || is_free(id)) bad = x;
+  }
+  if (bad >= 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, bad);
 }
 
 __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(CompactArgs a) {
@@ -86,25 +130,9 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(CompactAr
   for (int c = 0; c < rank; ++c) sum += s_sum[c];
   if (ok)
     for (int w = w0; w < w1; ++w) {
-      uint32_t b = __ldcg(a.bits + w);
-      a.before[w] = (int)sum;
-      if (live >> 5 == w) {
-        // (the word that `live` lies in; it has none where every page is free or in use up to the last word's end)
-        const int low = (int)sum + __popc(b & ((1u << (live & 31)) - 1));
-        a.live[0] = live;
-        a.live[1] = low;
-      }
-      // (the ids of the word that lie in the pool)
-      const uint32_t ids = a.num_pages - w * 32 >= 32 ? 0xffffffffu : (1u << (a.num_pages - w * 32)) - 1;
-      if (w >= live >> 5)
-        for (uint32_t u = ~b & ids; u; u &= u - 1) {
-          const int x = __ffs(u) - 1, id = w * 32 + x;
-          if (id >= live) a.movers[live - 1 - (id - (int)sum - __popc(b & ((1u << x) - 1)))] = id;
-        }
-      for (; b; b &= b - 1, ++sum) {
-        const int id = w * 32 + __ffs(b) - 1;
-        if (id < live) a.holes[sum] = id;
-      }
+      const uint32_t b = __ldcg(a.bits + w);
+      list_word(a, live, w, b, (int)sum);
+      sum += __popc(b);
     }
   if (ok && at == 0 && live >> 5 >= a.words) {  // every page is in use
     a.live[0] = live;
@@ -112,21 +140,50 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(CompactAr
   }
   // what the requests hold lies in the pool and is in use
   if (ok)
-    for (int r = at >> 5; r < a.R; r += threads >> 5) {
-      const long long held = ((long long)a.len[r] + (1 << a.shift) - 1) >> a.shift;
-      if (a.len[r] < 0 || held > a.max_pages) {
-        raise_error(a.err, a.len[r] < 0 ? AVSG_ERR_BAD_SELECTION : AVSG_ERR_CAPACITY, r, -1);
-        continue;
-      }
-      const int32_t* row = a.tables + (size_t)r * a.max_pages;
-#pragma unroll 4
-      for (int x = at & 31; x < (int)held; x += 32) {
-        const int32_t id = row[x];
-        if (id < 0 || id >= a.num_pages || (__ldcg(a.bits + (id >> 5)) >> (id & 31) & 1))
-          raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, x);
-      }
-    }
+    for (int r = at >> 5; r < a.R; r += threads >> 5)
+      check_held(a, r, [&](int id) { return __ldcg(a.bits + (id >> 5)) >> (id & 31) & 1; });
   cluster.sync();                          // (no CTA ends while another may write its s_sum)
+}
+
+constexpr int kSmallPool = 65536;          // pages whose bitmap every CTA builds for itself
+__global__ void __launch_bounds__(kCompactThreads) compact_plan_small_kernel(CompactArgs a) {
+  __shared__ uint32_t s_bits[kSmallPool / 32];
+  __shared__ int s_warp[kCompactThreads / 32];
+  constexpr int kEach = kSmallPool / 32 / kCompactThreads;  // words of a thread
+  const int tid = threadIdx.x;
+  for (int w = tid; w < a.words; w += kCompactThreads) s_bits[w] = 0;
+  griddep_wait();
+  const bool latched = load_err(a.err) != 0;
+  const int count = *a.count;
+  const bool fits = count >= 0 && count <= a.num_pages;
+  if (!fits && !latched && tid == 0 && blockIdx.x == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, -1);
+  if (__syncthreads_or(latched || !fits)) return;
+  griddep_launch();
+  int bad = -1;
+  for (int i = tid; i < count; i += kCompactThreads) {
+    const int32_t id = a.free_list[i];
+    if (id < 0 || id >= a.num_pages || (atomicOr(s_bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1)) bad = i;
+  }
+  if (bad >= 0 && blockIdx.x == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, bad);
+  if (__syncthreads_or(bad >= 0)) return;
+  const int live = a.num_pages - count;
+  if (blockIdx.x == 0) {
+    const int w0 = min(a.words, tid * kEach), w1 = min(a.words, w0 + kEach);
+    int mine = 0, all;
+    for (int w = w0; w < w1; ++w) mine += __popc(s_bits[w]);
+    int sum = block_exclusive(mine, s_warp, &all);
+    for (int w = w0; w < w1; ++w) {
+      list_word(a, live, w, s_bits[w], sum);
+      sum += __popc(s_bits[w]);
+    }
+    if (tid == 0 && live >> 5 >= a.words) {  // every page is in use
+      a.live[0] = live;
+      a.live[1] = 0;
+    }
+  }
+  const int warps = gridDim.x * (kCompactThreads / 32);
+  for (int r = blockIdx.x * (kCompactThreads / 32) + (tid >> 5); r < a.R; r += warps)
+    check_held(a, r, [&](int id) { return s_bits[id >> 5] >> (id & 31) & 1; });
 }
 
 struct PackArgs {
@@ -274,7 +331,12 @@ extern "C" int avsg_page_compact(const avsg_pages* p, const int32_t* d_shares, i
   const int64_t most = (int64_t)c.R * c.max_pages > c.num_pages ? (int64_t)c.R * c.max_pages : c.num_pages;
   int ctas = 1;
   while (ctas < kCompactCluster && ctas * kCompactThreads < most) ctas *= 2;
-  cudaError_t e = launch_pdl_cluster(ctas, compact_plan_kernel, dim3(ctas), dim3(kCompactThreads), 0, st, c);
+  // (a small pool: as many CTAs as the requests have warps, at most 32; each reads the whole stack)
+  const int rows = (c.R + kCompactThreads / 32 - 1) / (kCompactThreads / 32);
+  cudaError_t e =
+      c.num_pages <= kSmallPool
+          ? launch_pdl(compact_plan_small_kernel, dim3(rows < 32 ? rows : 32), dim3(kCompactThreads), 0, st, c)
+          : launch_pdl_cluster(ctas, compact_plan_kernel, dim3(ctas), dim3(kCompactThreads), 0, st, c);
   if (e == cudaSuccess) {
     const int64_t half = (c.num_pages + 1) / 2;            // no more pages move
     const int64_t warps = half * a.num_layers * 2 * ((a.page_chunks + kPackPiece - 1) / kPackPiece);

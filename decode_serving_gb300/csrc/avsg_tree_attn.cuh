@@ -23,7 +23,7 @@
 //   page ids looked up one tile ahead; rows past the end are zero-filled;
 // * scores, the running maximum and sum, and the output stay in registers
 //   (fp32); P is rounded to the cache's type for the second product, half a
-//   step and the only rounding before the last one (avsg_tree_umma.cu).
+//   step and the only rounding before the last one (avsg_tree_umma.cuh).
 // Measured (GB300, 6.78 TB/s copy): 64 requests x 8 kv-heads of 1000 tokens,
 // one token each, 4 query heads of 128: 57 us, 4.6 TB/s; 8 x 8 of 4000: 34 us;
 // one request of 4096 tokens and one head: 11 us with its merge, of which
@@ -100,7 +100,7 @@ struct TreeArgs {
 cudaError_t launch_tree_d64(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 cudaError_t launch_tree_d128(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
 cudaError_t launch_tree_d256(const TreeArgs& a, int dtype, int wm, int dev, cudaStream_t st);
-// Pages of at least 8 tokens, 256 rows per m-tile, 128 for D of 256 (avsg_tree_umma.cu).
+// Pages of at least 8 tokens, 256 rows per m-tile, 128 for D of 256 (avsg_tree_umma.cuh).
 cudaError_t launch_tree_umma(const TreeArgs& a, int dtype, int D, int dev, cudaStream_t st);
 // One part of an attention over common prefixes, without the joining of its pieces.
 cudaError_t launch_prefix_part(const TreeArgs& a, int dtype, int D, int wm, int dev, cudaStream_t st);
@@ -111,7 +111,7 @@ namespace tree {
 constexpr int KT = 64;           // keys per tile
 // fp16 weights are held times 2^6: the smallest normal one is then 2^-20 of
 // the largest, not 2^-14; with the 2^8 that a weight may reach relative to a
-// maximum not yet followed (avsg_tree_umma.cu) it is far from the type's end.
+// maximum not yet followed (avsg_tree_umma.cuh) it is far from the type's end.
 constexpr float kHalfShift = 6.f;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -45,7 +45,7 @@ inline Plan plan_kernel(bool umma, int D, int64_t rows, int sms) {
 }
 inline Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
   const int64_t rows = (int64_t)G * max_new;
-  // tcgen05 (avsg_tree_umma.cu): boxes of whole 8-row groups.  It always works on 128 rows; with
+  // tcgen05 (avsg_tree_umma.cuh): boxes of whole 8-row groups.  It always works on 128 rows; with
   // few rows it pays where contexts are long (8 x 8 units, one token, 16000 tokens: 91 us against
   // 99; 32 x 8 units, 32 rows, 3000 tokens: 80 against 89) and costs 4 to 10 us a call where they
   // are short (8 x 8 units, one token, 300 tokens: 17.4 against 11.6; 32 x 8 units, 32 rows, 50

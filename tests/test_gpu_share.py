@@ -187,6 +187,9 @@ def test_a_request_with_shared_pages_does_not_end_by_keep():
     ([300, 255, 1, 90], 16, 31, 3, 2, 128),                # several pieces of a page, 32 ids a word
     (list(range(0, 400, 3)), 8, 700, 1, 1, 16),
     ([2000, 33], 256, 17, 2, 1, 256),
+    ([50000, 0, 15000], 1, 536, 1, 1, 8),                  # 65536 pages, and more than a CTA's bitmap holds
+    ([50000, 0, 15000], 1, 537, 1, 1, 8),
+    ([60000, 9, 70000], 1, 60001, 1, 1, 8),
 ])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_compact(lens, page, spare, layers, heads, dim, in_place):
@@ -231,8 +234,9 @@ def test_compact_without_shares():
 
 @pytest.mark.parametrize("what,code", [("twice", -4), ("range", -4), ("count", -4), ("free page", -4), ("page", -4),
                                        ("length", -4), ("columns", -2)])
-def test_compact_errors_change_nothing(what, code):
-    p = Pool([40, 9, 100], 8, spare=12)
+@pytest.mark.parametrize("spare", [12, 70000])
+def test_compact_errors_change_nothing(what, code, spare):
+    p = Pool([40, 9, 100], 8, spare=spare)
     c = p.cache
     if what == "twice":
         c.free[1] = c.free[0]
