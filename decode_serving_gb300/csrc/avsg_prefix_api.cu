@@ -215,6 +215,21 @@ cudaError_t launch_join(const JoinArgs& a, int D, int sms, int dev, cudaStream_t
                     : launch_join_width<T, 256>(a, sms, dev, st);
 }
 
+// What a CTA takes for a unit's beginning and end, a tile, and on tcgen05 a tile of up to 128 rows,
+// in hundredths of a microsecond: least squares over the CTAs of several calls (GB300; wm 2 between its
+// neighbours).  Tiles are 128 keys on tcgen05, 64 with mma.sync and for heads of 256.
+struct CtaCost {
+  int begin, tile, small;
+};
+CtaCost cta_cost(const Plan& x, int D) {
+  const int w = D == 64 ? 0 : D == 128 ? 1 : 2;
+  static const CtaCost umma[3] = {{600, 153, 88}, {950, 158, 105}, {1040, 84, 84}};
+  static const CtaCost mma[3][3] = {{{330, 85, 85}, {400, 125, 125}, {590, 170, 170}},
+                                    {{400, 105, 105}, {500, 165, 165}, {650, 210, 210}},
+                                    {{450, 130, 130}, {700, 212, 212}, {700, 250, 250}}};
+  return x.umma ? umma[w] : mma[x.wm == 4 ? 2 : x.wm - 1][w];
+}
+
 struct PrefixWork {
   size_t unit[2], rows_ml[2], rows[2], part[2], bytes;
 };
@@ -270,22 +285,24 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
   a.token = x->d_token;
   a.request = x->d_request;
   a.sms = sms;
-  a.lead = 1000;                           // 10 us
   JoinArgs j{};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Plan plans[2] = {plan_attention(p, G, t->num_tokens, sms), plan_attention(p, G, t->max_new, sms)};
+  const Plan plans[2] = {plan_attention(p, G, t->num_tokens, sms), plan_attention(p, G, t->max_new, sms)};
+  CtaCost cost[2];
   for (int i = 0; i < 2; ++i) {
-    Plan& plan = plans[i];
-    // a unit takes 4 us and 1.2 a tile with mma.sync; on tcgen05 9 us and 1.6, with up to 128 rows 7.7 and 1.1
-    plan.begin = !plan.umma ? 3 : i == 0 ? 6 : 7;
-    a.cost[i].keys = plan.umma && D != 256 ? 128 : 64;
-    a.cost[i].tpm = plan.MT / G;
-    a.cost[i].begin = plan.begin;
-    // (in hundredths of a microsecond; part 1, whose units end one by one, counts a fifth more)
-    a.cost[i].tile = plan.tile * (i == 0 ? 10 : 12);
-    a.cost[i].small = plan.small * (i == 0 ? 10 : 12);
-    a.cost[i].per_sm = plan.ctas / sms;
+    cost[i] = cta_cost(plans[i], D);
+    TreeArgs::Cost& c = a.cost[i];
+    c.per_sm = plans[i].ctas / sms;
+    c.keys = plans[i].umma && D != 256 ? 128 : 64;
+    c.tpm = plans[i].MT / G;
+    // (part 1's CTAs end less evenly, 10% behind their median)
+    const int num = i == 0 ? 10 : 11, den = 10 * c.per_sm;
+    c.begin = cost[i].begin * num / den;
+    c.tile = cost[i].tile * num / den;
+    c.small = cost[i].small * num / den;
   }
+  // Cutting a list into shares splits about a unit per CTA, which pays for a beginning and an end more.
+  a.lead = a.cost[0].begin > a.cost[1].begin ? a.cost[0].begin - a.cost[1].begin : 0;
   for (int i = 0; i < 2; ++i) {
     const Plan& plan = plans[i];
     const Workspace l = tree_layout(plan, D);
@@ -298,13 +315,15 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
     b.partial = reinterpret_cast<float*>(work + w.part[i] + l.part);
     b.tpm = plan.MT / G;
     b.ctas = plan.ctas;
+    // Places of the list: of a tile by its cost, of a unit's beginning and end in tiles.
     b.w_full = b.w_small = 1;
     if (i == 0 && plan.umma && D != 256) {
-      b.w_full = 3;
-      b.w_small = 2;
+      b.w_full = D == 64 ? 5 : 3;
+      b.w_small = D == 64 ? 3 : 2;
       b.small_rows = plan.MT / 2;
     }
-    b.begin = plan.begin * b.w_full;
+    const int tile = i == 0 ? cost[i].tile : cost[i].small;
+    b.begin = (cost[i].begin + tile / 2) / tile * b.w_full;
     b.min_tiles = 2 * b.w_full;
     j.part[i] = JoinPart{b.unit, b.rows, b.rows_ml, b.partial, b.ml, plan.ctas, plan.MT};
     const cudaError_t e = plan.umma ? launch_prefix_umma(b, p->dtype, D, dev, st)

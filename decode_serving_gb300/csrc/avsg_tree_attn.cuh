@@ -77,7 +77,8 @@ struct TreeArgs {
   // How the SMs are divided between the parts, by what their lists cost (in hundredths of an SM's
   // microsecond; nothing but the time depends on it).
   struct Cost {
-    int keys, tpm, begin;        // keys of a tile, tokens per m-tile, see `begin`
+    int keys, tpm;               // keys of a tile, tokens per m-tile
+    int begin;                   // of a unit's beginning and end
     int tile, small;             // of a tile, with more than half an m-tile's rows and with fewer
     int per_sm;                  // CTAs
   } cost[2];
@@ -353,7 +354,7 @@ __device__ __forceinline__ float part_cost(const TreeArgs& a, int part, int r) {
   }
   const int full = n / c.tpm, rest = n - full * c.tpm;
   const float tiles = (float)((keys + c.keys - 1) / c.keys);
-  return (float)(c.begin * c.tile) * (float)(full + (rest > 0)) +
+  return (float)c.begin * (float)(full + (rest > 0)) +
          tiles * ((float)full * (float)c.tile + (float)(rest == 0 ? 0 : 2 * rest > c.tpm ? c.tile : c.small));
 }
 

@@ -17,7 +17,6 @@ struct Plan {
   int MT;      // rows per m-tile
   int ctas;
   int begin;   // see TreeArgs
-  int tile, small;  // (attention over prefixes) see TreeArgs::Cost
 };
 inline Plan plan_kernel(bool umma, int D, int64_t rows, int sms) {
   Plan x;
@@ -32,15 +31,6 @@ inline Plan plan_kernel(bool umma, int D, int64_t rows, int sms) {
   // with 4.
   x.begin = !umma ? 1 : (rows > 32 ? 6 : 4) + (D == 256 ? 2 : 0);
   x.ctas = umma || D == 256 ? sms : 2 * sms;
-  // A tile alone on an SM's share of the bandwidth (GB300, heads of 128, measured): 128 keys and 256
-  // rows on tcgen05 1.6 us, up to 128 rows 1.1; 64 keys with mma.sync 0.7 (of two CTAs), with 64 rows 1.35.
-  // In proportion to the head's width; heads of 256 have 64 keys and 128 rows, and one CTA of mma.sync an SM.
-  if (umma) {
-    x.tile = D == 256 ? 14 : 16 * D / 128;
-    x.small = D == 256 ? 14 : 11 * D / 128;
-  } else {
-    x.tile = x.small = (x.wm == 4 ? 13 : x.wm == 2 ? 10 : 7) * D / 128;
-  }
   return x;
 }
 inline Plan plan_attention(const avsg_pages* p, int G, int max_new, int sms) {
