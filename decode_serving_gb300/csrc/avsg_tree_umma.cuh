@@ -543,32 +543,29 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       if (SHARED && a.part == 0 && mine) token = token_of<SHARED>(a, s, s.tok0 + lt);
       if (two || x == 0) {
         if (warp_live) {
+          // (Each lane finds its own row, the warp then loads row by row: the arithmetic of an address is
+          // a chain that few warps have nothing to put beside.)
           constexpr int LPR = D / 8, RPI = 32 / LPR;
-          const int ch = lane % LPR, rows = s.ntok * a.G, G = a.G;
-          int r = rl - lane + lane / LPR, at = (warp & 3) * 32 + lane / LPR, t = r / G, g = r - t * G;
-          const unsigned char* base =
-              a.q + ((long long)(s.f + s.tok0) * a.q_stride + (long long)s.h * G * D) * 2 + ch * 16;
-          const uint32_t to = smem + x * M::Q + (ch / 8) * 1024;
-#pragma unroll 4
-          for (int it = 0; it < 32 / RPI; ++it) {
-            const bool ok = r < rows;
-            const unsigned char* src = ok ? base + (t * a.q_stride + g * D) * 2 : a.q;
-            if constexpr (SHARED) {
-              const int of = __shfl_sync(0xffffffffu, token, it * RPI + lane / LPR);
-              if (a.part == 0 && ok) src = a.q + ch * 16 + ((long long)of * a.q_stride + ((long long)s.h * G + g) * D) * 2;
-            }
-            const uint32_t dst =
-                SOLO ? smem + M::STAGE + at * M::STAGE_ROW + ch * 16
-                     : to + (at / 8) * (1024 * COLS) + (at & 7) * 128 + (((ch & 7) ^ (at & 7)) << 4);
+          const int ch = lane % LPR, sub = lane / LPR;
+          const long long own =
+              ((long long)(SHARED && a.part == 0 ? token : s.f + s.tok0 + lt) * a.q_stride + (s.h * a.G + gg) * D) * 2;
+          const uint32_t to = SOLO ? smem + M::STAGE + ((warp & 3) * 32 + sub) * M::STAGE_ROW + ch * 16
+                                   : smem + x * M::Q + (ch / 8) * 1024 + (warp & 3) * (4 * 1024 * COLS);
+          const uint32_t shown = __ballot_sync(0xffffffffu, mine);
+#pragma unroll
+          for (int k = 0; k < 32; k += RPI) {
+            const bool ok = shown >> (k + sub) & 1;
+            const long long from = __shfl_sync(0xffffffffu, own, k + sub);
+            const unsigned char* src = a.q + (ok ? from + ch * 16 : 0);
+            const int r8 = (k & 7) | sub;              // the row in its group of 8
+            const uint32_t dst = SOLO ? to + k * M::STAGE_ROW
+                                      : to + (k / 8) * (1024 * COLS) + r8 * 128 + (((ch & 7) ^ r8) << 4);
             if (ua.q_vec) {
               cp_async16(dst, src, ok ? 16 : 0);
             } else {
 #pragma unroll
               for (int z = 0; z < 4; ++z) cp_async4(dst + 4 * z, src + 4 * z, ok ? 4 : 0);
             }
-            r += RPI;
-            at += RPI;
-            for (g += RPI; g >= G; g -= G) ++t;
           }
           cp_commit();
           q_loading = true;
@@ -910,6 +907,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         // rows: this warp's part of q's place, which the products are done with (4 KB of 32 rows by 32
         // columns, 16-byte chunks swapped by the row).  Up to 128 rows, m and l lie there too: read by now.
         const uint32_t shown = SHARED ? __ballot_sync(0xffffffffu, mine) : 0;
+        float* const first_row = a.partial + (slot - lane + (lane >> 3)) * D;
         unsigned char* const st = smem_raw + (SOLO ? M::STAGE + warp * 4096 : x * M::Q + (warp & 3) * (32 * D * 2));
 #pragma unroll 1
         for (int c = two ? 0 : x * (D / 64); c < (two ? D / 32 : (x + 1) * (D / 64)); ++c) {
@@ -934,9 +932,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int r = 4 * y + (lane >> 3);
-              const long long to_row = __shfl_sync(0xffffffffu, slot, r);
+              // a unit's rows lie one after the other, a token's where the token does
+              float* to_row = s.whole ? a.rows + __shfl_sync(0xffffffffu, slot, r) * D
+                                      : first_row + (4 * y) * D;
               if (shown >> r & 1)
-                *reinterpret_cast<float4*>(partial() + to_row * D + c * 32 + (lane & 7) * 4) =
+                *reinterpret_cast<float4*>(to_row + c * 32 + (lane & 7) * 4) =
                     *reinterpret_cast<const float4*>(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
             }
           } else if (!mine) {
