@@ -20,10 +20,10 @@
 // What bounds it: part 0 the tensor cores (from about 100 rows a group on), part
 // 1 HBM and what the beginnings and ends of its units take; K and V of a prefix are read once for
 // each 256 rows of its group.  Measured: 64 requests behind 32768 tokens, up to
-// 500 tokens of their own, one new token each, 8 kv-heads of 4: 67 us (the tree
-// attention reads 64 times the prefix, 1.3 ms at HBM's rate); one part after the other 88.  Of the 67: 4 us until
+// 500 tokens of their own, one new token each, 8 kv-heads of 4: 68 us (the tree
+// attention reads 64 times the prefix, 1.3 ms at HBM's rate); one part after the other 88.  Of the 68: 4 us until
 // both parts have found their shares, 50 for the parts, 2 between kernels, 5 for the join.
-// 69 requests with trees of up to 16 tokens in four groups of up to 32768: 306 to 312 us.
+// 69 requests with trees of up to 16 tokens in four groups of up to 32768: 298 to 305 us.
 #include "avsg_tree_plan.cuh"
 
 namespace avsg {
