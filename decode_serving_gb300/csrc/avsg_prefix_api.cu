@@ -21,9 +21,11 @@
 // 1 HBM and what the beginnings and ends of its units take; K and V of a prefix are read once for
 // each 256 rows of its group.  Measured: 64 requests behind 32768 tokens, up to
 // 500 tokens of their own, one new token each, 8 kv-heads of 4: 68 us (the tree
-// attention reads 64 times the prefix, 1.3 ms at HBM's rate); one part after the other 88.  Of the 68: 4 us until
+// attention, for which every request reads the prefix, 1030); one part after the other 88.  Of the 68: 4 us until
 // both parts have found their shares, 50 for the parts, 2 between kernels, 5 for the join.
 // 69 requests with trees of up to 16 tokens in four groups of up to 32768: 298 to 305 us.
+// Where no request has a group it costs 7 to 14 us more than the tree attention (64 requests alone,
+// one new token each: 58 and 44 us at 500 tokens, 334 and 327 at 8000).
 #include "avsg_tree_plan.cuh"
 
 namespace avsg {

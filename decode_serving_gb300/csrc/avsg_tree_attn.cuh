@@ -345,7 +345,7 @@ __device__ __forceinline__ float part_cost(const TreeArgs& a, int part, int r) {
   int n, keys;
   if (part == 0) {
     n = common > 0 ? max(a.group_first[r + 1] - a.group_first[r], 0) : 0;
-    keys = a.window > 0 ? min(common, a.window) : common;
+    keys = min(a.window > 0 ? min(common, a.window) : common, INT_MAX - 1024);
   } else {
     n = max(a.first[r + 1] - a.first[r], 0);
     keys = max(a.len[r] - common, 0);

@@ -256,6 +256,16 @@ def test_bad_inputs_are_latched(what, code):
     assert (s.out == 9.0).all()
 
 
+@pytest.mark.parametrize("shared", [2 ** 31 - 16, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("dim,new", [(64, 1), (64, 40), (256, 2)])
+def test_the_most_tokens_that_an_int_holds_are_no_prefix(shared, dim, new):
+    s = Shared([100, 90], [new, new], 16, 2, 4, dim, BF16, False, [((0, 1), 5)])
+    s.x.shared[0] = shared
+    s.out.fill_(9.0)
+    s.attend()
+    assert s.cache.error()[0] == -4
+
+
 def test_refusals():
     from decode_serving_gb300.avsg import AvsgError
     s = Shared([100, 90], [2, 2], 16, 2, 2, 64, BF16, True, [((0, 1), 5)])
