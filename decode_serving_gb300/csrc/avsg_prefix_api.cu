@@ -24,8 +24,10 @@
 // attention, for which every request reads the prefix, 1030); one part after the other 88.  Of the 68: 4 us until
 // both parts have found their shares, 50 for the parts, 2 between kernels, 5 for the join.
 // 69 requests with trees of up to 16 tokens in four groups of up to 32768: 298 to 305 us.
-// Where no request has a group it costs 7 to 14 us more than the tree attention (64 requests alone,
-// one new token each: 58 and 44 us at 500 tokens, 334 and 327 at 8000).
+// Where no request has a group it costs 7 to 19 us more than the tree attention (64 requests alone,
+// one new token each: 58 and 44 us at 500 tokens, 120 and 100 at 2000, 334 and 327 at 8000): the empty
+// part and the join, and part 1's kernel alone takes 13% more at 2000 tokens, of which twice the
+// stalls for instructions are seen, but neither its registers nor the order of its branches is the cause.
 #include "avsg_tree_plan.cuh"
 
 namespace avsg {
