@@ -67,23 +67,30 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(D)) prefix_join_kern
   const int part = warp % WPR;             // of the row's warps
   const long long row = (long long)blockIdx.x * ROWS + warp / WPR;
   const int t = (int)(row / heads), hg = (int)(row - (long long)t * heads), h = hg / a.G, g = hg - h * a.G;
-  if (t >= a.T) return;
-  const int tokens = a.first[a.R], latched = load_err(a.err);
-  const int4 own = a.part[1].unit[(long long)t * a.H + h];
-  int4 pre = a.part[0].unit[(long long)t * a.H + h];  // (any contents, where the token has no prefix)
-  // (own.y < 0: written by its part; a row's warps all leave or none)
-  if (latched != 0 || t >= tokens || own.y < 0) return;
+  // A row without anything to join has no pieces.  Its warps stay for the barrier below: each reads the
+  // error word for itself, and another row's warp may raise it between two reads.
+  bool live = t < a.T;
+  const int tokens = a.first[a.R];
+  const bool latched = __any_sync(0xffffffffu, load_err(a.err) != 0);
+  int4 own = make_int4(0, -1, 0, 0), pre = own;
+  if (live) {
+    own = a.part[1].unit[(long long)t * a.H + h];
+    pre = a.part[0].unit[(long long)t * a.H + h];  // (any contents, where the token has no prefix)
+  }
+  // (own.y < 0: written by its part)
+  live = live && !latched && t < tokens && own.y >= 0;
   if (!own.w) pre = make_int4(0, -1, 0, 0);
   auto pieces = [&](const int4& u) { return u.y < 0 ? 0 : u.y == 0 ? 1 : u.y; };
   auto fits = [&](const JoinPart& p, const int4& u) {
     return u.y <= 0 || (u.x >= 0 && u.x < p.ctas && u.y <= p.ctas - u.x && u.z >= 0 && u.z < p.MT / a.G);
   };
-  if ((own.w && pre.y < 0) || !fits(a.part[0], pre) || !fits(a.part[1], own)) {
+  if (live && ((own.w && pre.y < 0) || !fits(a.part[0], pre) || !fits(a.part[1], own))) {
     // (a token that no group lists)
     if (lane == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, t);
-    return;
+    live = false;
   }
-  const int n0 = pieces(pre), all = n0 + pieces(own);
+  if (WPR == 1 && !live) return;
+  const int n0 = pieces(pre), all = live ? n0 + pieces(own) : 0;
   const int n = (all - part + WPR - 1) / WPR;  // this warp's
   // where piece i lies among the part's partials or rows
   auto place = [&](int k, const float*& ml, const float*& o) {
@@ -155,18 +162,19 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(D)) prefix_join_kern
     }
   }
   if constexpr (WPR > 1) {
-    // the row's warps: one barrier of theirs, as other rows of the block may have left
 #pragma unroll
     for (int x = 0; x < VPL; ++x) s_o[warp][lane * VPL + x] = o[x];
     if (lane == 0) {
       s_ml[warp][0] = top;
-      s_ml[warp][1] = sum;
+      s_ml[warp][1] = live ? sum : -1.f;   // (a sum is never negative)
     }
+    // a barrier of the row's warps, to which all of them come (waiting for the block's other rows costs 0.8 us)
     asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WPR), "n"(32 * WPR) : "memory");
-    if (part != 0) return;
+    if (part != 0 || !live) return;
     float tops[WPR];
 #pragma unroll
     for (int w = 0; w < WPR; ++w) {
+      if (s_ml[warp + w][1] < 0.f) return; // a sibling saw an error: the row is written whole or not at all
       tops[w] = s_ml[warp + w][0];
       top = fmaxf(top, tops[w]);
     }
