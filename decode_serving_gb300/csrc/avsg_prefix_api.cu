@@ -46,11 +46,28 @@ struct JoinPart {
 struct JoinArgs {
   JoinPart part[2];
   const int32_t* first;
+  const int32_t* shared;         // the groups, see TreeArgs
+  const int32_t* group_first;
+  const int32_t* token;
   unsigned char* out;
   float* lse;
   DevErr* err;
-  int R, H, G, T;
+  int R, H, G, T, places;
+  unsigned checks;               // blocks that look at tokens, in front of those that join rows
 };
+
+// Whether token t, if it has a prefix, is in the list of a group with a prefix of that length.  The workspace
+// may hold another call's entries: one is this call's if the place that it names lies in the group that it
+// names and lists the token, as part 0 has then written the token's entries anew.
+__device__ __forceinline__ bool token_listed(const JoinArgs& a, int t) {
+  const int common = a.part[1].unit[(long long)t * a.H].w;
+  if (common == 0) return true;
+  const int4 pre = a.part[0].unit[(long long)t * a.H];
+  const int lead = pre.x >> 16;
+  const long long at = (long long)pre.w + pre.z;
+  if (lead < 0 || lead >= a.R || at < 0 || at >= a.places) return false;
+  return a.token[at] == t && a.shared[lead] == common && a.group_first[lead] <= at && at < a.group_first[lead + 1];
+}
 
 // WPR warps join the pieces of one row, each every WPR-th of them.  Two dependent chains of loads: where the pieces lie, then
 // their maxima, sums and outputs side by side, up to kJoinAhead outputs before the first weight is known.
@@ -64,8 +81,15 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(D)) prefix_join_kern
   __shared__ float s_o[WPR > 1 ? kJoinThreads / 32 : 1][D], s_ml[kJoinThreads / 32][2];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.H * a.G;
+  if (blockIdx.x < a.checks) {
+    // (in blocks of their own: in each row's way the check cost 2.4 us of 19 for 20 000 rows)
+    const long long t = (long long)blockIdx.x * kJoinThreads + threadIdx.x;
+    if (load_err(a.err) == 0 && t < min(a.T, a.first[a.R]) && !token_listed(a, (int)t))
+      raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, (int)t);
+    return;
+  }
   const int part = warp % WPR;             // of the row's warps
-  const long long row = (long long)blockIdx.x * ROWS + warp / WPR;
+  const long long row = (long long)(blockIdx.x - a.checks) * ROWS + warp / WPR;
   const int t = (int)(row / heads), hg = (int)(row - (long long)t * heads), h = hg / a.G, g = hg - h * a.G;
   // A row without anything to join has no pieces.  Its warps stay for the barrier below: each reads the
   // error word for itself, and another row's warp may raise it between two reads.
@@ -80,12 +104,12 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(D)) prefix_join_kern
   // (own.y < 0: written by its part)
   live = live && !latched && t < tokens && own.y >= 0;
   if (!own.w) pre = make_int4(0, -1, 0, 0);
+  pre.x &= 0xffff;                         // (see token_listed)
   auto pieces = [&](const int4& u) { return u.y < 0 ? 0 : u.y == 0 ? 1 : u.y; };
   auto fits = [&](const JoinPart& p, const int4& u) {
     return u.y <= 0 || (u.x >= 0 && u.x < p.ctas && u.y <= p.ctas - u.x && u.z >= 0 && u.z < p.MT / a.G);
   };
   if (live && ((own.w && pre.y < 0) || !fits(a.part[0], pre) || !fits(a.part[1], own))) {
-    // (a token that no group lists)
     if (lane == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, t);
     live = false;
   }
@@ -202,14 +226,15 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(D)) prefix_join_kern
 }
 
 template <typename T, int D, int WPR>
-cudaError_t launch_join_one(const JoinArgs& a, int dev, cudaStream_t st) {
+cudaError_t launch_join_one(JoinArgs a, int dev, cudaStream_t st) {
   constexpr int ROWS = kJoinThreads / 32 / WPR;
   static SmemSplit split;
   auto kernel = prefix_join_kernel<T, D, WPR>;
   const cudaError_t e = split.ask(reinterpret_cast<const void*>(kernel), dev);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.T * a.H * a.G;
-  return launch_pdl(kernel, dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(kJoinThreads), 0, st, a);
+  a.checks = ((unsigned)a.T + kJoinThreads - 1) / kJoinThreads;
+  return launch_pdl(kernel, dim3((unsigned)((rows + ROWS - 1) / ROWS) + a.checks), dim3(kJoinThreads), 0, st, a);
 }
 template <typename T, int D>
 cudaError_t launch_join_width(const JoinArgs& a, int sms, int dev, cudaStream_t st) {
@@ -289,7 +314,7 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
   const int D = p->head_dim, G = t->q_per_kv;
   const PrefixWork w = prefix_layout(p, G, t->max_new, t->num_tokens, sms);
   if (t->work_bytes < w.bytes) return AVSG_ERR_CAPACITY;
-  if ((int64_t)a.T * a.H * G > (int64_t)INT32_MAX * (kJoinThreads / 32)) return AVSG_ERR_CAPACITY;
+  if ((int64_t)a.T * a.H * G / (kJoinThreads / 32) + a.T / kJoinThreads + 2 > INT32_MAX) return AVSG_ERR_CAPACITY;
   unsigned char* work = static_cast<unsigned char*>(t->d_work);
   a.places = x->num_tokens;
   a.shared = x->d_shared;
@@ -343,6 +368,10 @@ extern "C" int avsg_prefix_attention(const avsg_pages* p, const avsg_tree* t, co
     if (e != cudaSuccess) return AVSG_ERR_CUDA;
   }
   j.first = t->d_first;
+  j.shared = a.shared;
+  j.group_first = a.group_first;
+  j.token = a.token;
+  j.places = a.places;
   j.out = a.out;
   j.lse = a.lse;
   j.err = a.err;

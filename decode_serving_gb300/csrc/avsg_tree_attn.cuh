@@ -91,8 +91,9 @@ struct TreeArgs {
   const int32_t* group_first;    // [R + 1] a leader's first place
   const int32_t* token;          // [places] the token in a place, and its request
   const int32_t* request;
-  int4* unit;                    // [T][H] {CTA of the unit's begin, pieces, its token, prefix}; pieces 0:
-                                 // a row of `rows`, -1: the output is written
+  int4* unit;                    // [T][H] {CTA of the unit's begin, pieces, number in the unit, tokens of the
+                                 // prefix}; pieces 0: a row of `rows`, -1: the output is written; of part 0
+                                 // {and the group's leader from bit 16 on, .., .., place of the unit's first}
   float* rows;                   // [T][H][G][D] outputs of units that lie in one share
   float* rows_ml;                // [T][H][G][2]
 };
@@ -553,12 +554,15 @@ __device__ __forceinline__ int member_position(const TreeArgs& a, const Piece& p
   const unsigned long long w = a.mask && a.first[r + 1] - f <= kMaxDrafts ? a.mask[t] : 0;
   return a.len[r] + (w ? __popcll(w) - 1 : t - f);
 }
-// (SHARED) Notes where the partial outputs of a unit's tokens lie; tid of `threads` threads.
+// (SHARED) Notes where the partial outputs of a unit's tokens lie; tid of `threads` threads.  (All but a
+// token's number is the unit's: with its place in the loop a step of draft trees took 332 us instead of 302.)
 __device__ __forceinline__ void note_unit(const TreeArgs& a, const Piece& p, int cta, int tid, int threads) {
-  const int prefix = a.part == 1 && a.shared[p.r] > 0;
+  static_assert(kMaxPagedRequests <= 1 << 15, "a leader and a CTA share a word");
+  const int prefix = a.part == 1 ? a.shared[p.r] : 0;
   const int pieces = !p.whole ? p.last - cta + 1 : a.part == 1 && !prefix ? -1 : 0;
+  const int from = a.part == 0 ? p.r << 16 | cta : cta, more = a.part == 0 ? p.f + p.tok0 : prefix;
   for (int x = tid; x < p.ntok; x += threads)
-    a.unit[(long long)token_of<true>(a, p, p.tok0 + x) * a.H + p.h] = make_int4(cta, pieces, x, prefix);
+    a.unit[(long long)token_of<true>(a, p, p.tok0 + x) * a.H + p.h] = make_int4(from, pieces, x, more);
 }
 
 template <typename T_, int D_, int WM_, bool SHARED_>

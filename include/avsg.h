@@ -636,9 +636,12 @@ int avsg_prefix_find(const avsg_pages* p, const int32_t* d_first, int32_t min_to
  *   t : as for avsg_tree_attention; t->d_work and t->work_bytes go by this
  *       operator's workspace, which grows with the tokens.
  *   x : the groups, as avsg_prefix_find wrote them for these tables, lengths
- *       and first tokens (arrays that do not fit them give undefined results;
- *       indices out of range are latched: BAD_SELECTION).
- * Every member's d_shared[r] must be its leader's.  Errors and rounding as avsg_tree_attention.
+ *       and first tokens.  Latched (BAD_SELECTION): indices out of range, and
+ *       a token of a request with a prefix (d_shared[r] > 0) that is not in the
+ *       list of a group whose leader has a prefix of that length.  Other
+ *       arrays that do not fit (a member whose first pages are not the
+ *       leader's) give undefined results.
+ * Errors and rounding as avsg_tree_attention; what a call that latches an error wrote is undefined.
  */
 int avsg_prefix_attention_workspace(const avsg_pages* p, int32_t q_per_kv, int32_t max_new, int32_t num_tokens,
                                     size_t* bytes);
