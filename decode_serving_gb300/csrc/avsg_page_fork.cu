@@ -20,7 +20,9 @@
 //     count            gains and losses added to each page's mark, the last request that touches it noted
 //     back             pages without a holder counted, piece by piece
 //     write            shares, free stack, then tables and lengths
-// with the hardware barriers of a cluster of up to 8 CTAs between the phases.
+// with the hardware barriers of a cluster of up to 8 CTAs between the phases.  Whether the fork
+// happens is one word, written by the check, and not the error word, which a call on another stream
+// may change between two CTAs' reads: a CTA that left would leave the others to write into its shared memory.
 // Only requests that become others are looked at, a row and its parent's side
 // by side; where their rows agree (beams and samples of one prompt, but for
 // the last pages) nothing is counted.  Nothing is written before every check has passed, but the check
@@ -62,7 +64,7 @@ struct ForkArgs {
   int32_t* aside;                          // [R][max_pages]
   int4* request;                           // [R] {length, parent, times, number of its copy or -1}
   int4* copies;                            // [R] {from, to, rows, 0}
-  int32_t* num_copies;                     // {copies, whether any page changes holders, free pages}
+  int32_t* num_copies;                     // {copies, whether any page changes holders, free pages, whether to go on}
   DevErr* err;
 };
 
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_check_kernel(ForkArgs a) {
     for (int r = r0; r < r1; ++r) s_request[r].w = copied(r) ? before++ : -1;
   __syncthreads();
 
-  bool any = false;
+  bool any = false, wrong = false;
   if (ok) {
     for (int r = rank * kForkThreads + tid; r < a.R; r += ctas * kForkThreads) {
       const int4 me = s_request[r];
@@ -200,10 +202,16 @@ __global__ void __launch_bounds__(kForkThreads) fork_check_kernel(ForkArgs a) {
       const int len = s_request[q].x;
       if ((len & page_mask) == 0) continue;
       const int32_t from = a.tables[(size_t)q * a.max_pages + (len >> a.shift)];
-      if (from < 0 || from >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, q, len >> a.shift);
+      if (from < 0 || from >= a.num_pages) {
+        raise_error(a.err, AVSG_ERR_BAD_SELECTION, q, len >> a.shift);
+        wrong = true;
+      }
       if (me.w >= 0) {
         const int to = a.free_list[count - 1 - me.w];
-        if (to < 0 || to >= a.num_pages) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, count - 1 - me.w);
+        if (to < 0 || to >= a.num_pages) {
+          raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, count - 1 - me.w);
+          wrong = true;
+        }
         a.copies[me.w] = make_int4(from, to, len & page_mask, 0);
       }
     }
@@ -211,8 +219,10 @@ __global__ void __launch_bounds__(kForkThreads) fork_check_kernel(ForkArgs a) {
       v.each_column(i, [&](int r, int x, bool loses, int32_t from, bool gains, int32_t to) {
         if (loses && (from < 0 || from >= a.num_pages)) {
           raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, x);
+          wrong = true;
         } else if (gains && (to < 0 || to >= a.num_pages)) {
           raise_error(a.err, AVSG_ERR_BAD_SELECTION, v.parent(r), x);
+          wrong = true;
         } else if (from != to) {
           any = true;
           if (loses) {
@@ -233,14 +243,19 @@ __global__ void __launch_bounds__(kForkThreads) fork_check_kernel(ForkArgs a) {
     }
   }
   any = __syncthreads_or(any);
+  ok = !__syncthreads_or(!ok || wrong);
   cluster.barrier_wait(std::move(started));
-  if (tid == 0) *cluster.map_shared_rank(&s_any[rank], 0) = any;
+  if (tid == 0) *cluster.map_shared_rank(&s_any[rank], 0) = ok ? any : -1;
   cluster.sync();
-  if (ok && rank == 0 && tid == 0) {
-    for (int c = 1; c < ctas; ++c) any |= s_any[c] != 0;
+  if (rank == 0 && tid == 0) {
+    for (int c = 1; c < ctas; ++c) {
+      any |= s_any[c] > 0;
+      ok &= s_any[c] >= 0;
+    }
     a.num_copies[0] = num_copies;
     a.num_copies[1] = any;
     a.num_copies[2] = count;
+    a.num_copies[3] = ok;
   }
 }
 
@@ -255,13 +270,13 @@ __global__ void __launch_bounds__(kWriteThreads, 3) fork_write_kernel(ForkArgs a
   const int items = a.R * a.pieces;
   // (every CTA of a copy has waited for the check before this one may begin)
   if (!a.beside) griddep_wait();
-  // every CTA sees the same word: all go on or none
-  if (load_err(a.err) != 0) {
+  // every CTA sees the same words: all go on or none
+  const int num_copies = __ldcg(a.num_copies), count = __ldcg(a.num_copies + 2);
+  const bool any = __ldcg(a.num_copies + 1) != 0;
+  if (__ldcg(a.num_copies + 3) == 0) {
     griddep_wait();
     return;
   }
-  const int num_copies = __ldcg(a.num_copies), count = __ldcg(a.num_copies + 2);
-  const bool any = __ldcg(a.num_copies + 1) != 0;
   for (int r = tid; r < a.R; r += kWriteThreads) s_request[r] = __ldcg(a.request + r);
   __syncthreads();
   const ForkView v{a, s_request};
@@ -374,7 +389,6 @@ struct ForkCopyArgs {
   unsigned char* v;
   const int4* copies;
   const int32_t* num_copies;
-  DevErr* err;
 };
 
 constexpr int kCopyThreads = 256;
@@ -385,7 +399,7 @@ constexpr int kCopyBlocks = 4;             // CTAs per SM
 __global__ void __launch_bounds__(kCopyThreads, 6) fork_copy_kernel(ForkCopyArgs a) {
   griddep_wait();
   griddep_launch();
-  if (load_err(a.err) != 0) return;
+  if (a.num_copies[3] == 0) return;
   const int lane = threadIdx.x & 31;
   const long long units = (long long)*a.num_copies * a.num_layers * 2 * a.H;
   const long long head_bytes = (long long)(a.chunks * 16) << a.shift;
@@ -504,7 +518,6 @@ extern "C" int avsg_page_fork(const avsg_pages* p, const int32_t* d_parent, int3
     c.v = static_cast<unsigned char*>(p->d_v);
     c.copies = a.copies;
     c.num_copies = a.num_copies;
-    c.err = a.err;
     // (no more CTAs than the copies of all requests have units)
     const int64_t most = ((int64_t)a.R * c.num_layers * 2 * c.H + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
     const int grid = most < kCopyBlocks * sms ? (int)most : kCopyBlocks * sms;
