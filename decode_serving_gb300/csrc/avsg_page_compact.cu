@@ -14,9 +14,11 @@
 // for larger ones it is one cluster's work, in global memory.  Everything else
 // is written by the second kernel, which takes tables, shares and stack
 // element by element, so that outputs may be the inputs, and pages in pieces of 4 KB by the warp.
+// It goes by what every CTA of the first one found, and not by the error word, which a call on another
+// stream may change between two CTAs' reads: part of the pages would move.
 // Measured: 64 requests of up to 1500 tokens, a third of the pool free, 8
-// layers, 0.54 GB of K and V moved: 176 us (6.1 TB/s read and written, 90% of the copy's
-// rate); a pool of one layer and 150 pages 10.4 us (12.7 with the cluster's barriers).
+// layers, 0.54 GB of K and V moved: 177 us (6.1 TB/s read and written, 90% of the copy's
+// rate); a pool of one layer and 150 pages 10.5 us (12.7 with the cluster's barriers).
 #include <cooperative_groups.h>
 
 #include "avsg_paged.cuh"
@@ -43,8 +45,11 @@ struct CompactArgs {
   int32_t* holes;                          // [num_pages / 2 + 1]
   int32_t* movers;                         // [num_pages / 2 + 1], the last one first
   int32_t* live;                           // {live pages, free ids below that: the pages that move}
+  int32_t* fine;                           // [ctas] whether the checks of a CTA of the first kernel passed
+  int ctas;
   DevErr* err;
 };
+constexpr int kMostPlanCtas = 32;          // (a warp of the second kernel reads their words)
 
 __device__ __forceinline__ int free_before(const uint32_t* bits, const int32_t* before, int id) {
   return __ldcg(before + (id >> 5)) + __popc(__ldcg(bits + (id >> 5)) & ((1u << (id & 31)) - 1));
@@ -70,13 +75,14 @@ __device__ __forceinline__ void list_word(const CompactArgs& a, int live, int w,
     if (id < live) a.holes[sum] = id;
   }
 }
-// What request r holds lies in the pool and is in use (a warp).
+// What request r holds lies in the pool and is in use (a warp); *fine is 0 afterwards if it does not.
 template <typename F>
-__device__ __forceinline__ void check_held(const CompactArgs& a, int r, F&& is_free) {
+__device__ __forceinline__ void check_held(const CompactArgs& a, int r, int32_t* fine, F&& is_free) {
   const int len = a.len[r];
   const long long held = ((long long)len + (1 << a.shift) - 1) >> a.shift;
   if (len < 0 || held > a.max_pages) {
     raise_error(a.err, len < 0 ? AVSG_ERR_BAD_SELECTION : AVSG_ERR_CAPACITY, r, -1);
+    *fine = 0;
     return;
   }
   const int32_t* row = a.tables + (size_t)r * a.max_pages;
@@ -86,7 +92,10 @@ __device__ __forceinline__ void check_held(const CompactArgs& a, int r, F&& is_f
     const int32_t id = row[x];
     if (id < 0 || id >= a.num_pages || is_free(id)) bad = x;
   }
-  if (bad >= 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, bad);
+  if (bad >= 0) {
+    raise_error(a.err, AVSG_ERR_BAD_SELECTION, r, bad);
+    *fine = 0;
+  }
 }
 
 __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(CompactArgs a) {
@@ -110,12 +119,15 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(CompactAr
   if (ok)
     for (long long i = at; i < count; i += threads) {
       const int32_t id = a.free_list[i];
-      if (id < 0 || id >= a.num_pages || (atomicOr(a.bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1))
+      if (id < 0 || id >= a.num_pages || (atomicOr(a.bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1)) {
         raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, (int)i);
+        ok = false;
+      }
     }
   __threadfence();
   cluster.sync();
   ok = !__syncthreads_or(!ok || load_err(a.err) != 0);
+  if (tid == 0) a.fine[rank] = ok;         // (before the barriers that what is found below comes after)
   // a range of words per CTA, of it one per thread
   const int per_cta = (a.words + ctas - 1) / ctas;
   const int c0 = min(a.words, rank * per_cta), c1 = min(a.words, c0 + per_cta);
@@ -141,7 +153,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(CompactAr
   // what the requests hold lies in the pool and is in use
   if (ok)
     for (int r = at >> 5; r < a.R; r += threads >> 5)
-      check_held(a, r, [&](int id) { return __ldcg(a.bits + (id >> 5)) >> (id & 31) & 1; });
+      check_held(a, r, a.fine + rank, [&](int id) { return __ldcg(a.bits + (id >> 5)) >> (id & 31) & 1; });
   cluster.sync();                          // (no CTA ends while another may write its s_sum)
 }
 
@@ -157,7 +169,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_small_kernel(Com
   const int count = *a.count;
   const bool fits = count >= 0 && count <= a.num_pages;
   if (!fits && !latched && tid == 0 && blockIdx.x == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, -1);
-  if (__syncthreads_or(latched || !fits)) return;
+  if (__syncthreads_or(latched || !fits)) {
+    if (tid == 0) a.fine[blockIdx.x] = 0;
+    return;
+  }
+  if (tid == 0) a.fine[blockIdx.x] = 1;    // (before the barrier that what is found below comes after)
   griddep_launch();
   int bad = -1;
   for (int i = tid; i < count; i += kCompactThreads) {
@@ -165,7 +181,10 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_small_kernel(Com
     if (id < 0 || id >= a.num_pages || (atomicOr(s_bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1)) bad = i;
   }
   if (bad >= 0 && blockIdx.x == 0) raise_error(a.err, AVSG_ERR_BAD_SELECTION, -1, bad);
-  if (__syncthreads_or(bad >= 0)) return;
+  if (__syncthreads_or(bad >= 0)) {
+    if (tid == 0) a.fine[blockIdx.x] = 0;
+    return;
+  }
   const int live = a.num_pages - count;
   if (blockIdx.x == 0) {
     const int w0 = min(a.words, tid * kEach), w1 = min(a.words, w0 + kEach);
@@ -183,7 +202,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_small_kernel(Com
   }
   const int warps = gridDim.x * (kCompactThreads / 32);
   for (int r = blockIdx.x * (kCompactThreads / 32) + (tid >> 5); r < a.R; r += warps)
-    check_held(a, r, [&](int id) { return s_bits[id >> 5] >> (id & 31) & 1; });
+    check_held(a, r, a.fine + blockIdx.x, [&](int id) { return s_bits[id >> 5] >> (id & 31) & 1; });
 }
 
 struct PackArgs {
@@ -203,8 +222,8 @@ struct PackArgs {
 __global__ void __launch_bounds__(kPackThreads) compact_move_kernel(PackArgs a) {
   const CompactArgs& c = a.c;
   griddep_wait();
-  if (load_err(c.err) != 0) return;
   const int lane = threadIdx.x & 31;
+  if (__any_sync(0xffffffffu, lane < c.ctas && c.fine[lane] == 0)) return;
   const long long threads = (long long)gridDim.x * kPackThreads;
   const long long at = (long long)blockIdx.x * kPackThreads + threadIdx.x;
   const int live = c.live[0], low = c.live[1], count = c.num_pages - live;
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(kPackThreads) compact_move_kernel(PackArgs a) 
 }
 
 struct CompactWork {
-  size_t bits, before, holes, movers, live, bytes;
+  size_t bits, before, holes, movers, live, fine, bytes;
   int words;
 };
 CompactWork compact_layout(const avsg_pages* p) {
@@ -267,7 +286,9 @@ CompactWork compact_layout(const avsg_pages* p) {
   w.holes = w.before + up((size_t)w.words * 4);
   w.movers = w.holes + up(((size_t)p->num_pages / 2 + 1) * 4);
   w.live = w.movers + up(((size_t)p->num_pages / 2 + 1) * 4);
+  w.fine = w.live + 128;
   w.bytes = w.live + 256;
+  static_assert(kMostPlanCtas * sizeof(int32_t) <= 128 && kCompactCluster <= kMostPlanCtas, "see fine");
   return w;
 }
 
@@ -316,6 +337,7 @@ extern "C" int avsg_page_compact(const avsg_pages* p, const int32_t* d_shares, i
   c.holes = reinterpret_cast<int32_t*>(work + w.holes);
   c.movers = reinterpret_cast<int32_t*>(work + w.movers);
   c.live = reinterpret_cast<int32_t*>(work + w.live);
+  c.fine = reinterpret_cast<int32_t*>(work + w.fine);
   c.err = reinterpret_cast<DevErr*>(p->d_error);
   a.num_layers = p->num_layers;
   a.page_chunks = (long long)p->num_kv_heads * p->page_tokens * p->head_dim / 8;
@@ -329,14 +351,15 @@ extern "C" int avsg_page_compact(const avsg_pages* p, const int32_t* d_shares, i
   a.map = d_map;
   // a warp for every 32 held entries, a thread for every word of the bitmap
   const int64_t most = (int64_t)c.R * c.max_pages > c.num_pages ? (int64_t)c.R * c.max_pages : c.num_pages;
-  int ctas = 1;
-  while (ctas < kCompactCluster && ctas * kCompactThreads < most) ctas *= 2;
-  // (a small pool: as many CTAs as the requests have warps, at most 32; each reads the whole stack)
+  const bool small = c.num_pages <= kSmallPool;
+  c.ctas = 1;
+  while (c.ctas < kCompactCluster && c.ctas * kCompactThreads < most) c.ctas *= 2;
+  // (a small pool: as many CTAs as the requests have warps; each reads the whole stack)
   const int rows = (c.R + kCompactThreads / 32 - 1) / (kCompactThreads / 32);
+  if (small) c.ctas = rows < kMostPlanCtas ? rows : kMostPlanCtas;
   cudaError_t e =
-      c.num_pages <= kSmallPool
-          ? launch_pdl(compact_plan_small_kernel, dim3(rows < 32 ? rows : 32), dim3(kCompactThreads), 0, st, c)
-          : launch_pdl_cluster(ctas, compact_plan_kernel, dim3(ctas), dim3(kCompactThreads), 0, st, c);
+      small ? launch_pdl(compact_plan_small_kernel, dim3(c.ctas), dim3(kCompactThreads), 0, st, c)
+            : launch_pdl_cluster(c.ctas, compact_plan_kernel, dim3(c.ctas), dim3(kCompactThreads), 0, st, c);
   if (e == cudaSuccess) {
     const int64_t half = (c.num_pages + 1) / 2;            // no more pages move
     const int64_t warps = half * a.num_layers * 2 * ((a.page_chunks + kPackPiece - 1) / kPackPiece);

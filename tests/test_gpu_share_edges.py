@@ -95,3 +95,53 @@ def test_a_fork_that_the_check_refuses_with_a_workspace_of_a_good_one():
         if what in ("page", "free page"):
             c.tables.copy_(dev(p.tables)), c.free.copy_(dev(p.free))
     assert host(c.lens).tolist() == [37, 37, 20, 20]
+
+
+@pytest.mark.parametrize("lens,page,spare", [(list(range(1, 400, 3)), 8, 3000), (list(range(2000)), 16, 90000),
+                                             ([300, 255, 1, 90] * 300, 4, 700)])
+def test_a_compaction_is_whole_beside_errors_of_another_cache(lens, page, spare):
+    """A pool whose lists are one cluster's work among them, and requests for many CTAs of the other kernel."""
+    p = Pool(lens, page, seed=2, spare=spare)
+    page_map, work = torch.zeros_like(p.cache.free), p.cache.compact_workspace()
+    work.fill_(255)                                        # any contents
+    b = Beside(p)
+    b.state.append(page_map)
+    b.before.append(page_map.clone())
+    p.tables, p.free, p.shares, where = want_of.compact(p.lens, p.tables, p.free, p.count, p.shares, page, p.pages)
+    b.run(lambda: p.cache.compact(page_map, work), on_device(p) + [dev(where)], rounds=60)
+
+
+@pytest.mark.parametrize("requests,spare", [(3, 40), (1100, 40), (3, 70000), (1100, 70000)])
+def test_a_compaction_that_is_refused_with_a_workspace_of_a_good_one(requests, spare):
+    """What the checks of the call before found is not taken for this one's, of the last request too."""
+    p = Pool([9 + i % 30 for i in range(requests)], 8, spare=spare)
+    c, work = p.cache, p.cache.compact_workspace()
+    page_map = torch.zeros_like(c.free)
+    p.tables, p.free, p.shares, _ = want_of.compact(p.lens, p.tables, p.free, p.count, p.shares, 8, p.pages)
+    c.compact(page_map, work)
+    p.check()
+    at = p.count // 2                                      # a page in use high up, so that something would move
+    high, low = int(p.free[0]), int(p.tables[0, 0])
+    p.free[0], p.tables[0, 0] = low, high
+    for a in p.pages:
+        a[:, high] = a[:, low]
+    for what in ("page", "free page", "twice", "length"):
+        for t, a in zip((c.lens, c.tables, c.free, c.k, c.v), (p.lens, p.tables, p.free, *p.pages)):
+            t.copy_(torch.from_numpy(a).cuda().view(t.dtype) if t.dim() == 5 else dev(a))
+        if what == "page":
+            c.tables[requests - 1, 0] = -1
+        elif what == "free page":
+            c.tables[requests - 1, 0] = c.free[at]
+        elif what == "twice":
+            c.free[at] = c.free[1]
+        elif what == "length":
+            c.lens[requests - 1] = -1
+        state = [c.lens, c.tables, c.free, c.free_count, c.shares, page_map, p.k, p.v]
+        before = [t.clone() for t in state]
+        c.compact(page_map, work)
+        assert c.error()[0] == -4
+        assert all(torch.equal(t, b) for t, b in zip(state, before)), what
+        c.compact(page_map, work)                          # latched: nothing happens
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, b) for t, b in zip(state, before)), what
+        c.clear_error()
