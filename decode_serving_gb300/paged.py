@@ -352,7 +352,9 @@ class PagedCache:
         """Moves the pages in use to the front of the pool, whole and in all
         layers.  page_map [num_pages] int32 receives each page's new id, -1
         for a free one; tables, free pages and shares change in place unless
-        others are given for them."""
+        others are given for them.  Between steps, when every token is
+        committed: pages of planned tokens move too, but neither their table
+        entries nor the step's slots follow."""
         tables = self.tables if tables_out is None else tables_out
         free = self.free if free_out is None else free_out
         shares = self.shares if shares_out is None else shares_out

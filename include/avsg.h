@@ -365,6 +365,9 @@ int avsg_read_rows(const void* src, int64_t num_rows, int64_t row_bytes, const i
  * avsg_page_fork shares it; a cache with shared pages is kept by
  * avsg_tree_keep_shared, as avsg_tree_keep would give a shared page back twice.  Calls on several streams are independent
  * as long as nothing that one of them writes is used by another at a time.
+ * That holds for a d_error of several caches too: an error that one latches
+ * may stop another's call part of the way, but for avsg_page_fork and
+ * avsg_page_compact, which happen as a whole or not at all.
  */
 #define AVSG_BF16 0
 #define AVSG_F16 1
@@ -587,7 +590,11 @@ int avsg_tree_keep_shared(const avsg_pages* p, const int32_t* d_shares, const in
  * Pages in use are those that are not on the stack, whoever holds them.  With
  * n of them, the i-th of those at or above n (by id) moves to the i-th free
  * id below n, whole and in all layers; pages above n can then be given to something
- * else, or the pool cut off there.
+ * else, or the pool cut off there.  Compact between steps, as for the fork:
+ * a page that avsg_page_plan took for tokens that are not committed yet is in
+ * use and moves, but its entry behind the committed tokens and the step's
+ * slots keep the old id, under which another page may lie from then on (a
+ * caller who holds pages of its own finds them by d_map).
  *   d_shares, d_shares_out : as above, both or neither NULL.
  *   d_tables_out : [R][max_pages], receives the tables (entries behind a
  *                  request's pages as they were).

@@ -145,3 +145,27 @@ def test_a_compaction_that_is_refused_with_a_workspace_of_a_good_one(requests, s
         torch.cuda.synchronize()
         assert all(torch.equal(t, b) for t, b in zip(state, before)), what
         c.clear_error()
+
+
+@pytest.mark.parametrize("spare", [60, 70000])
+def test_what_a_compaction_does_with_pages_of_planned_tokens(spare):
+    """They are in use and move, whole; what names them (entries behind the committed tokens, slots) does not follow."""
+    p = Pool([20, 37], 8, spare=spare, layers=2, room=4)
+    c = p.cache
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    first, slots, pos, page_map = i32(3), i32(16), i32(16), torch.zeros_like(c.free)
+    c.plan(dev(np.array([9, 7])), first, slots, pos)
+    planned, was = host(c.tables), host(slots)
+    pages = [c.k.clone(), c.v.clone()]
+    c.compact(page_map, c.compact_workspace())
+    assert c.error()[0] == 0
+    where, now = host(page_map), host(c.tables)
+    for r, (length, new) in enumerate(((20, 9), (37, 7))):
+        held, need = -(-length // 8), -(-(length + new) // 8)
+        assert need > held
+        assert (now[r, :held] == where[planned[r, :held]]).all()
+        assert (now[r, held:] == planned[r, held:]).all()
+        for x in planned[r, :need]:                        # (where the map says, whole)
+            assert 0 <= where[x] < c.pages - int(c.free_count)
+            assert all(torch.equal(new[:, int(where[x])], old[:, int(x)]) for new, old in zip((c.k, c.v), pages))
+    assert (host(slots) == was).all()
