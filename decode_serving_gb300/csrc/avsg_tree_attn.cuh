@@ -340,7 +340,8 @@ struct Piece {
 };
 
 // What part `part` of an attention over prefixes costs in all of request (or group) r's units of one kv-head.
-__device__ __forceinline__ float part_cost(const TreeArgs& a, int part, int r) {
+// (This and the next one run on the host too, for arrays there: so they are tested.)
+__host__ __device__ __forceinline__ float part_cost(const TreeArgs& a, int part, int r) {
   const TreeArgs::Cost& c = a.cost[part];
   const int common = max(a.shared[r], 0);
   int n, keys;
@@ -360,12 +361,17 @@ __device__ __forceinline__ float part_cost(const TreeArgs& a, int part, int r) {
 }
 
 // SMs of part 0: the fewest with which it ends no later than part 1 on the others, `lead` before it.
-__device__ __forceinline__ int first_sms(const TreeArgs& a, float c0, float c1) {
+__host__ __device__ __forceinline__ int first_sms(const TreeArgs& a, float c0, float c1) {
   if (c0 == 0.f) return 0;
   if (c1 == 0.f) return a.sms;
   // the positive root k of  c0 / k + lead = c1 / (sms - k)  (short calls need no room for the lead)
   const float n = (float)a.sms, lead = fminf((float)a.lead, 0.5f * (c0 + c1) / n), b = c0 + c1 - lead * n;
-  const float k = __fdividef(2.f * c0 * n, b + sqrtf(b * b + 4.f * lead * c0 * n));
+  const float up = 2.f * c0 * n, down = b + sqrtf(b * b + 4.f * lead * c0 * n);
+#ifdef __CUDA_ARCH__
+  const float k = __fdividef(up, down);
+#else
+  const float k = up / down;
+#endif
   return min(max((int)ceilf(k), 1), a.sms - 1);
 }
 
