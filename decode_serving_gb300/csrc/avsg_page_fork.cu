@@ -28,8 +28,8 @@
 // the last pages) nothing is counted.  Nothing is written before every check has passed, but the check
 // of the stack's room, which only wrong shares fail.  Sums and maxima of whole
 // numbers decide everything, so that the result does not depend on an order.
-// Measured: 8 samples of a prompt of 1000 tokens, one layer: 11.5 us; 256 beams
-// through 16 layers, 64 MB read and written: 22.5 us (29.5 with the copies
+// Measured: 8 samples of a prompt of 1000 tokens, one layer: 11.6 us; 256 beams
+// through 16 layers, 64 MB read and written: 22.3 us (29.5 with the copies
 // behind the tables); 96 samples of six prompts of up to 32768 tokens: 23 us
 // (46 when every row of a changed count was walked).
 #include <cooperative_groups.h>

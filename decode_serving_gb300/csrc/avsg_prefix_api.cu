@@ -10,7 +10,8 @@
 //           avsg_prefix_find, as rows, its prefix as keys;
 //   part 1  (request, kv-head, m-tile): a request's new tokens, its keys
 //           behind the prefix (all of them where it has none, and then the output itself);
-// and a kernel that joins a row's pieces of both.  The parts are launches of
+// and a kernel that joins a row's pieces of both (and looks every token with a
+// prefix up in the list).  The parts are launches of
 // their own: a group has many rows and a long prefix (tcgen05's work), a request often few rows
 // and few keys of its own (mma.sync's).  They run side by side: part 1 does
 // not wait for part 0 before it begins, only before it ends, so that what follows it follows
@@ -23,9 +24,10 @@
 // 500 tokens of their own, one new token each, 8 kv-heads of 4: 68 us (the tree
 // attention, for which every request reads the prefix, 1030); one part after the other 88.  Of the 68: 4 us until
 // both parts have found their shares, 50 for the parts, 2 between kernels, 5 for the join.
-// 69 requests with trees of up to 16 tokens in four groups of up to 32768: 298 to 305 us.
-// Where no request has a group it costs 7 to 19 us more than the tree attention (64 requests alone,
-// one new token each: 58 and 44 us at 500 tokens, 120 and 100 at 2000, 334 and 327 at 8000): the empty
+// 69 requests with trees of up to 16 tokens in four groups of up to 32768: 294 to 304 us.
+// Where no request has a group it costs 8 to 28 us more than the tree attention (64 requests alone,
+// one new token each: 42 and 32 us at 100 tokens, 59 and 44 at 500, 121 and 101 at 2000, 206 and 178 at
+// 4000, 335 and 327 at 8000): the empty
 // part and the join, and part 1's kernel alone takes 13% more at 2000 tokens, of which twice the
 // stalls for instructions are seen, but neither its registers nor the order of its branches is the cause.
 #include "avsg_tree_plan.cuh"
@@ -253,8 +255,8 @@ cudaError_t launch_join(const JoinArgs& a, int D, int sms, int dev, cudaStream_t
 }
 
 // What a CTA takes for a unit's beginning and end, a tile, and on tcgen05 a tile of up to 128 rows,
-// in hundredths of a microsecond: least squares over the CTAs of several calls (GB300; wm 2 between its
-// neighbours).  Tiles are 128 keys on tcgen05, 64 with mma.sync and for heads of 256.
+// in hundredths of a microsecond: least squares over the CTAs of calls with a long document or draft trees,
+// heads of each width, on either kernel (GB300; wm 2 between its neighbours).  Tiles are 128 keys on tcgen05, 64 with mma.sync and for heads of 256.
 struct CtaCost {
   int begin, tile, small;
 };

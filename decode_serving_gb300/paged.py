@@ -422,8 +422,9 @@ class PagedCache:
                         softcap=0.0, window=0, slopes=None, stream=None):
         """``attend`` with every group's prefix read and multiplied once for
         all of its members; prefixes from ``find_prefixes``, for the same
-        tables, lengths and first.  A step without groups is 7 to 19 us faster
-        by ``attend``."""
+        tables, lengths and first.  A step without groups is 8 to 28 us faster
+        by ``attend`` (64 requests: 42 and 32 us at 100 tokens, 206 and 178 at
+        4000, 335 and 327 at 8000)."""
         args = self._tree(q, first, out, max_new, work, mask, lse, layer, scale, softcap, window, slopes)
         rc = self._calls["avsg_prefix_attention"](self._at, args, self._prefixes(prefixes), self._stream(stream))
         if rc:
